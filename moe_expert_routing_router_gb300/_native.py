@@ -58,6 +58,23 @@ SIGNATURES = {
     "moe_abi_version": (_i32, []),
 }
 
+# Every symbol declared in include/moe_experts.h.
+EXPERT_SIGNATURES = {
+    "moe_experts_abi_version": (_i32, []),
+    "moe_route_fwd": (_i32, [_p, _i32, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _p, _i32, _f32, _f32, _p,
+                             _p, _p, _p, _p]),
+    "moe_route_bwd": (_i32, [_p, _i32, _i64, _i32, _i32, _i32, _i32, _f32, _p, _p, _p, _p]),
+    "moe_quantize_rows": (_i32, [_p, _i32, _i64, _i64, _i32, _p, _i32, _p, _p, _p]),
+    "moe_quantize_cols_width": (_i64, [_i64, _i32]),
+    "moe_quantize_cols": (_i32, [_p, _i32, _i64, _i64, _i32, _i32, _p, _p, _p, _i32, _p, _p, _p]),
+    "moe_quantize_weights": (_i32, [_p, _i32, _i32, _i32, _i32, _p, _p, _p, _p, _p]),
+    "moe_expert_matmul": (_i32, [_p, _p, _i64, _i32, _p, _p, _i32, _i32, _p, _p, _i32, _p, _p]),
+    "moe_expert_wgrad": (_i32, [_p, _p, _p, _p, _i64, _i32, _i32, _i32, _p, _p, _p]),
+    "moe_expert_device_status": (_i32, [_p, C.POINTER(_i32)]),
+    "moe_expert_combine": (_i32, [_p, _i32, _i64, _i32, _i64, _i32, _i32, _p, _p, _p, _p, _p, _p]),
+    "moe_expert_combine_bwd": (_i32, [_p, _p, _i32, _i64, _i32, _i64, _i32, _i32, _p, _p, _p, _p, _p, _p, _p]),
+}
+
 _lock = threading.Lock()
 _lib: C.CDLL | None = None
 
@@ -76,7 +93,7 @@ def lib() -> C.CDLL:
             if not LIB_PATH.exists():
                 raise RuntimeError(f"{LIB_PATH} is not built; run python -m moe_expert_routing_router_gb300.build")
             handle = C.CDLL(str(LIB_PATH))
-            for name, (res, args) in SIGNATURES.items():
+            for name, (res, args) in {**SIGNATURES, **EXPERT_SIGNATURES}.items():
                 fn = getattr(handle, name)
                 fn.restype = res
                 fn.argtypes = args

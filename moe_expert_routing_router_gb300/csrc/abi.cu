@@ -15,6 +15,7 @@
 #include <string>
 #include <unordered_map>
 
+#include "abi_common.h"
 #include "moe_router.h"
 #include "router_ext.cuh"
 #include "router_kernels.cuh"
@@ -1114,3 +1115,22 @@ extern "C" moe_status moe_router_step_static(const void* logits, moe_dtype dt, i
   return moe_router_step(logits, dt, T, E, k, alpha, renorm, n_ranks, capacity_factor, grad_scale, idx, gate, counts,
                          f, P, scalars, rank_load, perm, slot, offsets, kept, n_dropped, dlogits, ws, need, stream);
 }
+
+// The parts of this file that the other entry-point files use.
+namespace moe {
+
+moe_status abi_fail(moe_status s, const char* message) { return fail(s, "%s", message); }
+
+moe_status abi_sms(int* sms) {
+  DeviceInfo d;
+  int dev = 0;
+  const moe_status s = device_info(&d, &dev);
+  *sms = d.sms;
+  return s;
+}
+
+uint64_t abi_wait_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
+
+unsigned abi_barrier_extra() { return g_barrier_extra.load(std::memory_order_relaxed); }
+
+}  // namespace moe

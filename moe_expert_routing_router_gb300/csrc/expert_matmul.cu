@@ -1,0 +1,505 @@
+// The experts' 8-bit matrix products on the fifth-generation tensor cores.
+//
+// Operands are e4m3 with a fp32 scale for each block of 128 along the
+// contraction.  A block's product is formed by four tcgen05.mma (K = 32 each)
+// in tensor memory, from zero; the epilogue warps read it back, multiply by the
+// block's two scales and add it in fp32 registers, which hold the tile's sum
+// over all blocks.  The scales may be any fp32 numbers, and no sum is kept in
+// fewer than 32 bits.
+//
+// One persistent CTA per SM, 20 warps: a TMA producer (one thread), an MMA
+// issuer (one thread), two spare warps, and 16 epilogue warps of 32 rows by a
+// quarter of the tile's columns.  Shared memory is a ring of operand stages
+// (one block of 128 of both operands, 128-byte swizzled); tensor memory is a
+// ring of block products, so that the tensor core forms block b + 1 while the
+// epilogue adds block b, and runs ahead into the next tile while a tile is
+// stored.  Every wait is bounded: when one runs out, the CTA records the
+// pipeline's error bit, drains its copies and returns.
+#include "device_common.cuh"
+#include "expert_matmul.h"
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+namespace moe {
+namespace {
+
+constexpr int kBM = 128;                      // rows of a tile
+constexpr int kBK = 128;                      // block along the contraction: bytes of e4m3, and one scale
+constexpr int kBoxA = 32, kBoxB = 64;         // rows of one copy: a ragged tile copies only the boxes that it needs
+constexpr int kEpiWarps = 16, kFirstEpi = 4;
+constexpr int kMmThreads = (kFirstEpi + kEpiWarps) * kWarp;
+constexpr int kTmemCols = 512;
+constexpr int kMaxE = 1024;
+constexpr int kGroupM = 16;                   // row tiles of an expert that are taken before the next column tile
+constexpr unsigned kFull = 0xffffffffu;
+
+// Error bits of the device's calls: they carry no other state from call to call,
+// so calls on any streams, and captured ones, share the word.
+__device__ int g_mm_errors;
+
+// ---- tcgen05 / TMA primitives ------------------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(slot)), "r"(kTmemCols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(kTmemCols) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+      :: "r"(smem_addr(dst)), "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y) : "memory");
+}
+
+// Shared-memory matrix descriptor of a K-major operand in rows of 128 bytes,
+// 128-byte swizzle: groups of 8 rows lie 1024 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(const void* p) {
+  return uint64_t((smem_addr(p) >> 4) & 0x3fffu) | uint64_t(1) << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 |
+         uint64_t(2) << 61;
+}
+
+// 16 columns of the warp's 32 rows; the values are there when it returns (the
+// wait is in the same statement, so no use of them can be moved before it).
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// ---- the kernel ----------------------------------------------------------------
+template <int BN>
+struct Tile {
+  static constexpr int kStageBytes = (kBM + BN) * kBK;
+  static constexpr int kStages = 196608 / kStageBytes;         // 192 KB of operands
+  static constexpr int kBufs = kTmemCols / BN;                 // block products in tensor memory
+  static constexpr int kCols = BN / 4;                         // columns of one epilogue warp
+};
+
+struct alignas(16) Shared {
+  uint64_t full[8], empty[8], tfull[8], tempty[8], drain;
+  uint32_t tmem;
+  int abort;
+  int first[kMaxE + 1];                                        // tiles before expert e
+  int block[kMaxE + 1];                                        // weight gradient: column blocks before expert e
+  alignas(16) float bscale[kEpiWarps][2][64];                  // weight gradient: a block's column scales, per warp
+};
+
+// Bounded wait that every role uses: false once it, or another role's, ran out.
+__device__ __forceinline__ bool mm_wait(Shared& sh, const MatmulParams& p, uint64_t* bar, uint32_t parity) {
+  if (mbar_test(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (!mbar_test_suspend(bar, parity, 20000u)) {
+    if (*reinterpret_cast<volatile int*>(&sh.abort) != 0) return false;
+    if (global_ns() - t0 > p.timeout_ns) {
+      *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+      atomicOr(&g_mm_errors, kErrPipelineTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
+// The rows of expert e: their place and number, whatever the arrays hold, inside [0, M).
+__device__ __forceinline__ void expert_rows(const MatmulParams& p, int e, int64_t* start, int64_t* n) {
+  if (p.offsets == nullptr) {
+    *start = 0;
+    *n = p.M;
+    return;
+  }
+  const int64_t lo = min(max(int64_t(p.offsets[e]), int64_t(0)), p.M);
+  const int64_t hi = min(max(int64_t(p.offsets[e + 1]), lo), p.M);
+  *start = lo;
+  *n = p.kept != nullptr ? min(hi - lo, max(int64_t(p.kept[e]), int64_t(0))) : hi - lo;
+}
+
+// A tile of the persistent loop, walked in ascending order by every role.
+struct Walk {
+  int e = 0;
+  int row0 = 0, rows = 0;         // rows of a: the first one and how many are the tile's
+  int col0 = 0, cols = 0;         // columns of out within the expert
+  int r0 = 0;                     // the tile's first row within the expert's out
+  int block0 = 0, blocks = 0;     // blocks along the contraction
+
+  template <int BN, bool WGRAD>
+  __device__ __forceinline__ void at(const MatmulParams& p, const Shared& sh, int tile) {
+    while (sh.first[e + 1] <= tile) ++e;
+    const int i = tile - sh.first[e];
+    const int ct = (p.C + BN - 1) / BN;
+    const int rt = (sh.first[e + 1] - sh.first[e]) / ct;
+    // kGroupM row tiles by all column tiles at a time, rows fastest: the CTAs at
+    // work share both operands' tiles in L2.
+    const int group = i / (kGroupM * ct), in = i - group * kGroupM * ct;
+    const int gm = min(kGroupM, rt - group * kGroupM);
+    const int m = group * kGroupM + in % gm;
+    col0 = in / gm * BN;
+    cols = min(BN, p.C - col0);
+    r0 = m * kBM;
+    if constexpr (WGRAD) {
+      row0 = r0;
+      rows = min(kBM, p.R - r0);
+      block0 = sh.block[e];
+      blocks = sh.block[e + 1] - block0;
+    } else {
+      int64_t start, n;
+      expert_rows(p, e, &start, &n);
+      row0 = int(start) + r0;
+      rows = int(min(n - r0, int64_t(kBM)));
+      block0 = 0;
+      blocks = (p.K + kBK - 1) / kBK;
+    }
+  }
+};
+
+template <int BN, bool WGRAD, bool BF16>
+__global__ void __launch_bounds__(kMmThreads, 1)
+expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
+  using TL = Tile<BN>;
+  extern __shared__ uint8_t s_dyn[];
+  __shared__ Shared sh;
+  uint8_t* ring = s_dyn + (1024 - smem_addr(s_dyn) % 1024) % 1024;
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < TL::kStages; ++i) {
+        mbar_init(&sh.full[i], 1 + p.extra);
+        mbar_init(&sh.empty[i], 1);
+      }
+      for (int i = 0; i < TL::kBufs; ++i) {
+        mbar_init(&sh.tfull[i], 1);
+        mbar_init(&sh.tempty[i], kEpiWarps);
+      }
+      mbar_init(&sh.drain, 1);
+      mbar_fence_init();
+      // an error that the host has not read yet: write nothing
+      sh.abort = *static_cast<volatile int*>(&g_mm_errors) != 0;
+    }
+  } else if (warp == 1) {
+    tmem_alloc(&sh.tmem);
+    tc_fence_before();
+  } else if (warp == 2) {                                        // tiles and blocks before each expert
+    const int ct = (p.C + BN - 1) / BN;
+    int tiles = 0, blocks = 0;
+    for (int e0 = 0; e0 < p.E; e0 += kWarp) {
+      int t = 0, b = 0;
+      if (e0 + lane < p.E) {
+        if constexpr (WGRAD) {
+          t = (p.R + kBM - 1) / kBM * ct;
+          b = int((max(int64_t(p.kept[e0 + lane]), int64_t(0)) + kBK - 1) / kBK);
+        } else {
+          int64_t start, n;
+          expert_rows(p, e0 + lane, &start, &n);
+          t = int((n + kBM - 1) / kBM) * ct;
+        }
+      }
+      int ti = t, bi = b;
+#pragma unroll
+      for (int off = 1; off < kWarp; off <<= 1) {
+        const int to = __shfl_up_sync(kFull, ti, off), bo = __shfl_up_sync(kFull, bi, off);
+        if (lane >= off) {
+          ti += to;
+          bi += bo;
+        }
+      }
+      if (e0 + lane < p.E) {
+        sh.first[e0 + lane] = tiles + ti - t;
+        if constexpr (WGRAD) sh.block[e0 + lane] = int(min(int64_t(blocks) + bi - b, p.blocks));   // inside the operands
+      }
+      tiles += __shfl_sync(kFull, ti, kWarp - 1);
+      blocks = int(min(int64_t(blocks) + __shfl_sync(kFull, bi, kWarp - 1), p.blocks));
+    }
+    if (lane == 0) {
+      sh.first[p.E] = tiles;
+      sh.block[p.E] = blocks;
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int n_tiles = sh.abort != 0 ? 0 : sh.first[p.E];
+  __syncthreads();                                               // every thread has seen abort before a role sets it
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- producer: one stage per block ----
+      int s = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      Walk w;
+      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
+        w.at<BN, WGRAD>(p, sh, tile);
+        const int na = (w.rows + kBoxA - 1) / kBoxA, nb = (w.cols + kBoxB - 1) / kBoxB;
+        const int b_row = WGRAD ? w.col0 : w.e * p.C + w.col0;
+        for (int b = 0; b < w.blocks; ++b) {
+          if (!(ok = mm_wait(sh, p, &sh.empty[s], phase ^ 1u))) break;
+          uint8_t* sa = ring + s * TL::kStageBytes;
+          uint8_t* sb = sa + kBM * kBK;
+          mbar_arrive_expect_tx(&sh.full[s], uint32_t(na * kBoxA + nb * kBoxB) * kBK);
+          const int x = (w.block0 + b) * kBK;
+          for (int i = 0; i < na; ++i) tma_2d(sa + i * kBoxA * kBK, &map_a, x, w.row0 + i * kBoxA, &sh.full[s]);
+          for (int i = 0; i < nb; ++i) tma_2d(sb + i * kBoxB * kBK, &map_b, x, b_row + i * kBoxB, &sh.full[s]);
+          ++issued;
+          if (++s == TL::kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {                                                 // copies in flight land before shared memory goes
+        for (int i = 0; i < TL::kStages && i < issued; ++i) {
+          const int back = issued - 1 - i;
+          mbar_wait(&sh.full[back % TL::kStages], uint32_t(back / TL::kStages) & 1u, p.timeout_ns);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---- MMA issuer ----
+      // D fp32, A and B e4m3, both K-major, N = BN, M = 128
+      constexpr uint32_t idesc = (1u << 4) | uint32_t(BN / 8) << 17 | uint32_t(kBM / 16) << 24;
+      int s = 0, t = 0;
+      uint32_t phase = 0, tphase = 0;
+      bool ok = true;
+      Walk w;
+      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
+        w.at<BN, WGRAD>(p, sh, tile);
+        for (int b = 0; b < w.blocks; ++b) {
+          if (!(ok = mm_wait(sh, p, &sh.tempty[t], tphase ^ 1u) && mm_wait(sh, p, &sh.full[s], phase))) break;
+          tc_fence_after();
+          const uint64_t da = smem_desc(ring + s * TL::kStageBytes), db = smem_desc(ring + s * TL::kStageBytes + kBM * kBK);
+#pragma unroll
+          for (int k = 0; k < kBK / 32; ++k)                     // 32 bytes along the row: 2 units of 16
+            tc_mma_f8(tmem + t * BN, da + k * 2, db + k * 2, idesc, k > 0);
+          tc_commit(&sh.empty[s]);
+          tc_commit(&sh.tfull[t]);
+          if (++s == TL::kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+          if (++t == TL::kBufs) {
+            t = 0;
+            tphase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {                                                 // products in flight end before tensor memory goes
+        tc_commit(&sh.drain);
+        mbar_wait(&sh.drain, 0, p.timeout_ns);
+      }
+    }
+  } else if (warp >= kFirstEpi) {
+    // ---- epilogue: rows 32 * quad + lane, kCols columns ----
+    constexpr int CW = TL::kCols;
+    const int quad = warp % 4, cg = (warp - kFirstEpi) / 4, row = quad * 32 + lane;
+    float(*s_bs)[64] = sh.bscale[warp - kFirstEpi];
+    const int kblocks = (p.K + kBK - 1) / kBK, cblocks = (p.C + kBK - 1) / kBK;
+    int t = 0;
+    uint32_t tphase = 0;
+    bool ok = true;
+    Walk w;
+    for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
+      w.at<BN, WGRAD>(p, sh, tile);
+      const int c0 = w.col0 + cg * CW;                           // the warp's first column of out
+      const bool busy = quad * 32 < w.rows && c0 < p.C;          // warp-uniform: whether it has anything to add
+      const bool live = row < w.rows;
+      float2 acc[CW / 2];
+#pragma unroll
+      for (int i = 0; i < CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      const float* pa = nullptr;
+      const float* pb = nullptr;
+      int64_t step_a = 0, step_b = 0;
+      if constexpr (WGRAD) {
+        pa = p.a_scale + int64_t(w.block0) * p.R + w.r0 + row;
+        pb = p.b_scale + int64_t(w.block0) * p.C + c0 + lane;
+        step_a = p.R;
+        step_b = p.C;
+      } else {
+        pa = p.a_scale + w.row0 + row;
+        pb = p.b_scale + (int64_t(w.e) * cblocks + c0 / kBK) * kblocks;
+        step_a = p.M;
+        step_b = 1;
+      }
+      const bool lo_col = c0 + lane < p.C && lane < CW, hi_col = CW > 32 && c0 + 32 + lane < p.C;
+      float sa = 0.f, sb = 0.f, sb_hi = 0.f;
+      const auto fetch = [&]() {
+        if (busy) {
+          sa = live ? *pa : 0.f;
+          if constexpr (WGRAD) {
+            sb = lo_col ? *pb : 0.f;
+            sb_hi = hi_col ? pb[32] : 0.f;
+          } else {
+            sb = *pb;
+          }
+        }
+        pa += step_a;
+        pb += step_b;
+      };
+      if (w.blocks > 0) fetch();
+      for (int b = 0; b < w.blocks; ++b) {
+        const float ra = sa, rb = sb;
+        if constexpr (WGRAD) {
+          if (lane < CW) s_bs[b & 1][lane] = sb;
+          if constexpr (CW > 32) s_bs[b & 1][32 + lane] = sb_hi;
+          __syncwarp();
+        }
+        if (b + 1 < w.blocks) fetch();
+        ok = __all_sync(kFull, mm_wait(sh, p, &sh.tfull[t], tphase));   // one answer for the warp
+        if (!ok) break;
+        tc_fence_after();
+        if (busy) {
+          const uint32_t addr = tmem + t * BN + cg * CW + (uint32_t(quad * 32) << 16);
+          const float2 s2 = WGRAD ? make_float2(ra, ra) : make_float2(ra * rb, ra * rb);
+#pragma unroll
+          for (int c = 0; c < CW; c += 16) {
+            float v[16];
+            tmem_ld16(addr + c, v);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              float2 x = make_float2(v[i], v[i + 1]), y = make_float2(v[i + 2], v[i + 3]);
+              if constexpr (WGRAD) {
+                const float4 q = *reinterpret_cast<const float4*>(&s_bs[b & 1][c + i]);
+                acc[(c + i) / 2] = fma2(mul2(x, s2), make_float2(q.x, q.y), acc[(c + i) / 2]);
+                acc[(c + i) / 2 + 1] = fma2(mul2(y, s2), make_float2(q.z, q.w), acc[(c + i) / 2 + 1]);
+              } else {
+                acc[(c + i) / 2] = fma2(x, s2, acc[(c + i) / 2]);
+                acc[(c + i) / 2 + 1] = fma2(y, s2, acc[(c + i) / 2 + 1]);
+              }
+            }
+          }
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.tempty[t]);
+        if (++t == TL::kBufs) {
+          t = 0;
+          tphase ^= 1u;
+        }
+      }
+      if (!ok || !busy || !live) continue;
+      const int64_t out_row = WGRAD ? int64_t(w.e) * p.R + w.r0 + row : int64_t(w.row0) + row;
+      const int64_t at = out_row * p.C + c0;
+#pragma unroll
+      for (int c = 0; c < CW; c += 8) {
+        if (c0 + c < p.C) {                                      // C is a multiple of 16: eight columns are whole
+          const float2* a = &acc[c / 2];
+          if constexpr (BF16) {
+            uint4 u;
+            uint32_t* h = &u.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(a[i].x, a[i].y);
+              h[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + c) = u;
+          } else {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at + c);
+            o[0] = make_float4(a[0].x, a[0].y, a[1].x, a[1].y);
+            o[1] = make_float4(a[2].x, a[2].y, a[3].x, a[3].y);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_free(tmem);
+}
+
+// ---- host ------------------------------------------------------------------------
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// A row-major [rows, cols] byte matrix read in boxes of `box` rows by 128
+// columns; what lies outside reads as zero.
+bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box) {
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols};
+  const cuuint32_t boxes[2] = {kBK, box}, ones[2] = {1, 1};
+  return encode_fn() != nullptr &&
+         encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, boxes, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, bool WGRAD, bool BF16>
+cudaError_t launch(const MatmulParams& p, int sms, const char** error, cudaStream_t stream) {
+  CUtensorMap ma, mb;
+  const uint64_t cols = WGRAD ? uint64_t(p.blocks) * kBK : uint64_t(p.K);
+  const uint64_t rows_a = WGRAD ? uint64_t(p.R) : uint64_t(p.M), rows_b = WGRAD ? uint64_t(p.C) : uint64_t(p.E) * p.C;
+  if (!make_map(&ma, p.a, rows_a, cols, kBoxA) || !make_map(&mb, p.b, rows_b, cols, kBoxB)) {
+    *error = "cuTensorMapEncodeTiled refused an operand";
+    return cudaErrorUnknown;
+  }
+  constexpr size_t smem = size_t(Tile<BN>::kStages) * Tile<BN>::kStageBytes + 1024;
+  static_assert(Tile<BN>::kStages <= 8 && Tile<BN>::kBufs <= 8 && sizeof(Shared) + smem <= 232448, "shared memory of one CTA");
+  const auto kernel = expert_matmul_kernel<BN, WGRAD, BF16>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  // At most this many tiles: every expert's last row tile may be ragged.
+  const int64_t ct = (p.C + BN - 1) / BN;
+  int64_t rt = WGRAD ? int64_t(p.E) * ((p.R + kBM - 1) / kBM) : p.M / kBM + p.E;
+  if (!WGRAD && rt > p.M) rt = p.M;
+  const int grid = int(rt * ct < sms ? rt * ct : sms);
+  kernel<<<grid, kMmThreads, smem, stream>>>(p, ma, mb);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t expert_matmul_errors(int* bits, cudaStream_t stream) {
+  void* word = nullptr;
+  cudaError_t e = cudaGetSymbolAddress(&word, g_mm_errors);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(bits, word, sizeof(int), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e == cudaSuccess && *bits != 0) {
+    e = cudaMemsetAsync(word, 0, sizeof(int), stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  }
+  return e;
+}
+
+cudaError_t launch_expert_matmul(const MatmulParams& p, int sms, const char** error, cudaStream_t stream) {
+  if (p.wgrad) return launch<256, true, false>(p, sms, error, stream);
+  // Few rows an expert: reading the weights is what takes the time, and narrow
+  // tiles spread them over more SMs.
+  const bool narrow = p.M <= int64_t(p.E) * 64;
+  if (p.out_bf16)
+    return narrow ? launch<128, false, true>(p, sms, error, stream) : launch<256, false, true>(p, sms, error, stream);
+  return narrow ? launch<128, false, false>(p, sms, error, stream) : launch<256, false, false>(p, sms, error, stream);
+}
+
+}  // namespace moe

@@ -1,0 +1,345 @@
+"""GPU parity of the block-scaled quantisation, the experts' products and their weight gradient against float64.
+
+Codes and scales are compared exactly.  Bounds of the products, against the sum
+of the sizes of an element's terms: the tensor core adds a block's 128 products
+in fp32 (at most 2^-23 of the running size each), the blocks' sums are scaled
+(two roundings) and added (one each): (256 + 3 * blocks) * 2^-24; and half a
+step of bf16, 2^-8 of the value, for a bf16 result.  Where every sum is a whole
+number below 2^24 the result has to be exact.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import experts_reference as ref
+
+pytestmark = pytest.mark.gpu
+F8 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def mr(native_lib):
+    import moe_expert_routing_router_gb300 as m
+    yield m
+    assert m.moe_expert_device_status() == 0
+
+
+def values(shape, seed, dtype=torch.bfloat16, sigma=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(*shape, generator=g) * sigma * torch.exp(0.8 * torch.randn(shape[0], *([1] * (len(shape) - 1)), generator=g))
+    return x.to(dtype)
+
+
+def wide(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def i32(a):
+    return torch.as_tensor(np.asarray(a), dtype=torch.int32).cuda()
+
+
+def split(counts, kept=None):
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    return i32(offsets), None if kept is None else i32(kept), ref.expert_rows(offsets, kept, int(offsets[-1]))
+
+
+# -- quantisation ------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 128), (33, 144), (100, 512), (7, 1040), (65, 2064)])
+def test_rows(mr, M, K, dtype):
+    x = values((M, K), M + K, dtype)
+    x[0, :16] = 0
+    if K > 128:
+        x[-1, :128] = 0                                          # a block of zeros
+    got = mr.moe_quantize_rows(x.cuda())
+    q, scale = ref.quantize_rows(wide(x))
+    assert np.array_equal(wide(got["q"]), q) and np.array_equal(wide(got["scale"]), scale)
+
+
+def test_rows_gathered(mr):
+    T, k, E, K = 70, 3, 8, 272
+    rng = np.random.default_rng(0)
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(T)])
+    perm, _, _, _ = ref.dispatch(idx, E, 1000)
+    x = values((T, K), 1)
+    got = mr.moe_quantize_rows(x.cuda(), perm=i32(perm), k=k)
+    q, scale = ref.quantize_rows(wide(x)[perm // k])
+    assert np.array_equal(wide(got["q"]), q) and np.array_equal(wide(got["scale"]), scale)
+    bad = perm.copy()
+    bad[5], bad[6] = -1, T * k                                   # outside x: zeros
+    got = mr.moe_quantize_rows(x.cuda(), perm=i32(bad), k=k)
+    assert not wide(got["q"])[5:7].any() and (wide(got["scale"])[:, 5:7] == 1).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_every_rounding_and_scale(mr, dtype):
+    """All bf16 magnitudes next to a block maximum, values half-way between codes, tiny and huge blocks."""
+    top = torch.tensor([448.0, 447.0, 449.0, 2.0 ** -133, 2.0 ** -126, 1.75 * 2.0 ** -120, 3.0e38, 1.0])
+    x = torch.zeros(8 * 64, 128)
+    codes = torch.from_numpy(ref.e4m3_values()).float()
+    mid = (codes[:-1] + codes[1:]) / 2                           # ties
+    for i in range(8 * 64):
+        m = float(top[i // 64])
+        g = torch.Generator().manual_seed(i)
+        x[i] = torch.randn(128, generator=g) * m / 8
+        if i % 4 == 0:
+            x[i, :126] = mid[torch.randperm(126, generator=g)] * (2.0 ** torch.floor(torch.log2(torch.tensor(m))) / 256)
+        x[i] = x[i].clamp(-m, m)
+        x[i, 5] = m if i % 2 else -m
+    x = x.to(dtype)
+    got = mr.moe_quantize_rows(x.cuda())
+    q, scale = ref.quantize_rows(wide(x))
+    assert np.array_equal(wide(got["scale"]), scale)
+    assert np.array_equal(wide(got["q"]), q)
+
+
+def test_not_finite_blocks(mr):
+    x = values((5, 384), 3, torch.float32)
+    x[1, 130], x[2, 0], x[3, 383] = float("nan"), float("inf"), -float("inf")
+    got = mr.moe_quantize_rows(x.cuda())
+    s = wide(got["scale"])
+    bad = np.zeros((3, 5), bool)
+    bad[1, 1] = bad[0, 2] = bad[2, 3] = True
+    assert np.array_equal(np.isnan(s), bad)
+    ok = ref.quantize_rows(np.nan_to_num(wide(x), nan=0, posinf=0, neginf=0))
+    assert np.array_equal(wide(got["q"])[[0, 4]], ok[0][[0, 4]])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("counts,kept,K", [([1], None, 16), ([5, 0, 300, 128], None, 144), ([129, 127, 256, 1], [100, 127, 129, 0], 64),
+                                           ([0, 0, 3], None, 80), ([40] * 70, [33] * 70, 32)])
+def test_cols(mr, counts, kept, K, dtype):
+    M, E = sum(counts), len(counts)
+    x = values((M, K), M, dtype)
+    x[:, 3] = 0
+    offsets, kt, rows = split(counts, kept)
+    width = mr.moe_quantize_cols_width(M, E)
+    out = {"q": torch.full((K, width), 2.0, device="cuda").to(F8), "scale": torch.full((width // 128, K), 7.0, device="cuda")}
+    mr.moe_quantize_cols(x.cuda(), offsets, kt, out=out)
+    q, scale = ref.quantize_cols(wide(x), rows)
+    n = q.shape[1]
+    assert np.array_equal(wide(out["q"])[:, :n], q) and np.array_equal(wide(out["scale"])[:n // 128], scale)
+    assert (wide(out["q"])[:, n:] == 2).all() and (wide(out["scale"])[n // 128:] == 7).all()     # left as they were
+    if kept is None:
+        token = np.random.default_rng(1).permutation(M * 2)[:M]                                  # gathered rows
+        got = mr.moe_quantize_cols(x.cuda(), offsets, None, perm=i32(token), k=2)
+        q, scale = ref.quantize_cols(wide(x)[token // 2], rows)
+        assert np.array_equal(wide(got["q"])[:, :n], q) and np.array_equal(wide(got["scale"])[:n // 128], scale)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("E,N,K", [(1, 16, 16), (2, 128, 256), (3, 144, 272), (2, 272, 112)])
+def test_weights(mr, E, N, K, dtype):
+    w = values((E, N, K), N, dtype, 0.02)
+    w[0, :128, :128] = 0
+    got = mr.moe_quantize_weights(w.cuda(), transposed=True)
+    q, scale = ref.quantize_weights(wide(w))
+    assert np.array_equal(wide(got["q"]), q) and np.array_equal(wide(got["scale"]), scale)
+    assert np.array_equal(wide(got["qt"]), q.transpose(0, 2, 1)) and np.array_equal(wide(got["scalet"]), scale.transpose(0, 2, 1))
+    plain = mr.moe_quantize_weights(w.cuda())
+    assert set(plain) == {"q", "scale"} and torch.equal(plain["q"].view(torch.uint8), got["q"].view(torch.uint8))
+
+
+# -- products ------------------------------------------------------------------------
+
+def operands(M, K, E, N, seed):
+    g = torch.Generator().manual_seed(seed)
+    q = (torch.randn(M, K, generator=g) * 60).clamp(-448, 448).to(F8).cuda()
+    wq = (torch.randn(E, N, K, generator=g) * 60).clamp(-448, 448).to(F8).cuda()
+    # any fp32 scales, not only powers of two
+    scale = torch.exp(torch.randn(-(-K // 128), M, generator=g)).cuda()
+    wscale = torch.exp(torch.randn(E, -(-N // 128), -(-K // 128), generator=g)).cuda()
+    return q, scale, wq, wscale
+
+
+def check_matmul(mr, counts, kept, K, N, dtype, seed=0):
+    M, E = sum(counts), len(counts)
+    q, scale, wq, wscale = operands(M, K, E, N, seed)
+    offsets, kt, rows = split(counts, kept)
+    out = torch.full((M, N), 3.0, dtype=dtype, device="cuda")
+    got = mr.moe_expert_matmul(q, scale, wq, wscale, offsets, kt, out=out)
+    assert got is out
+    want, size = ref.matmul(wide(q), wide(scale), wide(wq), wide(wscale), rows)
+    untouched = np.isnan(want)
+    assert (wide(got)[untouched] == 3).all()
+    bound = (256 + 3 * (-(-K // 128))) * ref.U32 * size
+    if dtype == torch.bfloat16:
+        bound = bound * (1 + ref.U16) + ref.U16 * np.abs(want)
+    ref.assert_near("out", np.where(untouched, 0, wide(got)), np.where(untouched, 0, want), np.nan_to_num(bound))
+    return got
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("counts,kept,K,N", [
+    ([1], None, 16, 16), ([128], None, 128, 128), ([3, 0, 1], None, 144, 48), ([130, 5, 64], [129, 0, 64], 272, 272),
+    ([1] * 8, None, 512, 528), ([300, 17, 0, 200], None, 1040, 144), ([40] * 9, [33] * 9, 640, 256), ([257], None, 2064, 304),
+    ([700, 650, 1], [700, 600, 1], 384, 512), ([2] * 200, None, 144, 64),
+])
+def test_matmul(mr, counts, kept, K, N, dtype):
+    check_matmul(mr, counts, kept, K, N, dtype, seed=N)
+
+
+def test_whole_number_products_are_exact(mr):
+    """Sums that fp32 holds exactly: nothing may be lost in the tensor core or the registers."""
+    g = torch.Generator().manual_seed(1)
+    for M, K, E, N in ((200, 4096, 2, 256), (3, 1024, 3, 144)):
+        q = torch.randint(-8, 9, (M, K), generator=g).float().to(F8).cuda()
+        wq = torch.randint(-8, 9, (E, N, K), generator=g).float().to(F8).cuda()
+        scale = 2.0 ** torch.randint(0, 3, (K // 128, M), generator=g).float().cuda()
+        wscale = 2.0 ** torch.randint(0, 2, (E, -(-N // 128), K // 128), generator=g).float().cuda()
+        offsets, _, rows = split([M // E] * (E - 1) + [M - M // E * (E - 1)])
+        got = mr.moe_expert_matmul(q, scale, wq, wscale, offsets, out_dtype=torch.float32)
+        want, size = ref.matmul(wide(q), wide(scale), wide(wq), wide(wscale), rows)
+        assert size.max() < 2 ** 24 and np.array_equal(wide(got), want)
+
+
+def test_plain_product_without_offsets(mr):
+    q, scale, wq, wscale = operands(77, 400, 1, 208, 5)
+    got = mr.moe_expert_matmul(q, scale, wq, wscale)
+    want = mr.moe_expert_matmul(q, scale, wq, wscale, i32([0, 77]))
+    assert torch.equal(got, want) and got.dtype == torch.bfloat16
+
+
+def test_rows_do_not_depend_on_one_another(mr):
+    """A row alone, among few and among many (both tile widths): the same bits.  Not-a-number codes in
+    other rows, dropped ones and behind the last stay there."""
+    K, N, E = 512, 384, 2
+    q, scale, wq, wscale = operands(600, K, E, N, 9)
+    offsets, kept, _ = split([300, 300], [250, 300])
+    base = mr.moe_expert_matmul(q, scale, wq, wscale, offsets, kept, out_dtype=torch.float32)
+    bad = q.clone()
+    bad.view(torch.uint8)[7] = 0x7f
+    bad.view(torch.uint8)[250:300] = 0x7f
+    scale2 = scale.clone()
+    scale2[2, 11] = float("nan")
+    out = torch.zeros(600, N, device="cuda")
+    got = mr.moe_expert_matmul(bad, scale2, wq, wscale, offsets, kept, out=out)
+    keep = torch.ones(600, dtype=torch.bool, device="cuda")
+    keep[7] = keep[11] = False
+    keep[250:300] = False
+    assert torch.equal(got[keep], base[keep]) and got[7].isnan().all() and got[11].isnan().all() and not got[250:300].any()
+    for r in (0, 249, 300, 599):
+        one = mr.moe_expert_matmul(q[r:r + 1].contiguous(), scale[:, r:r + 1].contiguous(), wq, wscale,
+                                   i32([0, 1, 1] if r < 300 else [0, 0, 1]), out_dtype=torch.float32)
+        assert torch.equal(one[0], base[r])
+
+
+def test_positions_outside_the_arrays_stay_inside(mr):
+    """Offsets and counts that do not belong to the arrays give some result, and no access outside."""
+    q, scale, wq, wscale = operands(64, 128, 3, 64, 2)
+    for offsets, kept in (([0, 900, 64, 64], [9, 9, 9]), ([-5, 30, 20, 1 << 30], None), ([64, 64, 64, 64], None),
+                          ([0, 10, 20, 30], [-3, 1 << 30, 5])):
+        mr.moe_expert_matmul(q, scale, wq, wscale, i32(offsets), None if kept is None else i32(kept))
+        mr.moe_quantize_cols(values((64, 64), 1).cuda(), i32(offsets), None if kept is None else i32(kept))
+    torch.cuda.synchronize()
+    d = torch.zeros(32, 256, device="cuda").to(F8)
+    s = torch.ones(2, 32, device="cuda")
+    for kept in ([1 << 30, 5, 7], [-1, 300, 1], [256, 256, 256]):
+        mr.moe_expert_wgrad(d, s, d, s, i32(kept))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("counts,kept,N,K", [([1], None, 16, 16), ([128, 128], None, 128, 256), ([5, 0, 300, 129], None, 144, 272),
+                                             ([0, 0], None, 32, 48), ([260, 70, 600], [200, 70, 513], 304, 528), ([40] * 20, None, 64, 320)])
+def test_wgrad(mr, counts, kept, N, K):
+    M, E = max(sum(counts), 1), len(counts)
+    offsets, kt, rows = split(counts, kept)
+    dy, x = values((M, N), 1, sigma=0.01), values((M, K), 2)
+    # not-a-number in the columns behind the last expert's must not be read into any sum
+    width = mr.moe_quantize_cols_width(M, E)
+    outs = [{"q": torch.full((c, width), float("nan"), device="cuda").to(F8), "scale": torch.full((width // 128, c), float("nan"), device="cuda")} for c in (N, K)]
+    dq = mr.moe_quantize_cols(dy.cuda(), offsets, kt, out=outs[0])
+    xq = mr.moe_quantize_cols(x.cuda(), offsets, kt, out=outs[1])
+    kt = kt if kt is not None else i32(counts)
+    got = mr.moe_expert_wgrad(dq["q"], dq["scale"], xq["q"], xq["scale"], kt)
+    d64, x64 = ref.quantize_cols(wide(dy), rows), ref.quantize_cols(wide(x), rows)
+    want, size = ref.wgrad(*d64, *x64, rows)
+    blocks = max(-(-n // 128) for _, n in rows) if rows else 0
+    ref.assert_near("dw", wide(got), want, (256 + 3 * blocks) * ref.U32 * size)
+    for e, (_, n) in enumerate(rows):
+        if n == 0:
+            assert not wide(got)[e].any()
+
+
+def test_wgrad_with_any_scales(mr):
+    g = torch.Generator().manual_seed(3)
+    N, K, counts = 160, 288, [200, 128, 10]
+    rows = ref.expert_rows(np.concatenate([[0], np.cumsum(counts)]), None, sum(counts))
+    width = mr.moe_quantize_cols_width(sum(counts), 3)
+    dq, xq = ((torch.randn(n, width, generator=g) * 40).clamp(-448, 448).to(F8).cuda() for n in (N, K))
+    ds, xs = (torch.exp(torch.randn(width // 128, n, generator=g)).cuda() for n in (N, K))
+    got = mr.moe_expert_wgrad(dq, ds, xq, xs, i32(counts))
+    want, size = ref.wgrad(wide(dq), wide(ds), wide(xq), wide(xs), rows)
+    ref.assert_near("dw", wide(got), want, (256 + 3 * 2) * ref.U32 * size)
+
+
+def test_results_past_32_bit_offsets(mr):
+    """Operand and result positions past 2^31; rows at both ends are compared with a small call's."""
+    M, K, N = 2 ** 31 // 4096 + 300, 4096, 4112
+    part = torch.randint(-8, 9, (300, K), generator=torch.Generator().manual_seed(0)).float().to(F8).cuda()
+    q = torch.zeros(M, K, dtype=torch.uint8, device="cuda").view(F8)
+    q.view(torch.uint8)[:300] = part.view(torch.uint8)
+    q.view(torch.uint8)[-300:] = part.view(torch.uint8)
+    scale = torch.ones(K // 128, M, device="cuda")
+    _, _, wq, wscale = operands(1, K, 1, N, 1)
+    got = mr.moe_expert_matmul(q, scale, wq, wscale)
+    want = mr.moe_expert_matmul(part, torch.ones(K // 128, 300, device="cuda"), wq, wscale)
+    assert torch.equal(got[:300], want) and torch.equal(got[-300:], want)
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    x[-300:] = part.to(torch.bfloat16)
+    r = mr.moe_quantize_rows(x)
+    w = mr.moe_quantize_rows(x[-300:].contiguous())
+    assert torch.equal(r["q"][-300:].view(torch.uint8), w["q"].view(torch.uint8)) and torch.equal(r["scale"][:, -300:], w["scale"])
+
+
+def test_captured_and_concurrent_calls(mr):
+    """Two graphs on two streams at once, and eager calls beside them: no state is shared."""
+    sets = []
+    for i in range(2):
+        q, scale, wq, wscale = operands(300, 512, 4, 256, 20 + i)
+        offsets, kept, _ = split([100, 0, 150, 50], [90, 0, 150, 50])
+        out = torch.zeros(300, 256, dtype=torch.bfloat16, device="cuda")
+        want = mr.moe_expert_matmul(q, scale, wq, wscale, offsets, kept, out=torch.zeros_like(out))
+        sets.append((q, scale, wq, wscale, offsets, kept, out, want))
+    graphs = []
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for s, (q, scale, wq, wscale, offsets, kept, out, _) in zip(streams, sets):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(3):
+                mr.moe_expert_matmul(q, scale, wq, wscale, offsets, kept, out=out, stream=s)
+        graphs.append(g)
+    for _ in range(5):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        mr.moe_expert_matmul(*sets[0][:6], out=torch.zeros_like(sets[0][6]))
+    torch.cuda.synchronize()
+    for *_, out, want in sets:
+        assert torch.equal(out, want)
+
+
+def test_an_expired_wait_is_reported(mr, native_lib):
+    """A pipeline wait made to run out (1 ms, an arrival that never comes): the status
+    tells, later calls write nothing until it is read, then calls work again."""
+    q, scale, wq, wscale = operands(200, 1024, 1, 256, 4)
+    want = mr.moe_expert_matmul(q, scale, wq, wscale)
+    torch.cuda.synchronize()
+    assert mr.moe_expert_device_status() == 0
+    native_lib.moe_set_wait_timeout_ns(1_000_000)
+    native_lib.moe_set_unreachable_barriers(1)
+    try:
+        mr.moe_expert_matmul(q, scale, wq, wscale)
+        torch.cuda.synchronize()
+    finally:
+        native_lib.moe_set_unreachable_barriers(0)
+        native_lib.moe_set_wait_timeout_ns(0)
+    out = torch.full((200, 256), 5.0, dtype=torch.bfloat16, device="cuda")
+    mr.moe_expert_matmul(q, scale, wq, wscale, out=out)
+    assert (out == 5).all()
+    assert mr.moe_expert_device_status() == 2
+    assert mr.moe_expert_device_status() == 0
+    assert torch.equal(mr.moe_expert_matmul(q, scale, wq, wscale, out=out), want)

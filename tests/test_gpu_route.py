@@ -1,0 +1,286 @@
+"""GPU parity of the scored, group-limited routing and its gradient against float64.
+
+Picks and counts are compared exactly.  Bounds of the floating outputs, with D
+the row's spread of finite logits (the argument of an exponential is rounded to
+2^-24 of itself, which moves the exponential by 2^-24 D of its value):
+  gate     (2 D + 96) * 2^-24 of itself: two argument roundings; a sum of at most 64
+           values per lane, 5 steps across lanes and 8 picks (77 roundings); ex2.approx
+           (4 units of 2^-24), expf, quotient, 1 + e and scale (8)
+  dlogits  the same bound twice (shares and differences of them), against the sum of the
+           sizes of the gradient's terms
+and FLT_MIN (times the scale) absolutely, where an exponential underflows.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import experts_reference as ref
+
+pytestmark = pytest.mark.gpu
+FLT_MIN = 2.0 ** -126
+
+
+@pytest.fixture(scope="module")
+def mr(native_lib):
+    import moe_expert_routing_router_gb300 as m
+    return m
+
+
+def logits_of(T, E, dtype, seed, spread=1.5):
+    rng = np.random.default_rng(seed)
+    z = torch.from_numpy((rng.standard_normal((T, E)) * spread + rng.standard_normal(E)).astype(np.float32))
+    return z.to(dtype)
+
+
+def bias_of(E, seed):
+    return (np.random.default_rng(seed).integers(-150, 151, E) * 0.001).astype(np.float32)
+
+
+def widen(z):
+    return z.float().numpy().astype(np.float64)
+
+
+def spread_of(z):
+    f = np.where(np.isfinite(z), z, np.nan)
+    with np.errstate(all="ignore"):
+        import warnings
+        with warnings.catch_warnings():
+            warnings.simplefilter("ignore")
+            d = np.nanmax(np.abs(f), axis=1, keepdims=True) * 2
+    return np.minimum(np.nan_to_num(d), 400.0)       # beyond about 200 every exponential is 0 or 1
+
+
+def check(mr, z, k, score="sigmoid", bias=None, n_groups=1, topk_groups=1, group_score="top2", renorm=True, scale=1.0, gamma=0.01):
+    zd = widen(z)
+    T, E = zd.shape
+    b = None if bias is None else torch.from_numpy(bias).cuda()
+    got = mr.moe_route_fwd(z.cuda(), k, score=score, bias=b, n_groups=n_groups, topk_groups=topk_groups,
+                           group_score=group_score, renorm=int(renorm), scale=scale, bias_gamma=gamma, bias_out=True)
+    idx = ref.choose(zd, k, score, bias, n_groups, topk_groups, group_score)
+    gi = got["idx"].cpu().numpy()
+    assert np.array_equal(gi, idx), f"{(gi != idx).any(axis=1).sum()} rows of {T} pick other experts"
+    counts = np.bincount(idx.ravel(), minlength=E)
+    assert np.array_equal(got["counts"].cpu().numpy(), counts)
+    w = ref.pick_weights(zd, idx, score, renorm)
+    eps = (2 * spread_of(zd) + 96) * ref.U32
+    ref.assert_near("gate", got["gate"].cpu().numpy(), scale * w, scale * (eps * w + FLT_MIN))
+    b0 = np.zeros(E, np.float32) if bias is None else bias
+    want_b = (b0 + np.float32(gamma) * np.sign(T * k - counts * E).astype(np.float32)).astype(np.float32)
+    assert np.array_equal(got["bias_out"].cpu().numpy(), want_b)
+    return got, idx, zd
+
+
+def check_bwd(mr, z, idx, score, renorm, scale, seed=3):
+    zd = widen(z)
+    T, k = idx.shape
+    E = zd.shape[1]
+    dgate = np.random.default_rng(seed).standard_normal((T, k)).astype(np.float32)
+    got = mr.moe_route_bwd(z.cuda(), torch.from_numpy(idx.astype(np.int32)).cuda(), torch.from_numpy(dgate).cuda(),
+                           score=score, renorm=int(renorm), scale=scale).cpu().numpy()
+    want = ref.route_grad(zd, idx, dgate, score, renorm, scale)
+    live = (idx >= 0) & (idx < E)
+    safe = np.where(live, idx, 0)
+    size = np.zeros((T, E))
+    dg = np.abs(np.where(live, dgate, 0.0)).astype(np.float64) * abs(scale)
+    s = ref.scores(zd, score)
+    if renorm:
+        zz = np.where(live, np.take_along_axis(zd, safe, 1), -np.inf)
+        w = ref.pick_weights(zz, np.arange(k)[None, :].repeat(T, 0), score, True)
+        term = w * (dg + (w * dg).sum(axis=1, keepdims=True))
+    else:
+        w = np.take_along_axis(s, safe, 1)
+        term = w * dg
+    for j in range(k):
+        np.add.at(size, (np.arange(T), safe[:, j]), np.where(live[:, j], term[:, j], 0.0))
+    if score == "softmax" and not renorm:
+        size += s * (w * dg).sum(axis=1, keepdims=True)
+    eps = 2 * (2 * spread_of(zd) + 96) * ref.U32
+    ref.assert_near("dlogits", got, want, eps * size + 8 * abs(scale) * FLT_MIN)
+    return got
+
+
+SHAPES = [  # T, E, k, groups, kept groups
+    (1, 256, 8, 8, 4), (33, 256, 8, 8, 4), (257, 64, 6, 8, 3), (129, 384, 6, 12, 5), (1, 1, 1, 1, 1), (70, 2, 2, 1, 1),
+    (65, 60, 4, 4, 2), (31, 7, 3, 1, 1), (40, 1024, 8, 32, 8), (37, 1020, 8, 17, 5), (32, 1000, 7, 1, 1), (300, 160, 6, 8, 3),
+    (50, 9, 1, 3, 1), (41, 96, 8, 32, 3), (1031, 8, 2, 1, 1), (45, 30, 5, 6, 1),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_routing_and_gradient(mr, shape, score, dtype):
+    T, E, k, G, keep = shape
+    z = logits_of(T, E, dtype, seed=T + E)
+    for group_score in ("top2", "max"):
+        for bias in (None, bias_of(E, 5)):
+            for renorm in (True, False):
+                _, idx, _ = check(mr, z, k, score, bias, G, keep, group_score, renorm, 2.5)
+    for renorm in (True, False):
+        check_bwd(mr, z, idx, score, renorm, 2.5)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("group_score", ["top2", "max"])
+def test_ties_go_to_the_lower_index(mr, score, group_score):
+    rng = np.random.default_rng(0)
+    z = torch.from_numpy(rng.integers(-1, 2, (600, 64)).astype(np.float32)).to(torch.bfloat16)
+    z[:, 3] = -0.0
+    for bias in (None, np.zeros(64, np.float32), (rng.integers(-1, 2, 64) * 0.25).astype(np.float32)):
+        check(mr, z, 8, score, bias, 8, 3, group_score)
+        check(mr, z, 8, score, bias)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_choice_values_that_fp32_cannot_tell_apart(mr, score, grouped):
+    """Biases that make an expert's choice value equal another's to about one fp32
+    rounding, either way: the picks are those of double precision."""
+    rng = np.random.default_rng(11)
+    E, T = 64, 500
+    row = rng.standard_normal(E).astype(np.float32)
+    s = ref.scores(row[None].astype(np.float64), score)[0]
+    bias = np.zeros(E, np.float32)
+    bias[1::2] = (s[0::2] - s[1::2]).astype(np.float32)           # pairs (0, 1), (2, 3), ... all but equal
+    z = np.repeat(row[None], T, 0)
+    z[:, 1::2] = np.nextafter(z[:, 1::2], np.where(rng.random((T, E // 2)) < 0.5, -9, 9).astype(np.float32))
+    if grouped:                                                   # whole groups all but equal
+        z[:, 32:] = z[:, :32]
+        bias[32:] = bias[:32]
+        z[:, 40] = np.nextafter(z[:, 40], np.float32(9))
+    zt = torch.from_numpy(z)
+    for group_score in ("top2", "max"):
+        check(mr, zt, 8, score, bias, 4 if grouped else 1, 2 if grouped else 1, group_score)
+    check(mr, zt, 8, score, None, 4, 2, "top2")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_masked_logits(mr, score, dtype):
+    T, E, k, G = 64, 64, 6, 8
+    z = logits_of(T, E, dtype, seed=4)
+    rng = np.random.default_rng(2)
+    z[torch.from_numpy(rng.random((T, E)) < 0.5)] = -float("inf")
+    z[0] = -float("inf")                                         # nothing left
+    z[1] = -float("inf")
+    z[1, 37] = 0.5                                               # one expert left
+    z[2] = torch.finfo(dtype).min                                # the lowest finite value everywhere
+    z[3, :32] = torch.finfo(dtype).min
+    z[4, 10:20] = float("nan")
+    z[5] = float("nan")
+    z[6] = -float("inf")
+    z[6, ::8] = torch.arange(8).to(dtype)                        # one expert a group
+    for bias in (None, bias_of(E, 1)):
+        for group_score in ("top2", "max"):
+            for renorm in (True, False):
+                got, idx, zd = check(mr, z, k, score, bias, G, 3, group_score, renorm)
+                assert (got["gate"][0] == 0).all() and (got["gate"][5] == 0).all()
+                grad = check_bwd(mr, z, idx, score, renorm, 1.0)
+                assert np.isfinite(grad).all() and not grad[0].any()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_gates_keep_their_digits_where_scores_underflow(mr, score):
+    z = logits_of(100, 32, torch.float32, seed=6) - 300.0
+    got, _, _ = check(mr, z, 4, score, None, renorm=True)
+    assert abs(got["gate"].sum(1) - 1).max() < 1e-5
+    z[:, 0] = 250.0                                              # a saturated expert beside them
+    check(mr, z, 4, score, None, renorm=True)
+    check(mr, z, 4, score, None, renorm=False)
+    check_bwd(mr, z, np.tile(np.arange(4), (100, 1)), score, True, 1.0)
+
+
+def test_row_results_do_not_depend_on_the_batch(mr):
+    z = logits_of(300, 256, torch.bfloat16, seed=8).cuda()
+    b = torch.from_numpy(bias_of(256, 9)).cuda()
+    args = dict(bias=b, n_groups=8, topk_groups=4, scale=2.5)
+    whole = mr.moe_route_fwd(z, 8, **args)
+    again = mr.moe_route_fwd(z, 8, **args)
+    for key in whole:
+        assert torch.equal(whole[key], again[key])
+    for t in (0, 17, 299):
+        one = mr.moe_route_fwd(z[t:t + 1].contiguous(), 8, **args)
+        assert torch.equal(one["idx"][0], whole["idx"][t]) and torch.equal(one["gate"][0], whole["gate"][t])
+
+
+def test_bias_in_place_and_preallocated_outputs(mr):
+    z = logits_of(500, 64, torch.bfloat16, seed=1).cuda()
+    for T in (20, 500):                                          # one CTA, many
+        bias = torch.zeros(64, device="cuda")
+        want = mr.moe_route_fwd(z[:T].contiguous(), 4, bias=bias, bias_gamma=0.5, bias_out=True)
+        out = {"idx": torch.empty(T, 4, dtype=torch.int32, device="cuda"), "gate": torch.empty(T, 4, device="cuda"),
+               "counts": torch.full((64,), 99, dtype=torch.int32, device="cuda")}
+        got = mr.moe_route_fwd(z[:T].contiguous(), 4, bias=bias, bias_gamma=0.5, bias_out=bias, out=out)
+        assert got["bias_out"] is bias and got["counts"] is out["counts"]
+        for key in ("idx", "gate", "counts", "bias_out"):
+            assert torch.equal(got[key], want[key]), key
+
+
+@pytest.mark.parametrize("score,renorm", [("sigmoid", True), ("sigmoid", False), ("softmax", True), ("softmax", False)])
+def test_gradient_of_repeated_and_foreign_picks(mr, score, renorm):
+    z = logits_of(40, 33, torch.float32, seed=2)
+    rng = np.random.default_rng(1)
+    idx = rng.integers(0, 33, (40, 5))
+    idx[:, 1] = idx[:, 0]                                        # the same expert twice
+    idx[::3, 2] = -1                                             # no expert
+    idx[::5, 3] = 33
+    check_bwd(mr, z, idx, score, renorm, 1.5)
+
+
+def test_misaligned_views(mr):
+    """Logits that start two or four bytes past a vector boundary, and a gradient that does."""
+    for dtype in (torch.bfloat16, torch.float32):
+        flat = torch.zeros(64 * 256 + 1, dtype=dtype, device="cuda")
+        z = flat[1:].view(64, 256)
+        z.copy_(logits_of(64, 256, dtype, seed=3))
+        want = mr.moe_route_fwd(z.clone(), 8, n_groups=8, topk_groups=4)
+        got = mr.moe_route_fwd(z, 8, n_groups=8, topk_groups=4)
+        assert all(torch.equal(got[k], want[k]) for k in got)
+        dg = torch.randn(64, 8, device="cuda")
+        dl = torch.zeros(64 * 256 + 1, device="cuda")[1:].view(64, 256)
+        for score, renorm in (("sigmoid", 1), ("softmax", 0)):
+            a = mr.moe_route_bwd(z, got["idx"], dg, score=score, renorm=renorm, dlogits=dl)
+            assert torch.equal(a, mr.moe_route_bwd(z.clone(), got["idx"], dg, score=score, renorm=renorm))
+
+
+def test_captured_and_replayed_on_another_stream(mr):
+    z = logits_of(200, 64, torch.bfloat16, seed=5).cuda()
+    bias = torch.zeros(64, device="cuda")
+    out = {"idx": torch.empty(200, 4, dtype=torch.int32, device="cuda"), "gate": torch.empty(200, 4, device="cuda"),
+           "counts": torch.empty(64, dtype=torch.int32, device="cuda")}
+    dl = torch.empty(200, 64, device="cuda")
+    dg = torch.randn(200, 4, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        mr.moe_route_fwd(z, 4, bias=bias, bias_gamma=0.01, bias_out=bias, out=out, stream=s)
+        mr.moe_route_bwd(z, out["idx"], dg, dlogits=dl, stream=s)
+    b = torch.zeros(64, device="cuda")
+    for step in range(3):
+        z.copy_(logits_of(200, 64, torch.bfloat16, seed=50 + step))
+        g.replay()
+        want = mr.moe_route_fwd(z, 4, bias=b, bias_gamma=0.01, bias_out=True)
+        b = want["bias_out"]
+        torch.cuda.synchronize()
+        assert torch.equal(out["idx"], want["idx"]) and torch.equal(out["counts"], want["counts"]) and torch.equal(bias, b)
+        assert torch.equal(dl, mr.moe_route_bwd(z, want["idx"], dg))
+
+
+def test_a_large_batch_and_64_bit_offsets(mr):
+    """T * E passes 2^31 elements; rows at both ends are compared."""
+    T, E, k = 2 ** 23 + 5, 264, 4
+    z = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    part = logits_of(300, E, torch.bfloat16, seed=12)
+    z[-300:] = part.cuda()
+    z[:300] = part.cuda()
+    got = mr.moe_route_fwd(z, k, n_groups=8, topk_groups=3)
+    want = mr.moe_route_fwd(part.cuda(), k, n_groups=8, topk_groups=3)
+    for at in (slice(0, 300), slice(T - 300, T)):
+        assert torch.equal(got["idx"][at], want["idx"]) and torch.equal(got["gate"][at], want["gate"])
+    assert int(got["counts"].sum()) == T * k
+    dg = torch.ones(T, k, device="cuda")
+    dg[-300:] = torch.randn(300, k, device="cuda")
+    d = mr.moe_route_bwd(z, got["idx"], dg)
+    assert torch.equal(d[-300:], mr.moe_route_bwd(part.cuda(), want["idx"], dg[-300:].contiguous()))
