@@ -6,9 +6,11 @@
 //   dgate[t,j]  = <dout[t], y[row]>
 //
 // over the assignments that were kept (slot >= 0).  Both are bound by memory:
-// every row is read once, in 16-byte loads that are all in flight before the
-// first is used, sums are fp32 in the order of j, and there are no atomics:
-// a token's rows belong to one CTA, so repeated calls give the same bits.
+// every row is read once, in 16-byte loads of which a thread has k in flight,
+// sums are fp32 in the order of j, and there are no atomics: repeated calls give
+// the same bits.  W warps work on a token; many tokens take one warp each (its
+// index loads and row loads overlap with the other warps' of the SM), few tokens
+// take up to eight.
 #include "device_common.cuh"
 #include "expert_combine.h"
 
@@ -18,43 +20,44 @@ namespace moe {
 namespace {
 
 constexpr int kMaxK = 8;
+constexpr int kWarps = 8;            // of a CTA
+constexpr unsigned kFull = 0xffffffffu;
 
+// VEC neighbouring values, kept as they were loaded.
 template <bool BF16, int VEC>
-__device__ __forceinline__ void load_vec(const void* x, int64_t at, float* v) {
-  if constexpr (VEC == 1) {
-    v[0] = BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(x)[at]) : static_cast<const float*>(x)[at];
-  } else if constexpr (BF16) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + at);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-    const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-  }
-}
+struct Piece {
+  static constexpr int kWords = VEC == 1 ? 1 : 4;
+  uint32_t w[kWords];
 
-template <bool BF16, int VEC>
-__device__ __forceinline__ void store_vec(void* x, int64_t at, const float* v) {
-  if constexpr (VEC == 1) {
-    if constexpr (BF16) static_cast<__nv_bfloat16*>(x)[at] = __float2bfloat16_rn(v[0]);
-    else static_cast<float*>(x)[at] = v[0];
-  } else if constexpr (BF16) {
-    uint4 u;
-    uint32_t* w = &u.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  __device__ __forceinline__ void load(const void* x, int64_t at) {
+    if constexpr (VEC == 1) {
+      w[0] = BF16 ? uint32_t(static_cast<const uint16_t*>(x)[at]) : static_cast<const uint32_t*>(x)[at];
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const char*>(x) + at * (BF16 ? 2 : 4));
+      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
     }
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(x) + at) = u;
-  } else {
-    *reinterpret_cast<float4*>(static_cast<float*>(x) + at) = make_float4(v[0], v[1], v[2], v[3]);
   }
-}
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (BF16) return __uint_as_float(i % 2 == 0 ? w[i / 2] << 16 : w[i / 2] & 0xffff0000u);
+    else return __uint_as_float(w[i]);
+  }
+  __device__ __forceinline__ static void store(void* x, int64_t at, const float* v) {
+    if constexpr (VEC == 1) {
+      if constexpr (BF16) static_cast<__nv_bfloat16*>(x)[at] = __float2bfloat16_rn(v[0]);
+      else static_cast<float*>(x)[at] = v[0];
+    } else if constexpr (BF16) {
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        h[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(x) + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    } else {
+      *reinterpret_cast<float4*>(static_cast<float*>(x) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  }
+};
 
 // The row of an assignment, or -1 when it was dropped or lies outside y.
 __device__ __forceinline__ int64_t assigned_row(const int32_t* idx, const int32_t* slot, const int32_t* offsets, int64_t a,
@@ -65,123 +68,140 @@ __device__ __forceinline__ int64_t assigned_row(const int32_t* idx, const int32_
   return r >= 0 && r < M ? r : -1;
 }
 
-// One CTA per token and piece of blockDim.x * VEC columns.
-template <bool BF16, int VEC>
-__global__ void __launch_bounds__(512) expert_combine_kernel(const CombineRowsParams p) {
-  __shared__ int64_t s_row[kMaxK];
-  __shared__ float s_gate[kMaxK];
-  const int64_t t = blockIdx.x;
-  if (threadIdx.x < p.k) {
-    const int64_t a = t * p.k + threadIdx.x;
-    s_row[threadIdx.x] = assigned_row(p.idx, p.slot, p.offsets, a, p.E, p.M);
-    s_gate[threadIdx.x] = p.gate != nullptr ? p.gate[a] : 1.f;
-  }
-  __syncthreads();
-  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
-  if (c >= p.H) return;
-  float v[kMaxK][VEC];
-#pragma unroll
-  for (int j = 0; j < kMaxK; ++j)
-    if (j < p.k && s_row[j] >= 0) load_vec<BF16, VEC>(p.y, s_row[j] * p.H + c, v[j]);
-  float acc[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
-#pragma unroll
-  for (int j = 0; j < kMaxK; ++j)
-    if (j < p.k && s_row[j] >= 0) {
-      const float g = s_gate[j];
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] = fmaf(g, v[j][i], acc[i]);
+// A warp's token, its pieces of the row, and lane j's assignment spread to all lanes.
+struct Token {
+  int64_t t;
+  int part;                       // of the W warps of the token
+  int row[kMaxK];                 // rows of y, -1 for none
+  float gate[kMaxK];
+
+  __device__ __forceinline__ void fetch(const int32_t* idx, const int32_t* slot, const int32_t* offsets, const float* g,
+                                        int64_t T, int64_t M, int k, int E, int W, int lane) {
+    const int64_t unit = int64_t(blockIdx.x) * kWarps + threadIdx.x / kWarp;
+    t = unit / W;
+    part = int(unit % W);
+    int r = -1;
+    float gv = 0.f;
+    if (t < T && lane < k) {
+      r = int(assigned_row(idx, slot, offsets, t * k + lane, E, M));
+      gv = g != nullptr ? g[t * k + lane] : 1.f;
     }
-  store_vec<BF16, VEC>(p.out, t * p.H + c, acc);
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j) {
+      row[j] = __shfl_sync(kFull, r, j);          // lanes from k on hold -1
+      gate[j] = __shfl_sync(kFull, gv, j);
+    }
+  }
+};
+
+template <bool BF16, int VEC>
+__global__ void __launch_bounds__(kWarps * kWarp) expert_combine_kernel(const CombineRowsParams p, int W) {
+  using P = Piece<BF16, VEC>;
+  const int lane = threadIdx.x % kWarp;
+  Token tk;
+  tk.fetch(p.idx, p.slot, p.offsets, p.gate, p.T, p.M, p.k, p.E, W, lane);
+  if (tk.t >= p.T) return;
+  for (int c = (tk.part * kWarp + lane) * VEC; c < p.H; c += W * kWarp * VEC) {
+    P v[kMaxK];
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j)
+      if (tk.row[j] >= 0) v[j].load(p.y, int64_t(tk.row[j]) * p.H + c);
+    float acc[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j)
+      if (tk.row[j] >= 0) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[i] = fmaf(tk.gate[j], v[j].get(i), acc[i]);
+      }
+    P::store(p.out, tk.t * p.H + c, acc);
+  }
 }
 
-// One CTA per token: it passes over the columns once and adds up the k dots.
 template <bool BF16, int VEC>
-__global__ void __launch_bounds__(256) expert_combine_bwd_kernel(const CombineRowsBwdParams p) {
-  __shared__ int64_t s_row[kMaxK];
-  __shared__ float s_gate[kMaxK];
-  __shared__ float s_dot[kMaxK][8];
-  const int64_t t = blockIdx.x;
+__global__ void __launch_bounds__(kWarps * kWarp) expert_combine_bwd_kernel(const CombineRowsBwdParams p, int W) {
+  using P = Piece<BF16, VEC>;
+  __shared__ float s_dot[kWarps][kMaxK];
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
-  if (threadIdx.x < p.k) {
-    const int64_t a = t * p.k + threadIdx.x;
-    s_row[threadIdx.x] = assigned_row(p.idx, p.slot, p.offsets, a, p.E, p.M);
-    s_gate[threadIdx.x] = p.gate[a];
-  }
-  __syncthreads();
+  Token tk;
+  tk.fetch(p.idx, p.slot, p.offsets, p.gate, p.T, p.M, p.k, p.E, W, lane);
   float dot[kMaxK];
 #pragma unroll
   for (int j = 0; j < kMaxK; ++j) dot[j] = 0.f;
-  for (int c = threadIdx.x * VEC; c < p.H; c += blockDim.x * VEC) {
-    float d[VEC], v[kMaxK][VEC];
-    load_vec<BF16, VEC>(p.dout, t * p.H + c, d);
+  if (tk.t < p.T) {
+    for (int c = (tk.part * kWarp + lane) * VEC; c < p.H; c += W * kWarp * VEC) {
+      P d, v[kMaxK];
+      d.load(p.dout, tk.t * p.H + c);
 #pragma unroll
-    for (int j = 0; j < kMaxK; ++j)
-      if (j < p.k && s_row[j] >= 0) load_vec<BF16, VEC>(p.y, s_row[j] * p.H + c, v[j]);
+      for (int j = 0; j < kMaxK; ++j)
+        if (tk.row[j] >= 0) v[j].load(p.y, int64_t(tk.row[j]) * p.H + c);
 #pragma unroll
-    for (int j = 0; j < kMaxK; ++j)
-      if (j < p.k && s_row[j] >= 0) {
-        const float g = s_gate[j];
+      for (int j = 0; j < kMaxK; ++j)
+        if (tk.row[j] >= 0) {
+          float o[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          dot[j] = fmaf(d[i], v[j][i], dot[j]);
-          v[j][i] = g * d[i];
+          for (int i = 0; i < VEC; ++i) {
+            dot[j] = fmaf(d.get(i), v[j].get(i), dot[j]);
+            o[i] = tk.gate[j] * d.get(i);
+          }
+          P::store(p.dy, int64_t(tk.row[j]) * p.H + c, o);
         }
-        store_vec<BF16, VEC>(p.dy, s_row[j] * p.H + c, v[j]);
-      }
-  }
-#pragma unroll
-  for (int j = 0; j < kMaxK; ++j)
-    if (j < p.k) {
-      const float s = warp_sum_f(dot[j]);
-      if (lane == 0) s_dot[j][warp] = s;
     }
-  __syncthreads();
-  if (threadIdx.x < p.k) {
-    float s = 0.f;
-    for (int w = 0; w < int(blockDim.x) / kWarp; ++w) s += s_dot[threadIdx.x][w];
-    p.dgate[t * p.k + threadIdx.x] = s_row[threadIdx.x] >= 0 ? s : 0.f;
   }
+  float mine = 0.f;                                             // lane j: the warp's part of dgate[t, j]
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    const float s = warp_sum_f(dot[j]);
+    if (lane == j) mine = s;
+  }
+  if (W > 1) {                                                  // the token's warps are neighbours in the CTA
+    if (lane < kMaxK) s_dot[warp][lane] = mine;
+    __syncthreads();
+    if (tk.part != 0 || lane >= kMaxK) return;
+    mine = 0.f;
+    for (int w = 0; w < W; ++w) mine += s_dot[warp + w][lane];
+  }
+  if (tk.t < p.T && lane < p.k) p.dgate[tk.t * p.k + lane] = mine;
 }
 
 bool vec_ok(int H, int vec, const void* a, const void* b, const void* c) {
   return H % vec == 0 && (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c)) % 16 == 0;
 }
 
-int threads_for(int64_t pieces, int most) {
-  int t = kWarp;
-  while (t < most && t < pieces) t += kWarp;
-  return t;
+// Warps of a token: one, and up to a CTA's eight (a power of two, at most one per
+// 32 pieces) while that leaves fewer than 16 warps an SM.
+int warps_for(int64_t T, int H, int vec, int sms) {
+  const int64_t pieces = (int64_t(H) + vec - 1) / vec;
+  int W = 1;
+  while (W < kWarps && T * W < int64_t(sms) * 16 && int64_t(W) * kWarp < pieces) W *= 2;
+  return W;
 }
 
 template <bool BF16, int VEC>
-cudaError_t combine_launch(const CombineRowsParams& p, cudaStream_t stream) {
-  const int64_t pieces = (p.H + VEC - 1) / VEC;
-  // Few tokens: small CTAs, so that a token's columns spread over several SMs.
-  const int threads = threads_for(pieces, p.T < 256 ? 64 : 256);
-  const dim3 grid(unsigned(p.T), unsigned((pieces + threads - 1) / threads));
-  expert_combine_kernel<BF16, VEC><<<grid, threads, 0, stream>>>(p);
+cudaError_t combine_launch(const CombineRowsParams& p, int sms, cudaStream_t stream) {
+  const int W = warps_for(p.T, p.H, VEC, sms);
+  expert_combine_kernel<BF16, VEC><<<unsigned((p.T * W + kWarps - 1) / kWarps), kWarps * kWarp, 0, stream>>>(p, W);
   return cudaGetLastError();
 }
 
 template <bool BF16, int VEC>
-cudaError_t combine_bwd_launch(const CombineRowsBwdParams& p, cudaStream_t stream) {
-  const int threads = threads_for((p.H + VEC - 1) / VEC, 256);
-  expert_combine_bwd_kernel<BF16, VEC><<<unsigned(p.T), threads, 0, stream>>>(p);
+cudaError_t combine_bwd_launch(const CombineRowsBwdParams& p, int sms, cudaStream_t stream) {
+  const int W = warps_for(p.T, p.H, VEC, sms);
+  expert_combine_bwd_kernel<BF16, VEC><<<unsigned((p.T * W + kWarps - 1) / kWarps), kWarps * kWarp, 0, stream>>>(p, W);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_expert_combine(const CombineRowsParams& p, bool bf16, cudaStream_t stream) {
-  if (bf16) return vec_ok(p.H, 8, p.y, p.out, nullptr) ? combine_launch<true, 8>(p, stream) : combine_launch<true, 1>(p, stream);
-  return vec_ok(p.H, 4, p.y, p.out, nullptr) ? combine_launch<false, 4>(p, stream) : combine_launch<false, 1>(p, stream);
+cudaError_t launch_expert_combine(const CombineRowsParams& p, bool bf16, int sms, cudaStream_t stream) {
+  if (bf16) return vec_ok(p.H, 8, p.y, p.out, nullptr) ? combine_launch<true, 8>(p, sms, stream) : combine_launch<true, 1>(p, sms, stream);
+  return vec_ok(p.H, 4, p.y, p.out, nullptr) ? combine_launch<false, 4>(p, sms, stream) : combine_launch<false, 1>(p, sms, stream);
 }
 
-cudaError_t launch_expert_combine_bwd(const CombineRowsBwdParams& p, bool bf16, cudaStream_t stream) {
-  if (bf16) return vec_ok(p.H, 8, p.y, p.dout, p.dy) ? combine_bwd_launch<true, 8>(p, stream) : combine_bwd_launch<true, 1>(p, stream);
-  return vec_ok(p.H, 4, p.y, p.dout, p.dy) ? combine_bwd_launch<false, 4>(p, stream) : combine_bwd_launch<false, 1>(p, stream);
+cudaError_t launch_expert_combine_bwd(const CombineRowsBwdParams& p, bool bf16, int sms, cudaStream_t stream) {
+  if (bf16) return vec_ok(p.H, 8, p.y, p.dout, p.dy) ? combine_bwd_launch<true, 8>(p, sms, stream) : combine_bwd_launch<true, 1>(p, sms, stream);
+  return vec_ok(p.H, 4, p.y, p.dout, p.dy) ? combine_bwd_launch<false, 4>(p, sms, stream) : combine_bwd_launch<false, 1>(p, sms, stream);
 }
 
 }  // namespace moe

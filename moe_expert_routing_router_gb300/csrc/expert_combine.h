@@ -16,7 +16,7 @@ struct CombineRowsParams {
   const float* gate;      // [T, k] or null (all ones)
   void* out;              // [T, H]
 };
-cudaError_t launch_expert_combine(const CombineRowsParams& p, bool bf16, cudaStream_t stream);
+cudaError_t launch_expert_combine(const CombineRowsParams& p, bool bf16, int sms, cudaStream_t stream);
 
 struct CombineRowsBwdParams {
   const void* dout;       // [T, H]
@@ -30,6 +30,6 @@ struct CombineRowsBwdParams {
   void* dy;               // [M, H]: rows of kept assignments
   float* dgate;           // [T, k]
 };
-cudaError_t launch_expert_combine_bwd(const CombineRowsBwdParams& p, bool bf16, cudaStream_t stream);
+cudaError_t launch_expert_combine_bwd(const CombineRowsBwdParams& p, bool bf16, int sms, cudaStream_t stream);
 
 }  // namespace moe

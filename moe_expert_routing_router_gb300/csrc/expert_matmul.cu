@@ -7,9 +7,9 @@
 // over all blocks.  The scales may be any fp32 numbers, and no sum is kept in
 // fewer than 32 bits.
 //
-// One persistent CTA per SM, 20 warps: a TMA producer (one thread), an MMA
-// issuer (one thread), two spare warps, and 16 epilogue warps of 32 rows by a
-// quarter of the tile's columns.  Shared memory is a ring of operand stages
+// One persistent CTA per SM, 12 warps: a TMA producer (one thread), an MMA
+// issuer (one thread), two spare warps, and 8 epilogue warps of 32 rows by half
+// of the tile's columns.  Shared memory is a ring of operand stages
 // (one block of 128 of both operands, 128-byte swizzled); tensor memory is a
 // ring of block products, so that the tensor core forms block b + 1 while the
 // epilogue adds block b, and runs ahead into the next tile while a tile is
@@ -27,7 +27,7 @@ namespace {
 constexpr int kBM = 128;                      // rows of a tile
 constexpr int kBK = 128;                      // block along the contraction: bytes of e4m3, and one scale
 constexpr int kBoxA = 32, kBoxB = 64;         // rows of one copy: a ragged tile copies only the boxes that it needs
-constexpr int kEpiWarps = 16, kFirstEpi = 4;
+constexpr int kEpiWarps = 8, kFirstEpi = 4;
 constexpr int kMmThreads = (kFirstEpi + kEpiWarps) * kWarp;
 constexpr int kTmemCols = 512;
 constexpr int kMaxE = 1024;
@@ -73,18 +73,46 @@ __device__ __forceinline__ uint64_t smem_desc(const void* p) {
          uint64_t(2) << 61;
 }
 
-// 16 columns of the warp's 32 rows; the values are there when it returns (the
+// 32 columns of the warp's 32 rows; the values are there when it returns (the
 // wait is in the same statement, so no use of them can be moved before it).
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float* v) {
-  uint32_t r[16];
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
+  uint32_t r[32];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+      "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+      "}, [%32];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr) : "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Lane l of each NP neighbouring lanes holds the NP pieces of row l in v; after
+// it, v[r] is piece l of row r.  Rows are then stored NP * 16 bytes at a time
+// instead of 16: a store of 32 rows takes a cycle a row.
+template <int NP>
+__device__ __forceinline__ void turn(uint4* v, int lane) {
+#pragma unroll
+  for (int s = 1; s < NP; s <<= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if (i & s) continue;
+      uint4 x = up ? v[i] : v[i | s];
+      x.x = __shfl_xor_sync(kFull, x.x, s);
+      x.y = __shfl_xor_sync(kFull, x.y, s);
+      x.z = __shfl_xor_sync(kFull, x.z, s);
+      x.w = __shfl_xor_sync(kFull, x.w, s);
+      if (up) v[i] = x;
+      else v[i | s] = x;
+    }
+  }
 }
 
 // ---- the kernel ----------------------------------------------------------------
@@ -93,7 +121,7 @@ struct Tile {
   static constexpr int kStageBytes = (kBM + BN) * kBK;
   static constexpr int kStages = 196608 / kStageBytes;         // 192 KB of operands
   static constexpr int kBufs = kTmemCols / BN;                 // block products in tensor memory
-  static constexpr int kCols = BN / 4;                         // columns of one epilogue warp
+  static constexpr int kCols = BN / 2;                         // columns of one epilogue warp
 };
 
 struct alignas(16) Shared {
@@ -102,12 +130,13 @@ struct alignas(16) Shared {
   int abort;
   int first[kMaxE + 1];                                        // tiles before expert e
   int block[kMaxE + 1];                                        // weight gradient: column blocks before expert e
-  alignas(16) float bscale[kEpiWarps][2][64];                  // weight gradient: a block's column scales, per warp
+  alignas(16) float bscale[kEpiWarps][2][128];                 // weight gradient: a block's column scales, per warp
 };
 
 // Bounded wait that every role uses: false once it, or another role's, ran out.
+// The clock is read only after a first suspended wait of 20 us has failed.
 __device__ __forceinline__ bool mm_wait(Shared& sh, const MatmulParams& p, uint64_t* bar, uint32_t parity) {
-  if (mbar_test(bar, parity)) return true;
+  if (mbar_test_suspend(bar, parity, 20000u)) return true;
   const uint64_t t0 = global_ns();
   while (!mbar_test_suspend(bar, parity, 20000u)) {
     if (*reinterpret_cast<volatile int*>(&sh.abort) != 0) return false;
@@ -240,79 +269,86 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
   const int n_tiles = sh.abort != 0 ? 0 : sh.first[p.E];
   __syncthreads();                                               // every thread has seen abort before a role sets it
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ---- producer: one stage per block ----
-      int s = 0, issued = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      Walk w;
-      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
-        w.at<BN, WGRAD>(p, sh, tile);
-        const int na = (w.rows + kBoxA - 1) / kBoxA, nb = (w.cols + kBoxB - 1) / kBoxB;
-        const int b_row = WGRAD ? w.col0 : w.e * p.C + w.col0;
-        for (int b = 0; b < w.blocks; ++b) {
-          if (!(ok = mm_wait(sh, p, &sh.empty[s], phase ^ 1u))) break;
-          uint8_t* sa = ring + s * TL::kStageBytes;
-          uint8_t* sb = sa + kBM * kBK;
-          mbar_arrive_expect_tx(&sh.full[s], uint32_t(na * kBoxA + nb * kBoxB) * kBK);
-          const int x = (w.block0 + b) * kBK;
-          for (int i = 0; i < na; ++i) tma_2d(sa + i * kBoxA * kBK, &map_a, x, w.row0 + i * kBoxA, &sh.full[s]);
-          for (int i = 0; i < nb; ++i) tma_2d(sb + i * kBoxB * kBK, &map_b, x, b_row + i * kBoxB, &sh.full[s]);
-          ++issued;
-          if (++s == TL::kStages) {
-            s = 0;
-            phase ^= 1u;
+  // The epilogue's sums want more registers than an even split gives: of the
+  // launch's 384 x 168, the first four warps keep 56 a thread and the others take 224.
+  static_assert(kFirstEpi * 56 + kEpiWarps * 224 <= (kFirstEpi + kEpiWarps) * 168, "registers of the launch");
+  if (warp < kFirstEpi) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      if (lane == 0) {
+        // ---- producer: one stage per block ----
+        int s = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        Walk w;
+        for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
+          w.at<BN, WGRAD>(p, sh, tile);
+          const int na = (w.rows + kBoxA - 1) / kBoxA, nb = (w.cols + kBoxB - 1) / kBoxB;
+          const int b_row = WGRAD ? w.col0 : w.e * p.C + w.col0;
+          for (int b = 0; b < w.blocks; ++b) {
+            if (!(ok = mm_wait(sh, p, &sh.empty[s], phase ^ 1u))) break;
+            uint8_t* sa = ring + s * TL::kStageBytes;
+            uint8_t* sb = sa + kBM * kBK;
+            mbar_arrive_expect_tx(&sh.full[s], uint32_t(na * kBoxA + nb * kBoxB) * kBK);
+            const int x = (w.block0 + b) * kBK;
+            for (int i = 0; i < na; ++i) tma_2d(sa + i * kBoxA * kBK, &map_a, x, w.row0 + i * kBoxA, &sh.full[s]);
+            for (int i = 0; i < nb; ++i) tma_2d(sb + i * kBoxB * kBK, &map_b, x, b_row + i * kBoxB, &sh.full[s]);
+            ++issued;
+            if (++s == TL::kStages) {
+              s = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        if (!ok) {                                                 // copies in flight land before shared memory goes
+          for (int i = 0; i < TL::kStages && i < issued; ++i) {
+            const int back = issued - 1 - i;
+            mbar_wait(&sh.full[back % TL::kStages], uint32_t(back / TL::kStages) & 1u, p.timeout_ns);
           }
         }
       }
-      if (!ok) {                                                 // copies in flight land before shared memory goes
-        for (int i = 0; i < TL::kStages && i < issued; ++i) {
-          const int back = issued - 1 - i;
-          mbar_wait(&sh.full[back % TL::kStages], uint32_t(back / TL::kStages) & 1u, p.timeout_ns);
-        }
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      // ---- MMA issuer ----
-      // D fp32, A and B e4m3, both K-major, N = BN, M = 128
-      constexpr uint32_t idesc = (1u << 4) | uint32_t(BN / 8) << 17 | uint32_t(kBM / 16) << 24;
-      int s = 0, t = 0;
-      uint32_t phase = 0, tphase = 0;
-      bool ok = true;
-      Walk w;
-      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
-        w.at<BN, WGRAD>(p, sh, tile);
-        for (int b = 0; b < w.blocks; ++b) {
-          if (!(ok = mm_wait(sh, p, &sh.tempty[t], tphase ^ 1u) && mm_wait(sh, p, &sh.full[s], phase))) break;
-          tc_fence_after();
-          const uint64_t da = smem_desc(ring + s * TL::kStageBytes), db = smem_desc(ring + s * TL::kStageBytes + kBM * kBK);
+    } else if (warp == 1) {
+      if (lane == 0) {
+        // ---- MMA issuer ----
+        // D fp32, A and B e4m3, both K-major, N = BN, M = 128
+        constexpr uint32_t idesc = (1u << 4) | uint32_t(BN / 8) << 17 | uint32_t(kBM / 16) << 24;
+        int s = 0, t = 0;
+        uint32_t phase = 0, tphase = 0;
+        bool ok = true;
+        Walk w;
+        for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
+          w.at<BN, WGRAD>(p, sh, tile);
+          for (int b = 0; b < w.blocks; ++b) {
+            if (!(ok = mm_wait(sh, p, &sh.tempty[t], tphase ^ 1u) && mm_wait(sh, p, &sh.full[s], phase))) break;
+            tc_fence_after();
+            const uint64_t da = smem_desc(ring + s * TL::kStageBytes), db = smem_desc(ring + s * TL::kStageBytes + kBM * kBK);
 #pragma unroll
-          for (int k = 0; k < kBK / 32; ++k)                     // 32 bytes along the row: 2 units of 16
-            tc_mma_f8(tmem + t * BN, da + k * 2, db + k * 2, idesc, k > 0);
-          tc_commit(&sh.empty[s]);
-          tc_commit(&sh.tfull[t]);
-          if (++s == TL::kStages) {
-            s = 0;
-            phase ^= 1u;
-          }
-          if (++t == TL::kBufs) {
-            t = 0;
-            tphase ^= 1u;
+            for (int k = 0; k < kBK / 32; ++k)                     // 32 bytes along the row: 2 units of 16
+              tc_mma_f8(tmem + t * BN, da + k * 2, db + k * 2, idesc, k > 0);
+            tc_commit(&sh.empty[s]);
+            tc_commit(&sh.tfull[t]);
+            if (++s == TL::kStages) {
+              s = 0;
+              phase ^= 1u;
+            }
+            if (++t == TL::kBufs) {
+              t = 0;
+              tphase ^= 1u;
+            }
           }
         }
-      }
-      if (!ok) {                                                 // products in flight end before tensor memory goes
-        tc_commit(&sh.drain);
-        mbar_wait(&sh.drain, 0, p.timeout_ns);
+        if (!ok) {                                                 // products in flight end before tensor memory goes
+          tc_commit(&sh.drain);
+          mbar_wait(&sh.drain, 0, p.timeout_ns);
+        }
       }
     }
-  } else if (warp >= kFirstEpi) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // ---- epilogue: rows 32 * quad + lane, kCols columns ----
     constexpr int CW = TL::kCols;
     const int quad = warp % 4, cg = (warp - kFirstEpi) / 4, row = quad * 32 + lane;
-    float(*s_bs)[64] = sh.bscale[warp - kFirstEpi];
+    float(*s_bs)[128] = sh.bscale[warp - kFirstEpi];
     const int kblocks = (p.K + kBK - 1) / kBK, cblocks = (p.C + kBK - 1) / kBK;
     int t = 0;
     uint32_t tphase = 0;
@@ -331,7 +367,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       int64_t step_a = 0, step_b = 0;
       if constexpr (WGRAD) {
         pa = p.a_scale + int64_t(w.block0) * p.R + w.r0 + row;
-        pb = p.b_scale + int64_t(w.block0) * p.C + c0 + lane;
+        pb = p.b_scale + int64_t(w.block0) * p.C + c0 + lane * 4;
         step_a = p.R;
         step_b = p.C;
       } else {
@@ -340,14 +376,14 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
         step_a = p.M;
         step_b = 1;
       }
-      const bool lo_col = c0 + lane < p.C && lane < CW, hi_col = CW > 32 && c0 + 32 + lane < p.C;
-      float sa = 0.f, sb = 0.f, sb_hi = 0.f;
+      const bool col = lane * 4 < CW && c0 + lane * 4 < p.C;     // weight gradient: a lane's four column scales
+      float sa = 0.f, sb = 0.f;
+      float4 sb4 = make_float4(0.f, 0.f, 0.f, 0.f);
       const auto fetch = [&]() {
         if (busy) {
           sa = live ? *pa : 0.f;
           if constexpr (WGRAD) {
-            sb = lo_col ? *pb : 0.f;
-            sb_hi = hi_col ? pb[32] : 0.f;
+            if (col) sb4 = *reinterpret_cast<const float4*>(pb);
           } else {
             sb = *pb;
           }
@@ -359,8 +395,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       for (int b = 0; b < w.blocks; ++b) {
         const float ra = sa, rb = sb;
         if constexpr (WGRAD) {
-          if (lane < CW) s_bs[b & 1][lane] = sb;
-          if constexpr (CW > 32) s_bs[b & 1][32 + lane] = sb_hi;
+          *reinterpret_cast<float4*>(&s_bs[b & 1][lane * 4]) = sb4;
           __syncwarp();
         }
         if (b + 1 < w.blocks) fetch();
@@ -371,11 +406,11 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
           const uint32_t addr = tmem + t * BN + cg * CW + (uint32_t(quad * 32) << 16);
           const float2 s2 = WGRAD ? make_float2(ra, ra) : make_float2(ra * rb, ra * rb);
 #pragma unroll
-          for (int c = 0; c < CW; c += 16) {
-            float v[16];
-            tmem_ld16(addr + c, v);
+          for (int c = 0; c < CW; c += 32) {
+            float v[32];
+            tmem_ld32(addr + c, v);
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
+            for (int i = 0; i < 32; i += 4) {
               float2 x = make_float2(v[i], v[i + 1]), y = make_float2(v[i + 2], v[i + 3]);
               if constexpr (WGRAD) {
                 const float4 q = *reinterpret_cast<const float4*>(&s_bs[b & 1][c + i]);
@@ -396,27 +431,35 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
           tphase ^= 1u;
         }
       }
-      if (!ok || !busy || !live) continue;
-      const int64_t out_row = WGRAD ? int64_t(w.e) * p.R + w.r0 + row : int64_t(w.row0) + row;
-      const int64_t at = out_row * p.C + c0;
+      if (!ok || !busy) continue;
+      // Pieces of 16 bytes, NP of which are turned among NP lanes at a time.
+      constexpr int kPer = BF16 ? 8 : 4, NP = CW / kPer < 8 ? CW / kPer : 8;
+      const int64_t out_row = WGRAD ? int64_t(w.e) * p.R + w.r0 : int64_t(w.row0);
 #pragma unroll
-      for (int c = 0; c < CW; c += 8) {
-        if (c0 + c < p.C) {                                      // C is a multiple of 16: eight columns are whole
-          const float2* a = &acc[c / 2];
+      for (int h = 0; h < CW; h += NP * kPer) {
+        uint4 v[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const float2* a = &acc[(h + i * kPer) / 2];
           if constexpr (BF16) {
-            uint4 u;
-            uint32_t* h = &u.x;
+            uint32_t b2[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(a[i].x, a[i].y);
-              h[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 q = __floats2bfloat162_rn(a[j].x, a[j].y);
+              b2[j] = *reinterpret_cast<const uint32_t*>(&q);
             }
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + c) = u;
+            v[i] = make_uint4(b2[0], b2[1], b2[2], b2[3]);
           } else {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at + c);
-            o[0] = make_float4(a[0].x, a[0].y, a[1].x, a[1].y);
-            o[1] = make_float4(a[2].x, a[2].y, a[3].x, a[3].y);
+            v[i] = make_uint4(__float_as_uint(a[0].x), __float_as_uint(a[0].y), __float_as_uint(a[1].x), __float_as_uint(a[1].y));
           }
+        }
+        turn<NP>(v, lane);
+        const int c = c0 + h + lane % NP * kPer;                 // C is a multiple of 16: a piece is whole
+#pragma unroll
+        for (int r = 0; r < NP; ++r) {
+          const int to = quad * 32 + lane / NP * NP + r;
+          if (to < w.rows && c < p.C)
+            *reinterpret_cast<uint4*>(static_cast<char*>(p.out) + ((out_row + to) * p.C + c) * (BF16 ? 2 : 4)) = v[r];
         }
       }
     }

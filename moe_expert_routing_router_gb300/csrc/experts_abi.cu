@@ -165,7 +165,7 @@ moe_status moe_quantize_cols(const void* x, moe_dtype dt, int64_t rows, int64_t 
       (s = check_experts(E)) != MOE_OK)
     return s;
   if (!x || !offsets || !q || !scale) return fail(MOE_ERR_INVALID, "an argument is NULL");
-  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 8)) return fail(MOE_ERR_INVALID, "x, q (16 bytes) or scale (8 bytes) is misaligned");
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 16)) return fail(MOE_ERR_INVALID, "x, q or scale is not 16-byte aligned");
   if (!aligned(offsets, 4) || !aligned(kept, 4)) return fail(MOE_ERR_INVALID, "offsets or kept is not 4-byte aligned");
   moe::QuantColsParams p = {x, rows, M, K, k, E, offsets, kept, perm, moe_quantize_cols_width(M, E), static_cast<uint8_t*>(q), scale};
   if (p.width >= kInt32Limit) return fail(MOE_ERR_INVALID, "M = %lld over E = %d experts is too wide", (long long)M, E);
@@ -236,7 +236,8 @@ moe_status moe_expert_wgrad(const void* dyq, const float* dyscale, const void* x
     return fail(MOE_ERR_INVALID, "width = %lld must be a multiple of 128 in [128, 2^31)", (long long)width);
   if (!dyq || !dyscale || !xq || !xscale || !kept || !dw) return fail(MOE_ERR_INVALID, "an argument is NULL");
   if (!aligned(dyq, 16) || !aligned(xq, 16) || !aligned(dw, 16)) return fail(MOE_ERR_INVALID, "dyq, xq or dw is not 16-byte aligned");
-  if (!aligned(dyscale, 4) || !aligned(xscale, 4) || !aligned(kept, 4)) return fail(MOE_ERR_INVALID, "an array is not 4-byte aligned");
+  if (!aligned(xscale, 16) || !aligned(dyscale, 4) || !aligned(kept, 4))
+    return fail(MOE_ERR_INVALID, "xscale (16 bytes), dyscale or kept (4 bytes) is misaligned");
   if (int64_t(E) * ((N + 127) / 128) * ((K + 127) / 128) >= kInt32Limit) return fail(MOE_ERR_INVALID, "E x N x K is too large");
   int sms = 0;
   if ((s = moe::abi_sms(&sms)) != MOE_OK) return s;
@@ -281,8 +282,10 @@ moe_status moe_expert_combine(const void* y, moe_dtype dt, int64_t M, int32_t H,
   const size_t esize = dt == MOE_DTYPE_BF16 ? 2 : 4;
   if (!aligned(y, esize) || !aligned(out, esize) || !aligned(idx, 4) || !aligned(slot, 4) || !aligned(offsets, 4) || !aligned(gate, 4))
     return fail(MOE_ERR_INVALID, "an array is not element aligned");
+  int sms = 0;
+  if ((s = moe::abi_sms(&sms)) != MOE_OK) return s;
   moe::CombineRowsParams p = {y, T, M, H, k, E, idx, slot, offsets, gate, out};
-  return launched(moe::launch_expert_combine(p, dt == MOE_DTYPE_BF16, stream), "moe_expert_combine launch");
+  return launched(moe::launch_expert_combine(p, dt == MOE_DTYPE_BF16, sms, stream), "moe_expert_combine launch");
 }
 
 moe_status moe_expert_combine_bwd(const void* dout, const void* y, moe_dtype dt, int64_t M, int32_t H, int64_t T,
@@ -299,8 +302,10 @@ moe_status moe_expert_combine_bwd(const void* dout, const void* y, moe_dtype dt,
   if (!aligned(dout, esize) || !aligned(y, esize) || !aligned(dy, esize) || !aligned(idx, 4) || !aligned(slot, 4) ||
       !aligned(offsets, 4) || !aligned(gate, 4) || !aligned(dgate, 4))
     return fail(MOE_ERR_INVALID, "an array is not element aligned");
+  int sms = 0;
+  if ((s = moe::abi_sms(&sms)) != MOE_OK) return s;
   moe::CombineRowsBwdParams p = {dout, y, T, M, H, k, E, idx, slot, offsets, gate, dy, dgate};
-  return launched(moe::launch_expert_combine_bwd(p, dt == MOE_DTYPE_BF16, stream), "moe_expert_combine_bwd launch");
+  return launched(moe::launch_expert_combine_bwd(p, dt == MOE_DTYPE_BF16, sms, stream), "moe_expert_combine_bwd launch");
 }
 
 }  // extern "C"

@@ -34,7 +34,7 @@ __device__ __forceinline__ Pow2Scale pow2_scale(float amax) {
   return {__uint_as_float(uint32_t(n + 127) << 23), __uint_as_float(uint32_t(127 - n) << 23)};
 }
 
-// max of |x| that keeps a NaN (its bits are above those of every number).
+// bits of |x|, in the order of |x|, that keep a NaN (its bits are above those of every number).
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
@@ -44,27 +44,44 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
   return uint32_t(lo) | uint32_t(hi) << 16;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void load8(const void* x, int64_t at, float* v) {
-  if constexpr (BF16) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + at);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 a = s[0], b = s[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-}
+// N neighbouring values, kept as they were loaded (bf16: two in a register).
+template <bool BF16, int N>
+struct Values {
+  static constexpr int kWords = BF16 ? N / 2 : N;
+  uint32_t w[kWords];
 
-__device__ __forceinline__ int64_t source_row(const int32_t* perm, int k, int64_t r, int64_t rows) {
-  const int64_t a = perm != nullptr ? perm[r] : r * k;
-  return a >= 0 && a / k < rows ? a / k : -1;    // an index outside x: a row of zeros
+  __device__ __forceinline__ void load(const void* x, int64_t at) {
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(static_cast<const char*>(x) + at * (BF16 ? 2 : 4));
+    if constexpr (kWords % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(s + i);
+        w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(s + i);
+        w[i] = u.x; w[i + 1] = u.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (BF16) return __uint_as_float(i % 2 == 0 ? w[i / 2] << 16 : w[i / 2] & 0xffff0000u);
+    else return __uint_as_float(w[i]);
+  }
+};
+
+// The row of x that row r of the output holds, or -1: zeros.  All rows fit int32.
+__device__ __forceinline__ int source_row(const int32_t* perm, int k, int64_t r, int64_t rows) {
+  if (perm == nullptr) return int(r);
+  const int a = perm[r];
+  const uint32_t t = uint32_t(a) / uint32_t(k);
+  return a >= 0 && t < uint64_t(rows) ? int(t) : -1;
 }
 
 // ---------------------------------------------------------------------------
@@ -77,37 +94,36 @@ constexpr int kRowsTile = 32, kRowsBlocks = 4, kQuantThreads = 256;
 template <bool BF16>
 __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const QuantRowsParams p) {
   __shared__ float s_scale[kRowsBlocks][kRowsTile];
+  __shared__ int s_row[kRowsTile];
   const int64_t r0 = int64_t(blockIdx.x) * kRowsTile;
+  if (threadIdx.x < kRowsTile)
+    s_row[threadIdx.x] = r0 + threadIdx.x < p.M ? source_row(p.perm, p.k, r0 + threadIdx.x, p.rows) : -1;
+  __syncthreads();
   const int half = threadIdx.x / 16, hl = threadIdx.x % 16;      // 16 half warps
   const int kb = blockIdx.y * kRowsBlocks + half % kRowsBlocks;
   const int col = kb * kScaleBlock + hl * 8;
   constexpr int kIter = kRowsTile * kRowsBlocks / (kQuantThreads / 16);
-  float v[kIter][8];
+  Values<BF16, 8> v[kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    const int64_t r = r0 + i * (kRowsTile / kIter) + half / kRowsBlocks;
-    const int64_t t = r < p.M && col < p.K ? source_row(p.perm, p.k, r, p.rows) : -1;
-    if (t >= 0) {
-      load8<BF16>(p.x, t * p.K + col, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    }
+    const int t = s_row[i * (kRowsTile / kIter) + half / kRowsBlocks];
+    if (t >= 0 && col < p.K) v[i].load(p.x, int64_t(t) * p.K + col);
+    else v[i].zero();
   }
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
     const int row = i * (kRowsTile / kIter) + half / kRowsBlocks;
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
+    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i].get(j)));
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(kFull, m, off));
     const Pow2Scale s = pow2_scale(__uint_as_float(m));
     if (hl == 0) s_scale[half % kRowsBlocks][row] = s.scale;
     if (r0 + row < p.M && col < p.K) {
       uint2 o;
-      o.x = pack4(v[i][0] * s.inv, v[i][1] * s.inv, v[i][2] * s.inv, v[i][3] * s.inv);
-      o.y = pack4(v[i][4] * s.inv, v[i][5] * s.inv, v[i][6] * s.inv, v[i][7] * s.inv);
+      o.x = pack4(v[i].get(0) * s.inv, v[i].get(1) * s.inv, v[i].get(2) * s.inv, v[i].get(3) * s.inv);
+      o.y = pack4(v[i].get(4) * s.inv, v[i].get(5) * s.inv, v[i].get(6) * s.inv, v[i].get(7) * s.inv);
       *reinterpret_cast<uint2*>(p.q + (r0 + row) * p.K + col) = o;
     }
   }
@@ -123,16 +139,17 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const Quan
 // Columns: blocks of 128 rows of one expert by one column, written transposed
 // (the rows become the contraction of a weight gradient).  Expert e's rows
 // start at column 128 * (sum over e' < e of ceil(kept[e'] / 128)); its last
-// block ends in zeros.  A CTA takes one block of rows by 64 columns: a thread
-// holds 2 columns of 16 rows, the maxima meet in shared memory, and the bytes
+// block ends in zeros.  A CTA takes one block of rows by 128 columns: a thread
+// holds 4 columns of 16 rows, the maxima meet in shared memory, and the bytes
 // turn through shared memory into rows of 128.
 // ---------------------------------------------------------------------------
-constexpr int kColsTile = 64, kColsWarps = kQuantThreads / kWarp, kColsRows = kScaleBlock / kColsWarps;
+constexpr int kColsTile = 128, kColsLane = kColsTile / kWarp, kColsWarps = kQuantThreads / kWarp, kColsRows = kScaleBlock / kColsWarps;
 
 template <bool BF16>
 __global__ void __launch_bounds__(kQuantThreads) quantize_cols_kernel(const QuantColsParams p) {
   __shared__ int s_where[3];                                     // first row, rows, found
-  __shared__ uint32_t s_max[kColsWarps][kColsTile];
+  __shared__ int s_row[kScaleBlock];
+  __shared__ __align__(16) uint32_t s_max[kColsWarps][kColsTile];
   __shared__ __align__(16) uint8_t s_q[kColsTile][kScaleBlock + 16];
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   const int64_t blk = blockIdx.x;
@@ -168,52 +185,42 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_cols_kernel(const Quan
   }
   __syncthreads();
   if (s_where[2] == 0) return;                                   // behind the last expert: left as it is
-  const int64_t r0 = s_where[0];
-  const int n = s_where[1];
-  const int col = blockIdx.y * kColsTile + lane * 2;
-  float v[kColsRows][2];
+  if (threadIdx.x < kScaleBlock)
+    s_row[threadIdx.x] = threadIdx.x < s_where[1] ? source_row(p.perm, p.k, int64_t(s_where[0]) + threadIdx.x, p.rows) : -1;
+  __syncthreads();
+  const int col = blockIdx.y * kColsTile + lane * kColsLane;
+  Values<BF16, kColsLane> v[kColsRows];
 #pragma unroll
   for (int i = 0; i < kColsRows; ++i) {
-    const int r = warp * kColsRows + i;
-    v[i][0] = v[i][1] = 0.f;
-    const int64_t t = r < n && col < p.K ? source_row(p.perm, p.k, r0 + r, p.rows) : -1;
-    if (t >= 0) {
-      if constexpr (BF16) {
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.x) + t * p.K + col);
-        v[i][0] = __uint_as_float(u << 16);
-        v[i][1] = __uint_as_float(u & 0xffff0000u);
-      } else {
-        const float2 u = *reinterpret_cast<const float2*>(static_cast<const float*>(p.x) + t * p.K + col);
-        v[i][0] = u.x;
-        v[i][1] = u.y;
-      }
-    }
+    const int t = s_row[warp * kColsRows + i];
+    if (t >= 0 && col < p.K) v[i].load(p.x, int64_t(t) * p.K + col);
+    else v[i].zero();
   }
-  uint32_t m0 = 0, m1 = 0;
+  uint32_t m[kColsLane] = {};
 #pragma unroll
-  for (int i = 0; i < kColsRows; ++i) {
-    m0 = max(m0, abs_bits(v[i][0]));
-    m1 = max(m1, abs_bits(v[i][1]));
-  }
-  s_max[warp][lane * 2] = m0;
-  s_max[warp][lane * 2 + 1] = m1;
+  for (int i = 0; i < kColsRows; ++i)
+#pragma unroll
+    for (int j = 0; j < kColsLane; ++j) m[j] = max(m[j], abs_bits(v[i].get(j)));
+  *reinterpret_cast<uint4*>(&s_max[warp][lane * kColsLane]) = make_uint4(m[0], m[1], m[2], m[3]);
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kColsWarps; ++w) {
-    m0 = max(m0, s_max[w][lane * 2]);
-    m1 = max(m1, s_max[w][lane * 2 + 1]);
+    const uint4 o = *reinterpret_cast<const uint4*>(&s_max[w][lane * kColsLane]);
+    m[0] = max(m[0], o.x); m[1] = max(m[1], o.y); m[2] = max(m[2], o.z); m[3] = max(m[3], o.w);
   }
-  const Pow2Scale a = pow2_scale(__uint_as_float(m0)), b = pow2_scale(__uint_as_float(m1));
-  if (warp == 0 && col < p.K)
-    *reinterpret_cast<float2*>(p.scale + blk * p.K + col) = make_float2(a.scale, b.scale);
-  uint32_t o0[kColsRows / 4], o1[kColsRows / 4];
+  Pow2Scale s[kColsLane];
 #pragma unroll
-  for (int i = 0; i < kColsRows / 4; ++i) {
-    o0[i] = pack4(v[4 * i][0] * a.inv, v[4 * i + 1][0] * a.inv, v[4 * i + 2][0] * a.inv, v[4 * i + 3][0] * a.inv);
-    o1[i] = pack4(v[4 * i][1] * b.inv, v[4 * i + 1][1] * b.inv, v[4 * i + 2][1] * b.inv, v[4 * i + 3][1] * b.inv);
+  for (int j = 0; j < kColsLane; ++j) s[j] = pow2_scale(__uint_as_float(m[j]));
+  if (warp == 0 && col < p.K)
+    *reinterpret_cast<float4*>(p.scale + blk * p.K + col) = make_float4(s[0].scale, s[1].scale, s[2].scale, s[3].scale);
+#pragma unroll
+  for (int j = 0; j < kColsLane; ++j) {
+    uint32_t o[kColsRows / 4];
+#pragma unroll
+    for (int i = 0; i < kColsRows / 4; ++i)
+      o[i] = pack4(v[4 * i].get(j) * s[j].inv, v[4 * i + 1].get(j) * s[j].inv, v[4 * i + 2].get(j) * s[j].inv, v[4 * i + 3].get(j) * s[j].inv);
+    *reinterpret_cast<uint4*>(&s_q[lane * kColsLane + j][warp * kColsRows]) = make_uint4(o[0], o[1], o[2], o[3]);
   }
-  *reinterpret_cast<uint4*>(&s_q[lane * 2][warp * kColsRows]) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-  *reinterpret_cast<uint4*>(&s_q[lane * 2 + 1][warp * kColsRows]) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
   __syncthreads();
   for (int i = threadIdx.x; i < kColsTile * (kScaleBlock / 16); i += kQuantThreads) {
     const int c = i / (kScaleBlock / 16), part = i % (kScaleBlock / 16);
@@ -238,20 +245,18 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_weights_kernel(const Q
   const int tr = threadIdx.x / 16, tc = threadIdx.x % 16 * 8;
   const int col = kb * kScaleBlock + tc;
   const int64_t matrix = int64_t(e) * p.N * p.K;
-  float v[8][8];
+  Values<BF16, 8> v[8];
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = nb * kScaleBlock + i * 16 + tr;
-    if (row < p.N && col < p.K) {
-      load8<BF16>(p.w, matrix + int64_t(row) * p.K + col, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
+    if (row < p.N && col < p.K) v[i].load(p.w, matrix + int64_t(row) * p.K + col);
+    else v[i].zero();
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i].get(j)));
   m = __reduce_max_sync(kFull, m);
   if (lane == 0) s_max[warp] = m;
   __syncthreads();
@@ -267,8 +272,8 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_weights_kernel(const Q
   for (int i = 0; i < 8; ++i) {
     const int row = nb * kScaleBlock + i * 16 + tr;
     uint2 o;
-    o.x = pack4(v[i][0] * s.inv, v[i][1] * s.inv, v[i][2] * s.inv, v[i][3] * s.inv);
-    o.y = pack4(v[i][4] * s.inv, v[i][5] * s.inv, v[i][6] * s.inv, v[i][7] * s.inv);
+    o.x = pack4(v[i].get(0) * s.inv, v[i].get(1) * s.inv, v[i].get(2) * s.inv, v[i].get(3) * s.inv);
+    o.y = pack4(v[i].get(4) * s.inv, v[i].get(5) * s.inv, v[i].get(6) * s.inv, v[i].get(7) * s.inv);
     if (p.q != nullptr && row < p.N && col < p.K)
       *reinterpret_cast<uint2*>(p.q + matrix + int64_t(row) * p.K + col) = o;
     if (p.qt != nullptr) {

@@ -14,9 +14,9 @@
 // Picks are integers, decided by comparing sums of exponentials.  The fast path
 // compares them in fp32 and bounds what its rounding can have changed: where
 // two values that decide a pick are nearer than that bound (and not equal
-// because their inputs are), the warp ranks its row again in double.  A row
-// takes that path about once in some hundred, so the picks are those of the
-// double-precision definition at fp32 cost.
+// because their inputs are), the warp ranks them again in double.  That is a row
+// in some hundred, so the picks are those of the double-precision definition at
+// fp32 cost.
 #include "device_common.cuh"
 #include "route.h"
 
@@ -60,14 +60,53 @@ __device__ __forceinline__ float sigmoid_exact(float z) {
   return (z >= 0.f ? 1.f : t) / (1.f + t);
 }
 
-// The picks' scores up to a common factor, so that renormalised gates keep
-// their digits where the scores themselves underflow.  Lane j < k holds pick j.
+// Eight neighbouring lanes hold the picks of one row, so that a warp finishes
+// four rows at once; reductions over them.
+constexpr int kPickLanes = 8;
+__device__ __forceinline__ float pick_max(float x) {
+#pragma unroll
+  for (int off = kPickLanes / 2; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, off));
+  return x;
+}
+__device__ __forceinline__ float pick_value(float x, int j) { return __shfl_sync(kFull, x, j, kPickLanes); }
+
+// The picks' scores up to a common factor of the row, so that renormalised
+// gates keep their digits where the scores themselves underflow.
 __device__ __forceinline__ float pick_weight(float z, bool live, int softmax) {
-  const float m = warp_max_f(live ? z : neg_inf());
+  const float m = pick_max(live ? z : neg_inf());
   if (!live || !(z > neg_inf())) return 0.f;                    // masked or not a number: no weight
   if (softmax) return expf(z - m);
   if (m >= 0.f) return sigmoid_exact(z);
   return expf(z - m) / (1.f + expf(z));                         // every pick's sigmoid times exp(-m)
+}
+// Its share of the row's sum (0 where nothing is left).
+__device__ __forceinline__ float pick_share(float w, int k) {
+  float sum = 0.f;
+  for (int j = 0; j < k; ++j) sum += pick_value(w, j);
+  return sum > 0.f ? w / sum : 0.f;
+}
+
+// Descending order of NV keys: Batcher's merge exchange, unrolled.
+template <int NV>
+__device__ __forceinline__ void sort_keys(unsigned long long (&v)[NV]) {
+  constexpr int N = NV <= 4 ? 4 : NV <= 8 ? 8 : NV <= 16 ? 16 : NV <= 32 ? 32 : 64;
+#pragma unroll
+  for (int p = 1; p < N; p *= 2) {
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2) {
+#pragma unroll
+      for (int a = 0; a < NV; ++a) {
+        const int b = a + q;
+        // pairs a, a + q whose distance from q % p falls into even runs of q, inside one block of 2p
+        if (b < NV && a >= q % p && (a - q % p) / q % 2 == 0 && a / (2 * p) == b / (2 * p)) {
+          const unsigned long long x = v[a], y = v[b];
+          const bool swap = x < y;
+          v[a] = swap ? y : x;
+          v[b] = swap ? x : y;
+        }
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -150,11 +189,22 @@ __device__ __noinline__ int route_row_double(const RouteParams& p, int64_t row, 
 
 // ---------------------------------------------------------------------------
 // Forward.  NV: experts per lane, at least `chunk`; VB: bytes per load.
+//
+// A lane sorts its experts' keys (value above the inverted place, so that ties
+// stand in expert order) into shared memory; a pick is then the largest head of
+// the 32 lists (one warp reduction, the lowest lane that has it), whose lane
+// goes on to its next entry.  With a bias two more than the k picks are taken,
+// to see what hangs on rounding.  A warp selects for `per` rows one after another and then
+// computes the gates of all of them, a pick a lane.
 // ---------------------------------------------------------------------------
+constexpr int kMaxRounds = 10;                                   // 8 picks and two more
+
 template <class Elem, int NV, int VB>
-__global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
   using Raw = typename Elem::Raw;
   constexpr int kPer = VB / int(sizeof(Raw));                    // elements per load
+  constexpr int kList = NV < kMaxRounds ? NV : kMaxRounds;
+  __shared__ unsigned long long s_list[kRouteWarps][kList][kWarp];
   extern __shared__ int s_hist[];                                // [E]
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   for (int e = threadIdx.x; e < p.E; e += kRouteThreads) s_hist[e] = 0;
@@ -164,172 +214,204 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RoutePar
   const int base = g * p.gs + sub * p.chunk;
   const int n = g < p.G ? max(0, min(p.chunk, p.gs - sub * p.chunk)) : 0;
   const bool has_bias = p.bias != nullptr;
-  const bool all_scores = has_bias || (p.top2 && p.G > p.keep) || (p.softmax && !p.renorm);
   const bool grouped = p.keep < p.G;
+  const bool all_scores = has_bias || (p.top2 && grouped) || (p.softmax && !p.renorm);
+  const int rounds = has_bias ? p.k + 2 : p.k;
   float bv[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) bv[i] = has_bias && i < n ? p.bias[base + i] : 0.f;
 
-  const int64_t stride = int64_t(gridDim.x) * kRouteWarps;
-  for (int64_t row = int64_t(blockIdx.x) * kRouteWarps + warp; row < p.T; row += stride) {
-    float z[NV];
-    const Raw* src = static_cast<const Raw*>(p.logits) + row * p.E + base;
+  const int64_t stride = int64_t(gridDim.x) * kRouteWarps * per;
+  for (int64_t first = (int64_t(blockIdx.x) * kRouteWarps + warp) * per; first < p.T; first += stride) {
+    int my_e = 0;                                                // lane 8 r + j: pick j of row first + r
+    float my_max = 0.f, my_sum = 1.f;                            // and that row's softmax
+    for (int r = 0; r < per && first + r < p.T; ++r) {
+      const int64_t row = first + r;
+      float z[NV];
+      const Raw* src = static_cast<const Raw*>(p.logits) + row * p.E + base;
 #pragma unroll
-    for (int v = 0; v < NV / kPer; ++v) {
-      alignas(16) Raw raw[kPer];
-      if (v * kPer < n) {                                        // vector loads only where every lane's n is a multiple
-        if constexpr (VB == 16) *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(src + v * kPer);
-        else if constexpr (VB == 8) *reinterpret_cast<uint2*>(raw) = *reinterpret_cast<const uint2*>(src + v * kPer);
-        else raw[0] = src[v];
-      } else {
+      for (int v = 0; v < NV / kPer; ++v) {
+        alignas(16) Raw raw[kPer];
+        if (v * kPer < n) {                                      // vector loads only where every lane's n is a multiple
+          if constexpr (VB == 16) *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(src + v * kPer);
+          else if constexpr (VB == 8) *reinterpret_cast<uint2*>(raw) = *reinterpret_cast<const uint2*>(src + v * kPer);
+          else raw[0] = src[v];
+        } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) raw[i] = Elem::kNegInf;
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float x = __uint_as_float(Elem::bits(raw[i]));
-        z[v * kPer + i] = x == x ? x : neg_inf();                // not a number: never preferred
-      }
-    }
-
-    // Scores in fp32.  Their error is within tol / 2 of the row (see below).
-    float s[NV], tol = 0.f, row_max = 0.f, row_sum = 1.f;
-    if (all_scores) {
-      if (p.softmax) {
-        float m = z[0];
-#pragma unroll
-        for (int i = 1; i < NV; ++i) m = fmaxf(m, z[i]);
-        row_max = warp_max_f(m);
-        m = row_max > neg_inf() ? row_max : 0.f;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          s[i] = ex2_approx((z[i] - m) * kLog2e);
-          sum += s[i];
+          for (int i = 0; i < kPer; ++i) raw[i] = Elem::kNegInf;
         }
-        row_sum = warp_sum_f(sum);
-        const float inv = row_sum > 0.f ? 1.f / row_sum : 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) s[i] *= inv;
-        // x e^-x <= 0.37: the rounded argument moves a score by 2^-23 * 0.37 * 1.45 of
-        // the row's largest, ex2.approx by 2^-22 of itself, the sum of at most 64
-        // values a lane and 5 steps by 69 * 2^-24 of itself: 5e-6 covers them
-        tol = 1e-5f * inv;
-      } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) s[i] = rcp_approx(1.f + ex2_approx(z[i] * -kLog2e));
-        // e = exp(-z) is off by 2^-22 + 2^-24 * 1.45 |z| of itself; s moves by
-        // s (1 - s) of that, below 2^-23, and rcp.approx and 1 + e by 2^-22 of s: 6e-7 covers them
-        tol = 1.2e-6f;
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        s[i] += bv[i];
-        if (!(z[i] > neg_inf())) s[i] = neg_inf();
-      }
-    }
-    uint32_t key[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) key[i] = i < n ? float_key((has_bias ? s[i] : z[i]) + 0.f) : 0u;
-
-    bool unsure = false;
-    if (grouped) {
-      uint32_t gkey;
-      float gtol = tol;
-      if (p.top2) {
-        float a = neg_inf(), b = neg_inf();
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const float v = i < n ? s[i] : neg_inf();
-          b = fmaxf(b, fminf(a, v));
-          a = fmaxf(a, v);
+        for (int i = 0; i < kPer; ++i) {
+          const float x = __uint_as_float(Elem::bits(raw[i]));
+          z[v * kPer + i] = x == x ? x : neg_inf();              // not a number: never preferred
         }
-        for (int off = 1; off < p.L; off <<= 1) {
-          const float a2 = __shfl_xor_sync(kFull, a, off), b2 = __shfl_xor_sync(kFull, b, off);
-          b = fmaxf(fminf(a, a2), fmaxf(b, b2));
-          a = fmaxf(a, a2);
-        }
-        gkey = g < p.G ? float_key((b > neg_inf() ? a + b : a) + 0.f) : 0u;
-        gtol = 2.f * tol;
-      } else {
-        gkey = key[0];
-#pragma unroll
-        for (int i = 1; i < NV; ++i) gkey = max(gkey, key[i]);
-        for (int off = 1; off < p.L; off <<= 1) gkey = max(gkey, __shfl_xor_sync(kFull, gkey, off));
       }
-      int rank = 0;
-      for (int o = 0; o < p.G; ++o) {
-        const uint32_t other = __shfl_sync(kFull, gkey, o * p.L);
-        rank += other > gkey || (other == gkey && o < g);
-      }
-      const bool kept = rank < p.keep;
-      if (tol > 0.f && (has_bias || p.top2)) {
-        const float lo = key_float(__reduce_min_sync(kFull, kept && g < p.G ? gkey : 0xffffffffu));
-        const float hi = key_float(__reduce_max_sync(kFull, kept || g >= p.G ? 0u : gkey));
-        unsure = lo - hi <= gtol + 4.8e-7f * fabsf(lo);          // + the sums' own roundings
-      }
-      if (!kept)
-#pragma unroll
-        for (int i = 0; i < NV; ++i) key[i] = 0u;
-    }
 
-    // The k largest keys, and the next one where a pick may hang on it.
-    uint32_t best = key[0];
+      // Scores in fp32.  Their error is within tol / 2.
+      float s[NV], tol = 0.f;
+      if (all_scores) {
+        if (p.softmax) {
+          float m = z[0];
 #pragma unroll
-    for (int i = 1; i < NV; ++i) best = max(best, key[i]);
-    uint32_t my_key = 0;
-    int my_e = 0;
-    const int rounds = has_bias ? p.k + 1 : p.k;
-    for (int j = 0; j < rounds; ++j) {
-      const uint32_t top = __reduce_max_sync(kFull, best);
-      const int src_lane = __ffs(__ballot_sync(kFull, best == top)) - 1;
-      int e = 0;
-      if (lane == src_lane) {
-        bool found = false;
-        best = 0u;
+          for (int i = 1; i < NV; ++i) m = fmaxf(m, z[i]);
+          const float row_max = warp_max_f(m);
+          m = row_max > neg_inf() ? row_max : 0.f;
+          float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          if (!found && key[i] == top) {
-            found = true;
-            e = base + i;
-            key[i] = 0u;
+          for (int i = 0; i < NV; ++i) {
+            s[i] = ex2_approx((z[i] - m) * kLog2e);
+            sum += s[i];
           }
-          best = max(best, key[i]);
+          sum = warp_sum_f(sum);
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) s[i] *= inv;
+          if (lane / kPickLanes == r) {
+            my_max = row_max;
+            my_sum = sum;
+          }
+          // x e^-x <= 0.37: the rounded argument moves a score by 2^-23 * 0.37 * 1.45 of
+          // the row's largest, ex2.approx by 2^-22 of itself, the sum of at most 64
+          // values a lane and 5 steps by 69 * 2^-24 of itself: 5e-6 covers them
+          tol = 1e-5f * inv;
+        } else {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) s[i] = rcp_approx(1.f + ex2_approx(z[i] * -kLog2e));
+          // e = exp(-z) is off by 2^-22 + 2^-24 * 1.45 |z| of itself; s moves by
+          // s (1 - s) of that, below 2^-23, and rcp.approx and 1 + e by 2^-22 of s: 6e-7 covers them
+          tol = 1.2e-6f;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s[i] = z[i] > neg_inf() ? s[i] + bv[i] : neg_inf();
+      }
+      uint32_t key[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) key[i] = i < n ? float_key((has_bias ? s[i] : z[i]) + 0.f) : 0u;
+
+      bool unsure = false;                                       // whether the choice of groups hangs on rounding
+      if (grouped) {
+        uint32_t gkey;
+        float gtol = tol;
+        if (p.top2) {
+          float a = neg_inf(), b = neg_inf();
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const float v = i < n ? s[i] : neg_inf();
+            b = fmaxf(b, fminf(a, v));
+            a = fmaxf(a, v);
+          }
+          for (int off = 1; off < p.L; off <<= 1) {
+            const float a2 = __shfl_xor_sync(kFull, a, off), b2 = __shfl_xor_sync(kFull, b, off);
+            b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+            a = fmaxf(a, a2);
+          }
+          gkey = g < p.G ? float_key((b > neg_inf() ? a + b : a) + 0.f) : 0u;
+          gtol = 2.f * tol;
+        } else {
+          gkey = key[0];
+#pragma unroll
+          for (int i = 1; i < NV; ++i) gkey = max(gkey, key[i]);
+          for (int off = 1; off < p.L; off <<= 1) gkey = max(gkey, __shfl_xor_sync(kFull, gkey, off));
+        }
+        int rank = 0;
+        for (int o = 0; o < p.G; ++o) {
+          const uint32_t other = __shfl_sync(kFull, gkey, o * p.L);
+          rank += other > gkey || (other == gkey && o < g);
+        }
+        const bool kept = rank < p.keep;
+        if (has_bias || p.top2) {
+          const float lo = key_float(__reduce_min_sync(kFull, kept && g < p.G ? gkey : 0xffffffffu));
+          const float hi = key_float(__reduce_max_sync(kFull, kept || g >= p.G ? 0u : gkey));
+          unsure = lo - hi <= gtol + 4.8e-7f * fabsf(lo);        // + the sums' own roundings
+        }
+        if (!kept)
+#pragma unroll
+          for (int i = 0; i < NV; ++i) key[i] = 0u;
+      }
+
+      unsigned long long v[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = (unsigned long long)(key[i]) << 32 | uint32_t(~i);
+      sort_keys<NV>(v);
+#pragma unroll
+      for (int i = 1; i < kList; ++i) s_list[warp][i][lane] = v[i];
+      uint32_t head = uint32_t(v[0] >> 32), place = ~uint32_t(v[0]);
+      int next = 1;
+      uint32_t ck = 0;                                           // lane j: the j-th largest key and its expert
+      int ce = 0;
+      bool close = false;
+      float prev = __uint_as_float(0x7f800000u);
+      for (int j = 0; j < rounds; ++j) {
+        const uint32_t top = __reduce_max_sync(kFull, head);
+        const int from = __ffs(__ballot_sync(kFull, head == top)) - 1;
+        const int e = __shfl_sync(kFull, base + int(place), from);
+        if (lane == j) {
+          ck = top;
+          ce = e;
+        }
+        if (lane == from) {
+          const unsigned long long w = next < kList ? s_list[warp][next][lane] : 0ull;
+          head = uint32_t(w >> 32);
+          place = ~uint32_t(w);
+          ++next;
+        }
+        if (has_bias && j <= p.k) {
+          const float c = key_float(top);
+          close |= top != 0u && prev - c <= tol + 2.4e-7f * fabsf(prev);
+          prev = c;
         }
       }
-      e = __shfl_sync(kFull, e, src_lane);
-      if (lane == j) {
-        my_key = top;
-        my_e = e;
+      if (close || unsure) {
+        // Values next to one another: sure all the same where their inputs are equal.
+        const bool there = lane < rounds && ck != 0u;
+        const float zc = there ? load_logit<Elem>(p.logits, row * p.E + ce) : neg_inf();
+        const float bc = there && has_bias ? p.bias[ce] : 0.f, c = key_float(ck);
+        const float c_up = __shfl_up_sync(kFull, c, 1), z_up = __shfl_up_sync(kFull, zc, 1), b_up = __shfl_up_sync(kFull, bc, 1);
+        const bool open = close && lane >= 1 && lane <= p.k && there && c_up - c <= tol + 2.4e-7f * fabsf(c_up) &&
+                          !(zc == z_up && bc == b_up);
+        const float last = __shfl_sync(kFull, c, p.k - 1);
+        const bool beyond = lane == p.k + 1 && there && last - c <= tol + 2.4e-7f * fabsf(last);
+        const bool any_open = __any_sync(kFull, open), any_beyond = __any_sync(kFull, beyond);
+        if (unsure || (any_open && (any_beyond || p.softmax))) {
+          ce = route_row_double<Elem>(p, row, lane);
+        } else if (any_open) {
+          // The k + 1 largest are known as a set: one double-precision sigmoid a lane orders them.
+          const bool in = there && lane <= p.k;
+          const double d = in && zc > neg_inf() ? 1.0 / (1.0 + exp(-double(zc))) + double(bc) : double(neg_inf());
+          int rank = 0;
+          for (int o = 0; o <= p.k; ++o) {
+            const double od = __shfl_sync(kFull, d, o);
+            const int oe = __shfl_sync(kFull, ce, o);
+            rank += __shfl_sync(kFull, int(in), o) != 0 && (od > d || (od == d && oe < ce));
+          }
+          int to = ce;
+          for (int o = 0; o <= p.k; ++o) {
+            const int orank = __shfl_sync(kFull, in ? rank : kWarp, o), oe = __shfl_sync(kFull, ce, o);
+            if (orank == lane) to = oe;
+          }
+          ce = to;
+        }
       }
-    }
-    const bool pick = lane < p.k;
-    float zp = lane < rounds && my_key != 0u ? load_logit<Elem>(p.logits, row * p.E + my_e) : neg_inf();
-    if (has_bias) {
-      const float v = key_float(my_key), bp = lane < rounds && my_key != 0u ? p.bias[my_e] : 0.f;
-      const float v_up = __shfl_up_sync(kFull, v, 1), z_up = __shfl_up_sync(kFull, zp, 1), b_up = __shfl_up_sync(kFull, bp, 1);
-      unsure |= lane >= 1 && lane < rounds && my_key != 0u && v_up - v <= tol + 2.4e-7f * fabsf(v_up) &&
-                !(zp == z_up && bp == b_up);
-    }
-    if (__any_sync(kFull, unsure)) {
-      my_e = route_row_double<Elem>(p, row, lane);
-      if (pick) zp = load_logit<Elem>(p.logits, row * p.E + my_e);
+      const int pe = __shfl_sync(kFull, ce, lane % kPickLanes);
+      if (lane / kPickLanes == r) my_e = pe;
+      __syncwarp();                                              // the lists are read before the next row's are written
     }
 
+    const int64_t row = first + lane / kPickLanes;
+    const bool pick = lane / kPickLanes < per && row < p.T && lane % kPickLanes < p.k;
+    const float zp = pick ? load_logit<Elem>(p.logits, row * p.E + my_e) : neg_inf();
     float w;
     if (p.renorm) {
-      w = pick_weight(zp, pick, p.softmax);
-      float sum = 0.f;
-      for (int j = 0; j < p.k; ++j) sum += __shfl_sync(kFull, w, j);
-      w = sum > 0.f ? w / sum : 0.f;
+      w = pick_share(pick_weight(zp, pick, p.softmax), p.k);
     } else if (p.softmax) {
-      w = row_sum > 0.f && zp > neg_inf() ? expf(zp - row_max) / row_sum : 0.f;
+      w = my_sum > 0.f && zp > neg_inf() ? expf(zp - my_max) / my_sum : 0.f;
     } else {
       w = zp > neg_inf() ? sigmoid_exact(zp) : 0.f;
     }
     if (pick) {
-      p.idx[row * p.k + lane] = my_e;
-      p.gate[row * p.k + lane] = p.scale * w;
+      const int64_t at = row * p.k + lane % kPickLanes;
+      p.idx[at] = my_e;
+      p.gate[at] = p.scale * w;
       atomicAdd(&s_hist[my_e], 1);
     }
   }
@@ -359,18 +441,23 @@ __global__ void __launch_bounds__(256) route_bias_kernel(const RouteParams p) {
   p.bias_out[e] = over > 0 ? b + p.bias_gamma : over < 0 ? b - p.bias_gamma : b;
 }
 
+// Four rows a warp share the work on the picks; one row where that leaves fewer than
+// 16 warps an SM.
+int rows_per_warp(int64_t T, int sms) { return T >= int64_t(sms) * 64 ? 4 : 1; }
+
 template <class Elem, int NV, int VB>
 cudaError_t fwd_launch(const RouteParams& p, int sms, cudaStream_t stream) {
   const size_t smem = size_t(p.E) * sizeof(int);
   if (p.T <= kRouteOneCtaRows) {
-    route_fwd_kernel<Elem, NV, VB><<<1, kRouteThreads, smem, stream>>>(p);
+    route_fwd_kernel<Elem, NV, VB><<<1, kRouteThreads, smem, stream>>>(p, 1);
     return cudaGetLastError();
   }
   cudaError_t e = cudaMemsetAsync(p.counts, 0, smem, stream);
   if (e != cudaSuccess) return e;
-  const int64_t want = (p.T + kRouteWarps - 1) / kRouteWarps;
+  const int per = rows_per_warp(p.T, sms);
+  const int64_t rows = int64_t(kRouteWarps) * per, want = (p.T + rows - 1) / rows;
   const int64_t most = int64_t(sms) * 8;
-  route_fwd_kernel<Elem, NV, VB><<<int(want < most ? want : most), kRouteThreads, smem, stream>>>(p);
+  route_fwd_kernel<Elem, NV, VB><<<int(want < most ? want : most), kRouteThreads, smem, stream>>>(p, per);
   if ((e = cudaGetLastError()) != cudaSuccess || p.bias_out == nullptr) return e;
   route_bias_kernel<<<(p.E + 255) / 256, 256, 0, stream>>>(p);
   return cudaGetLastError();
@@ -414,34 +501,37 @@ cudaError_t fwd_elem(const RouteParams& p, int sms, cudaStream_t stream) {
 __device__ __forceinline__ float sum_same(float v, int e, int k) {
   float total = 0.f;
   for (int j = 0; j < k; ++j) {
-    const float o = __shfl_sync(kFull, v, j);
-    if (__shfl_sync(kFull, e, j) == e) total += o;
+    const float o = pick_value(v, j);
+    if (__shfl_sync(kFull, e, j, kPickLanes) == e) total += o;
   }
   return total;
 }
 
+// `per` rows a warp, lane 8 r + j with pick j of row r.
 template <class Elem, bool VEC>
-__global__ void __launch_bounds__(kRouteThreads) route_bwd_picks_kernel(const RouteBwdParams p) {
+__global__ void __launch_bounds__(kRouteThreads) route_bwd_picks_kernel(const RouteBwdParams p, const int per) {
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
-  const int64_t stride = int64_t(gridDim.x) * kRouteWarps;
-  for (int64_t row = int64_t(blockIdx.x) * kRouteWarps + warp; row < p.T; row += stride) {
-    int e = lane < p.k ? p.idx[row * p.k + lane] : -1;
+  const int j = lane % kPickLanes;
+  const int64_t stride = int64_t(gridDim.x) * kRouteWarps * per;
+  for (int64_t first = (int64_t(blockIdx.x) * kRouteWarps + warp) * per; first < p.T; first += stride) {
+    const int64_t row = first + lane / kPickLanes;
+    const bool there = lane / kPickLanes < per && row < p.T && j < p.k;
+    const int e = there ? p.idx[row * p.k + j] : -1;
     const bool live = e >= 0 && e < p.E;
-    const float dg = live ? p.scale * p.dgate[row * p.k + lane] : 0.f;
+    const float dg = live ? p.scale * p.dgate[row * p.k + j] : 0.f;
     const float z = live ? load_logit<Elem>(p.logits, row * p.E + e) : neg_inf();
-    float* out = p.dlogits + row * p.E;
+    float* out = p.dlogits + first * p.E;
+    const int64_t rows = p.T - first < per ? p.T - first : per;
     if constexpr (VEC) {
-      for (int i = lane; i < p.E / 4; i += kWarp) reinterpret_cast<float4*>(out)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = lane; i < int(rows) * p.E / 4; i += kWarp) reinterpret_cast<float4*>(out)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     } else {
-      for (int i = lane; i < p.E; i += kWarp) out[i] = 0.f;
+      for (int i = lane; i < int(rows) * p.E; i += kWarp) out[i] = 0.f;
     }
     float v;
     if (p.renorm) {
-      float w = pick_weight(z, live, p.softmax), sum = 0.f;
-      for (int j = 0; j < p.k; ++j) sum += __shfl_sync(kFull, w, j);
-      w = sum > 0.f ? w / sum : 0.f;
-      float d = 0.f;                                     // dg - sum_j w_j dg_j, as a sum of differences
-      for (int j = 0; j < p.k; ++j) d += __shfl_sync(kFull, w, j) * (dg - __shfl_sync(kFull, dg, j));
+      const float w = pick_share(pick_weight(z, live, p.softmax), p.k);
+      float d = 0.f;                                     // dg - sum_i w_i dg_i, as a sum of differences
+      for (int i = 0; i < p.k; ++i) d += pick_value(w, i) * (dg - pick_value(dg, i));
       v = w * d;
       if (!p.softmax && w > 0.f) v *= sigmoid_exact(-z); // 1 - sigmoid(z)
     } else {
@@ -449,7 +539,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_picks_kernel(const Ro
     }
     v = sum_same(v, e, p.k);
     __syncwarp();                                        // the zeros lie before the picks' values
-    if (live) out[e] = v;
+    if (live) p.dlogits[row * p.E + e] = v;
   }
 }
 
@@ -482,7 +572,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_softmax_kernel(const 
     const float pp = zp > neg_inf() ? ex2_approx((zp - shift) * kLog2e) * inv : 0.f;
     float S = 0.f;                                       // sum_j p_j dg_j over the picks
     for (int j = 0; j < p.k; ++j) S += __shfl_sync(kFull, pp, j) * __shfl_sync(kFull, dg, j);
-    const float v = pp * (sum_same(dg, e, p.k) - S);
+    const float v = pp * (sum_same(dg, e, p.k) - S);     // the lanes from 8 on have no pick
     float* out = p.dlogits + row * p.E;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -496,14 +586,16 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_softmax_kernel(const 
 
 template <class Elem>
 cudaError_t bwd_elem(const RouteBwdParams& p, int sms, cudaStream_t stream) {
-  const int64_t want = (p.T + kRouteWarps - 1) / kRouteWarps;
+  const bool picks = !p.softmax || p.renorm;
+  const int per = picks ? rows_per_warp(p.T, sms) : 1;
+  const int64_t rows = int64_t(kRouteWarps) * per, want = (p.T + rows - 1) / rows;
   const int64_t most = int64_t(sms) * 8;
   const int grid = int(want < most ? want : most);
-  if (!p.softmax || p.renorm) {
+  if (picks) {
     if (p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.dlogits) % 16 == 0)
-      route_bwd_picks_kernel<Elem, true><<<grid, kRouteThreads, 0, stream>>>(p);
+      route_bwd_picks_kernel<Elem, true><<<grid, kRouteThreads, 0, stream>>>(p, per);
     else
-      route_bwd_picks_kernel<Elem, false><<<grid, kRouteThreads, 0, stream>>>(p);
+      route_bwd_picks_kernel<Elem, false><<<grid, kRouteThreads, 0, stream>>>(p, per);
   } else if (p.E <= 4 * kWarp) {
     route_bwd_softmax_kernel<Elem, 4><<<grid, kRouteThreads, 0, stream>>>(p);
   } else if (p.E <= 8 * kWarp) {

@@ -32,6 +32,15 @@ _F8 = torch.float8_e4m3fn
 _BLOCK = 128
 
 
+# The current device and its current stream's handle, without the stream object around it (a call's
+# arguments are checked and its outputs allocated in some 10 us; the object alone takes 3).
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _stream() -> int:
+    return torch._C._cuda_getCurrentRawStream(_device())
+
+
 def _entry(fn):
     """Runs an entry point on the device of its first argument, with its `stream`
     argument, when given, as torch's current stream (see ``api._on_stream``)."""
@@ -42,19 +51,14 @@ def _entry(fn):
     def call(*args, **kwargs):
         stream = args[pos] if len(args) > pos else kwargs.get("stream")
         t = args[0] if args else kwargs.get(first)
-        device = contextlib.nullcontext()
-        if isinstance(t, torch.Tensor) and t.is_cuda:
-            if stream is not None and stream.device != t.device:
-                raise ValueError(f"the stream is on {stream.device}, {first} on {t.device}")
-            if t.device.index != torch.cuda.current_device():
-                device = torch.cuda.device(t.device)
-        with device, _on(stream):
+        on = isinstance(t, torch.Tensor) and t.is_cuda
+        if stream is None and (not on or t.get_device() == _device()):
+            return fn(*args, **kwargs)
+        if on and stream is not None and stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, {first} on {t.device}")
+        with torch.cuda.device(t.device) if on else contextlib.nullcontext(), _on(stream):
             return fn(*args, **kwargs)
     return call
-
-
-def _stream() -> int:
-    return int(torch.cuda.current_stream().cuda_stream)
 
 
 def _need(name: str, t: torch.Tensor, device: torch.device, dtype: torch.dtype, shape: tuple | None = None) -> None:
@@ -62,7 +66,8 @@ def _need(name: str, t: torch.Tensor, device: torch.device, dtype: torch.dtype, 
     _need_cuda(name, t, dtype)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call's tensors on {device}")
-    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+    if shape is not None and t.shape != shape and (
+            t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
         raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
 
 
