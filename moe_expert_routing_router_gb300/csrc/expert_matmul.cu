@@ -7,14 +7,22 @@
 // over all blocks.  The scales may be any fp32 numbers, and no sum is kept in
 // fewer than 32 bits.
 //
-// One persistent CTA per SM, 12 warps: a TMA producer (one thread), an MMA
-// issuer (one thread), two spare warps, and 8 epilogue warps of 32 rows by half
-// of the tile's columns.  Shared memory is a ring of operand stages
-// (one block of 128 of both operands, 128-byte swizzled); tensor memory is a
-// ring of block products, so that the tensor core forms block b + 1 while the
-// epilogue adds block b, and runs ahead into the next tile while a tile is
-// stored.  Every wait is bounded: when one runs out, the CTA records the
-// pipeline's error bit, drains its copies and returns.
+// One persistent CTA per SM, 20 warps: a TMA producer (one thread), an MMA
+// issuer (one thread), two spare warps, and 16 epilogue warps of 32 rows by a
+// quarter of the tile's columns.  Shared memory is a ring of operand stages (one block
+// of 128 of both operands, 128-byte swizzled); tensor memory is a ring of block
+// products, so that the tensor core forms block b + 1 while the epilogue adds
+// block b, and runs ahead into the next tile while a tile is stored.
+//
+// Wide tiles are worked on by two CTAs of a cluster (cta_group::2): 256 rows by
+// 256 columns, each CTA with its 128 rows of a, half of b's rows, and its rows'
+// sums.  A block then brings 32 KB into an SM instead of 48 KB; with single CTAs
+// the operands' way from L2 is the bound (at 128 x 256 tiles, 131 us of 16,384 x
+// 4096 x 2048 with an empty epilogue).  The first CTA issues the products; both
+// CTAs' copies count on its barriers, its commits arrive in both.
+//
+// Every wait is bounded: when one runs out, the CTA records the pipeline's error
+// bit, drains its copies and returns; a pair leaves together.
 #include "device_common.cuh"
 #include "expert_matmul.h"
 
@@ -27,7 +35,7 @@ namespace {
 constexpr int kBM = 128;                      // rows of a tile
 constexpr int kBK = 128;                      // block along the contraction: bytes of e4m3, and one scale
 constexpr int kBoxA = 32, kBoxB = 64;         // rows of one copy: a ragged tile copies only the boxes that it needs
-constexpr int kEpiWarps = 8, kFirstEpi = 4;
+constexpr int kEpiWarps = 16, kFirstEpi = 4;
 constexpr int kMmThreads = (kFirstEpi + kEpiWarps) * kWarp;
 constexpr int kTmemCols = 512;
 constexpr int kMaxE = 1024;
@@ -38,34 +46,87 @@ constexpr unsigned kFull = 0xffffffffu;
 // so calls on any streams, and captured ones, share the word.
 __device__ int g_mm_errors;
 
-// ---- tcgen05 / TMA primitives ------------------------------------------------
+// ---- tcgen05 / TMA primitives (CG: CTAs that work on a tile) -------------------
+template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(slot)), "r"(kTmemCols) : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  if constexpr (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(slot)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(slot)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
 }
+template <int CG>
 __device__ __forceinline__ void tmem_free(uint32_t addr) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(kTmemCols) : "memory");
+  if constexpr (CG == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(kTmemCols) : "memory");
+  else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(kTmemCols) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// Arrives on the barrier (of a pair: in both CTAs) when the products issued so far have ended.
+template <int CG>
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_addr(bar)) : "memory");
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(smem_addr(bar)), "h"(uint16_t(3)) : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_addr(bar)) : "memory");
 }
 
+template <int CG>
 __device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
-      :: "r"(smem_addr(dst)), "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y) : "memory");
+// `bar`: a shared::cluster address; of a pair, the first CTA's barrier.
+template <int CG>
+__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+        :: "r"(smem_addr(dst)), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+        :: "r"(smem_addr(dst)), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The address of the first CTA's copy of a shared variable.
+__device__ __forceinline__ uint32_t first_cta_addr(const void* p) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_addr(p)));
+  return a;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Arrives on a barrier of either CTA.  What it orders lies in tensor memory
+// (tcgen05.fence on both sides), so no wider scope than the default is asked for.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
 // Shared-memory matrix descriptor of a K-major operand in rows of 128 bytes,
 // 128-byte swizzle: groups of 8 rows lie 1024 bytes apart.
 __device__ __forceinline__ uint64_t smem_desc(const void* p) {
@@ -73,24 +134,24 @@ __device__ __forceinline__ uint64_t smem_desc(const void* p) {
          uint64_t(2) << 61;
 }
 
-// 32 columns of the warp's 32 rows; the values are there when it returns (the
-// wait is in the same statement, so no use of them can be moved before it).
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
-  uint32_t r[32];
+// 16 columns of the warp's 32 rows, asynchronously.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
-      "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
-      "}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+      "}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr) : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Waits for the thread's loads.  The values pass through the statement, so that
+// no use of them can be moved before it.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+      :: "memory");
 }
 
 // Lane l of each NP neighbouring lanes holds the NP pieces of row l in v; after
@@ -116,31 +177,44 @@ __device__ __forceinline__ void turn(uint4* v, int lane) {
 }
 
 // ---- the kernel ----------------------------------------------------------------
-template <int BN>
+template <int BN, int CG>
 struct Tile {
-  static constexpr int kStageBytes = (kBM + BN) * kBK;
+  static constexpr int kRows = kBM * CG;                       // of the CTAs together
+  static constexpr int kShareB = BN / CG;                      // rows of b that a CTA holds
+  static constexpr int kStageBytes = (kBM + kShareB) * kBK;
   static constexpr int kStages = 196608 / kStageBytes;         // 192 KB of operands
   static constexpr int kBufs = kTmemCols / BN;                 // block products in tensor memory
-  static constexpr int kCols = BN / 2;                         // columns of one epilogue warp
+  static constexpr int kCols = BN / 4;                         // columns of one epilogue warp
 };
 
 struct alignas(16) Shared {
-  uint64_t full[8], empty[8], tfull[8], tempty[8], drain;
+  // full: a stage's operands have landed; done: its product has been formed (the
+  // producer may fill it again, the epilogue may read); tempty: the product has been read
+  uint64_t full[8], done[8], tempty[8], drain;
   uint32_t tmem;
   int abort;
   int first[kMaxE + 1];                                        // tiles before expert e
   int block[kMaxE + 1];                                        // weight gradient: column blocks before expert e
-  alignas(16) float bscale[kEpiWarps][2][128];                 // weight gradient: a block's column scales, per warp
+  alignas(16) float bscale[kEpiWarps][2][64];                  // weight gradient: a block's column scales, per warp
 };
 
 // Bounded wait that every role uses: false once it, or another role's, ran out.
-// The clock is read only after a first suspended wait of 20 us has failed.
-__device__ __forceinline__ bool mm_wait(Shared& sh, const MatmulParams& p, uint64_t* bar, uint32_t parity) {
-  if (mbar_test_suspend(bar, parity, 20000u)) return true;
-  const uint64_t t0 = global_ns();
-  while (!mbar_test_suspend(bar, parity, 20000u)) {
+// Time is counted in SM cycles (at most about two a nanosecond), whose counter is
+// read in a few cycles, and only after some waits have failed.
+// With a second barrier, both are tested at once: a test takes some 100 cycles.
+__device__ __forceinline__ bool mm_wait(Shared& sh, const MatmulParams& p, uint64_t* bar, uint32_t parity,
+                                        uint64_t* bar2 = nullptr, uint32_t parity2 = 0) {
+  const auto test = [&]() {
+    const bool a = mbar_test(bar, parity), b = bar2 == nullptr || mbar_test(bar2, parity2);
+    return a && b;
+  };
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (test()) return true;
+  const long long t0 = clock64();
+  while (!test()) {
     if (*reinterpret_cast<volatile int*>(&sh.abort) != 0) return false;
-    if (global_ns() - t0 > p.timeout_ns) {
+    if (clock64() - t0 > 2 * (long long)(p.timeout_ns)) {
       *reinterpret_cast<volatile int*>(&sh.abort) = 1;
       atomicOr(&g_mm_errors, kErrPipelineTimeout);
       return false;
@@ -165,13 +239,18 @@ __device__ __forceinline__ void expert_rows(const MatmulParams& p, int e, int64_
 // A tile of the persistent loop, walked in ascending order by every role.
 struct Walk {
   int e = 0;
-  int row0 = 0, rows = 0;         // rows of a: the first one and how many are the tile's
+  int row0 = 0, rows = 0;         // rows of a: the CTA's first one, and how many of its 128 are in the tile
   int col0 = 0, cols = 0;         // columns of out within the expert
-  int r0 = 0;                     // the tile's first row within the expert's out
+  int r0 = 0;                     // the CTA's first row within the expert's out
+  int pair_rows = 0;              // rows of both CTAs
   int block0 = 0, blocks = 0;     // blocks along the contraction
 
-  template <int BN, bool WGRAD>
-  __device__ __forceinline__ void at(const MatmulParams& p, const Shared& sh, int tile) {
+  // The part of n that CTA `rank` has when each has `each`.
+  __device__ __forceinline__ static int share(int n, int rank, int each) { return max(0, min(each, n - rank * each)); }
+
+  template <int BN, int CG, bool WGRAD>
+  __device__ __forceinline__ void at(const MatmulParams& p, const Shared& sh, int tile, int rank) {
+    constexpr int kRows = Tile<BN, CG>::kRows;
     while (sh.first[e + 1] <= tile) ++e;
     const int i = tile - sh.first[e];
     const int ct = (p.C + BN - 1) / BN;
@@ -183,41 +262,44 @@ struct Walk {
     const int m = group * kGroupM + in % gm;
     col0 = in / gm * BN;
     cols = min(BN, p.C - col0);
-    r0 = m * kBM;
+    const int tile_r0 = m * kRows;
+    r0 = tile_r0 + rank * kBM;
     if constexpr (WGRAD) {
       row0 = r0;
-      rows = min(kBM, p.R - r0);
+      pair_rows = min(kRows, p.R - tile_r0);
       block0 = sh.block[e];
       blocks = sh.block[e + 1] - block0;
     } else {
       int64_t start, n;
       expert_rows(p, e, &start, &n);
       row0 = int(start) + r0;
-      rows = int(min(n - r0, int64_t(kBM)));
+      pair_rows = int(min(n - tile_r0, int64_t(kRows)));
       block0 = 0;
       blocks = (p.K + kBK - 1) / kBK;
     }
+    rows = share(pair_rows, rank, kBM);
   }
 };
 
-template <int BN, bool WGRAD, bool BF16>
+template <int BN, int CG, bool WGRAD, bool BF16>
 __global__ void __launch_bounds__(kMmThreads, 1)
 expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
-  using TL = Tile<BN>;
+  using TL = Tile<BN, CG>;
   extern __shared__ uint8_t s_dyn[];
   __shared__ Shared sh;
-  uint8_t* ring = s_dyn + (1024 - smem_addr(s_dyn) % 1024) % 1024;
+  uint8_t* ring = s_dyn + (1024 - smem_addr(s_dyn) % 1024) % 1024;     // the same place in both CTAs of a pair
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int rank = CG == 2 ? int(cluster_rank()) : 0;
+  const int first_tile = int(blockIdx.x) / CG, tile_step = int(gridDim.x) / CG;
 
   if (warp == 0) {
     if (lane == 0) {
       for (int i = 0; i < TL::kStages; ++i) {
         mbar_init(&sh.full[i], 1 + p.extra);
-        mbar_init(&sh.empty[i], 1);
+        mbar_init(&sh.done[i], 1);
       }
       for (int i = 0; i < TL::kBufs; ++i) {
-        mbar_init(&sh.tfull[i], 1);
-        mbar_init(&sh.tempty[i], kEpiWarps);
+        mbar_init(&sh.tempty[i], kEpiWarps * CG);
       }
       mbar_init(&sh.drain, 1);
       mbar_fence_init();
@@ -225,7 +307,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       sh.abort = *static_cast<volatile int*>(&g_mm_errors) != 0;
     }
   } else if (warp == 1) {
-    tmem_alloc(&sh.tmem);
+    tmem_alloc<CG>(&sh.tmem);
     tc_fence_before();
   } else if (warp == 2) {                                        // tiles and blocks before each expert
     const int ct = (p.C + BN - 1) / BN;
@@ -234,12 +316,12 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       int t = 0, b = 0;
       if (e0 + lane < p.E) {
         if constexpr (WGRAD) {
-          t = (p.R + kBM - 1) / kBM * ct;
+          t = (p.R + TL::kRows - 1) / TL::kRows * ct;
           b = int((max(int64_t(p.kept[e0 + lane]), int64_t(0)) + kBK - 1) / kBK);
         } else {
           int64_t start, n;
           expert_rows(p, e0 + lane, &start, &n);
-          t = int((n + kBM - 1) / kBM) * ct;
+          t = int((n + TL::kRows - 1) / TL::kRows) * ct;
         }
       }
       int ti = t, bi = b;
@@ -267,95 +349,114 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const int n_tiles = sh.abort != 0 ? 0 : sh.first[p.E];
-  __syncthreads();                                               // every thread has seen abort before a role sets it
+  // Every thread has seen abort before a role sets it, and a pair's barriers are
+  // set up before the other CTA arrives on them.
+  if constexpr (CG == 2) cluster_sync();
+  else __syncthreads();
 
   // The epilogue's sums want more registers than an even split gives: of the
-  // launch's 384 x 168, the first four warps keep 56 a thread and the others take 224.
-  static_assert(kFirstEpi * 56 + kEpiWarps * 224 <= (kFirstEpi + kEpiWarps) * 168, "registers of the launch");
+  // launch's 640 x 96, the first four warps keep 32 a thread and the others take 112.
+  static_assert(kFirstEpi * 32 + kEpiWarps * 112 <= (kFirstEpi + kEpiWarps) * 96, "registers of the launch");
   if (warp < kFirstEpi) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+    // Both roles run as whole warps, of which one elected thread issues: their
+    // addresses and descriptors then stay in uniform registers.  (With one thread
+    // in a branch of its own a block took 430 ns however little it copied.)
     if (warp == 0) {
-      if (lane == 0) {
-        // ---- producer: one stage per block ----
-        int s = 0, issued = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        Walk w;
-        for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
-          w.at<BN, WGRAD>(p, sh, tile);
-          const int na = (w.rows + kBoxA - 1) / kBoxA, nb = (w.cols + kBoxB - 1) / kBoxB;
-          const int b_row = WGRAD ? w.col0 : w.e * p.C + w.col0;
-          for (int b = 0; b < w.blocks; ++b) {
-            if (!(ok = mm_wait(sh, p, &sh.empty[s], phase ^ 1u))) break;
+      // ---- producer: one stage per block ----
+      int s = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      Walk w;
+      for (int tile = first_tile; tile < n_tiles && ok; tile += tile_step) {
+        w.at<BN, CG, WGRAD>(p, sh, tile, rank);
+        const int na = (w.rows + kBoxA - 1) / kBoxA;
+        const int nb = (Walk::share(w.cols, rank, TL::kShareB) + kBoxB - 1) / kBoxB;
+        const int b_row = (WGRAD ? w.col0 : w.e * p.C + w.col0) + rank * TL::kShareB;
+        int bytes = 0;                                           // of both CTAs: the first one's barrier counts them
+        for (int r = 0; r < CG; ++r)
+          bytes += ((Walk::share(w.pair_rows, r, kBM) + kBoxA - 1) / kBoxA * kBoxA +
+                    (Walk::share(w.cols, r, TL::kShareB) + kBoxB - 1) / kBoxB * kBoxB) * kBK;
+        for (int b = 0; b < w.blocks; ++b) {
+          ok = __all_sync(kFull, mm_wait(sh, p, &sh.done[s], phase ^ 1u));
+          if (!ok) break;
+          if (elect_one()) {
             uint8_t* sa = ring + s * TL::kStageBytes;
             uint8_t* sb = sa + kBM * kBK;
-            mbar_arrive_expect_tx(&sh.full[s], uint32_t(na * kBoxA + nb * kBoxB) * kBK);
+            if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], uint32_t(bytes));
+            const uint32_t bar = CG == 2 ? first_cta_addr(&sh.full[s]) : smem_addr(&sh.full[s]);
             const int x = (w.block0 + b) * kBK;
-            for (int i = 0; i < na; ++i) tma_2d(sa + i * kBoxA * kBK, &map_a, x, w.row0 + i * kBoxA, &sh.full[s]);
-            for (int i = 0; i < nb; ++i) tma_2d(sb + i * kBoxB * kBK, &map_b, x, b_row + i * kBoxB, &sh.full[s]);
-            ++issued;
-            if (++s == TL::kStages) {
-              s = 0;
-              phase ^= 1u;
-            }
+            for (int i = 0; i < na; ++i) tma_2d<CG>(sa + i * kBoxA * kBK, &map_a, x, w.row0 + i * kBoxA, bar);
+            for (int i = 0; i < nb; ++i) tma_2d<CG>(sb + i * kBoxB * kBK, &map_b, x, b_row + i * kBoxB, bar);
           }
-        }
-        if (!ok) {                                                 // copies in flight land before shared memory goes
-          for (int i = 0; i < TL::kStages && i < issued; ++i) {
-            const int back = issued - 1 - i;
-            mbar_wait(&sh.full[back % TL::kStages], uint32_t(back / TL::kStages) & 1u, p.timeout_ns);
+          __syncwarp();
+          ++issued;
+          if (++s == TL::kStages) {
+            s = 0;
+            phase ^= 1u;
           }
         }
       }
-    } else if (warp == 1) {
-      if (lane == 0) {
-        // ---- MMA issuer ----
-        // D fp32, A and B e4m3, both K-major, N = BN, M = 128
-        constexpr uint32_t idesc = (1u << 4) | uint32_t(BN / 8) << 17 | uint32_t(kBM / 16) << 24;
-        int s = 0, t = 0;
-        uint32_t phase = 0, tphase = 0;
-        bool ok = true;
-        Walk w;
-        for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
-          w.at<BN, WGRAD>(p, sh, tile);
-          for (int b = 0; b < w.blocks; ++b) {
-            if (!(ok = mm_wait(sh, p, &sh.tempty[t], tphase ^ 1u) && mm_wait(sh, p, &sh.full[s], phase))) break;
-            tc_fence_after();
-            const uint64_t da = smem_desc(ring + s * TL::kStageBytes), db = smem_desc(ring + s * TL::kStageBytes + kBM * kBK);
+      // Copies in flight land before shared memory goes; those of a pair's second
+      // CTA count on the first one's barriers, and the pair leaves together.
+      if (!ok && rank == 0) {
+        for (int i = 0; i < TL::kStages && i < issued; ++i) {
+          const int back = issued - 1 - i;
+          mbar_wait(&sh.full[back % TL::kStages], uint32_t(back / TL::kStages) & 1u, p.timeout_ns);
+        }
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ---- MMA issuer: of a pair, the first CTA's ----
+      // D fp32, A and B e4m3, both K-major, N = BN, M = the tile's rows
+      constexpr uint32_t idesc = (1u << 4) | uint32_t(BN / 8) << 17 | uint32_t(TL::kRows / 16) << 24;
+      const uint64_t desc0 = smem_desc(ring);
+      int s = 0, t = 0;
+      uint32_t phase = 0, tphase = 0;
+      bool ok = true;
+      Walk w;
+      for (int tile = first_tile; tile < n_tiles && ok; tile += tile_step) {
+        w.at<BN, CG, WGRAD>(p, sh, tile, rank);
+        for (int b = 0; b < w.blocks; ++b) {
+          ok = __all_sync(kFull, mm_wait(sh, p, &sh.full[s], phase, &sh.tempty[t], tphase ^ 1u));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t da = desc0 + uint64_t(s * (TL::kStageBytes >> 4)), db = da + (kBM * kBK >> 4);
 #pragma unroll
-            for (int k = 0; k < kBK / 32; ++k)                     // 32 bytes along the row: 2 units of 16
-              tc_mma_f8(tmem + t * BN, da + k * 2, db + k * 2, idesc, k > 0);
-            tc_commit(&sh.empty[s]);
-            tc_commit(&sh.tfull[t]);
-            if (++s == TL::kStages) {
-              s = 0;
-              phase ^= 1u;
-            }
-            if (++t == TL::kBufs) {
-              t = 0;
-              tphase ^= 1u;
-            }
+            for (int k = 0; k < kBK / 32; ++k)                   // 32 bytes along the row: 2 units of 16
+              tc_mma_f8<CG>(tmem + t * BN, da + k * 2, db + k * 2, idesc, k > 0);
+            tc_commit<CG>(&sh.done[s]);                          // the stage is free, and the product there
+          }
+          __syncwarp();
+          if (++s == TL::kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+          if (++t == TL::kBufs) {
+            t = 0;
+            tphase ^= 1u;
           }
         }
-        if (!ok) {                                                 // products in flight end before tensor memory goes
-          tc_commit(&sh.drain);
-          mbar_wait(&sh.drain, 0, p.timeout_ns);
-        }
+      }
+      if (!ok) {                                                 // products in flight end before tensor memory goes
+        if (elect_one()) tc_commit<CG>(&sh.drain);
+        __syncwarp();
+        mbar_wait(&sh.drain, 0, p.timeout_ns);
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     // ---- epilogue: rows 32 * quad + lane, kCols columns ----
     constexpr int CW = TL::kCols;
     const int quad = warp % 4, cg = (warp - kFirstEpi) / 4, row = quad * 32 + lane;
-    float(*s_bs)[128] = sh.bscale[warp - kFirstEpi];
+    float(*s_bs)[64] = sh.bscale[warp - kFirstEpi];
     const int kblocks = (p.K + kBK - 1) / kBK, cblocks = (p.C + kBK - 1) / kBK;
-    int t = 0;
-    uint32_t tphase = 0;
+    int s = 0, t = 0;
+    uint32_t phase = 0;
     bool ok = true;
     Walk w;
-    for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
-      w.at<BN, WGRAD>(p, sh, tile);
+    for (int tile = first_tile; tile < n_tiles && ok; tile += tile_step) {
+      w.at<BN, CG, WGRAD>(p, sh, tile, rank);
       const int c0 = w.col0 + cg * CW;                           // the warp's first column of out
       const bool busy = quad * 32 < w.rows && c0 < p.C;          // warp-uniform: whether it has anything to add
       const bool live = row < w.rows;
@@ -395,23 +496,35 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       for (int b = 0; b < w.blocks; ++b) {
         const float ra = sa, rb = sb;
         if constexpr (WGRAD) {
-          *reinterpret_cast<float4*>(&s_bs[b & 1][lane * 4]) = sb4;
+          if (lane * 4 < CW) *reinterpret_cast<float4*>(&s_bs[b & 1][lane * 4]) = sb4;
           __syncwarp();
         }
         if (b + 1 < w.blocks) fetch();
-        ok = __all_sync(kFull, mm_wait(sh, p, &sh.tfull[t], tphase));   // one answer for the warp
+        ok = __all_sync(kFull, mm_wait(sh, p, &sh.done[s], phase));   // one answer for the warp
         if (!ok) break;
         tc_fence_after();
+        // The buffer is free as soon as its last columns have been read.
+        const auto release = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (CG == 2) arrive_cluster(first_cta_addr(&sh.tempty[t]));
+            else mbar_arrive(&sh.tempty[t]);
+          }
+        };
         if (busy) {
           const uint32_t addr = tmem + t * BN + cg * CW + (uint32_t(quad * 32) << 16);
           const float2 s2 = WGRAD ? make_float2(ra, ra) : make_float2(ra * rb, ra * rb);
 #pragma unroll
-          for (int c = 0; c < CW; c += 32) {
-            float v[32];
-            tmem_ld32(addr + c, v);
+          for (int c = 0; c < CW; c += 16) {
+            uint32_t u[16];
+            tmem_ld16(addr + c, u);
+            tmem_ld_wait(u);
+            if (c + 16 == CW) release();
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              float2 x = make_float2(v[i], v[i + 1]), y = make_float2(v[i + 2], v[i + 3]);
+            for (int i = 0; i < 16; i += 4) {
+              const float2 x = make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1]));
+              const float2 y = make_float2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3]));
               if constexpr (WGRAD) {
                 const float4 q = *reinterpret_cast<const float4*>(&s_bs[b & 1][c + i]);
                 acc[(c + i) / 2] = fma2(mul2(x, s2), make_float2(q.x, q.y), acc[(c + i) / 2]);
@@ -422,14 +535,14 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
               }
             }
           }
-          tc_fence_before();
+        } else {
+          release();
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.tempty[t]);
-        if (++t == TL::kBufs) {
-          t = 0;
-          tphase ^= 1u;
+        if (++s == TL::kStages) {
+          s = 0;
+          phase ^= 1u;
         }
+        if (++t == TL::kBufs) t = 0;
       }
       if (!ok || !busy) continue;
       // Pieces of 16 bytes, NP of which are turned among NP lanes at a time.
@@ -464,10 +577,12 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       }
     }
   }
+  __syncwarp();                                                  // the roles' single threads are back
   tc_fence_before();
-  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();                         // nothing of the other CTA's is on its way here any more
+  else __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_free(tmem);
+  if (warp == 1) tmem_free<CG>(tmem);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -498,7 +613,7 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, 
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool WGRAD, bool BF16>
+template <int BN, int CG, bool WGRAD, bool BF16>
 cudaError_t launch(const MatmulParams& p, int sms, const char** error, cudaStream_t stream) {
   CUtensorMap ma, mb;
   const uint64_t cols = WGRAD ? uint64_t(p.blocks) * kBK : uint64_t(p.K);
@@ -507,18 +622,31 @@ cudaError_t launch(const MatmulParams& p, int sms, const char** error, cudaStrea
     *error = "cuTensorMapEncodeTiled refused an operand";
     return cudaErrorUnknown;
   }
-  constexpr size_t smem = size_t(Tile<BN>::kStages) * Tile<BN>::kStageBytes + 1024;
-  static_assert(Tile<BN>::kStages <= 8 && Tile<BN>::kBufs <= 8 && sizeof(Shared) + smem <= 232448, "shared memory of one CTA");
-  const auto kernel = expert_matmul_kernel<BN, WGRAD, BF16>;
+  using TL = Tile<BN, CG>;
+  constexpr size_t smem = size_t(TL::kStages) * TL::kStageBytes + 1024;
+  static_assert(TL::kStages <= 8 && TL::kBufs <= 8 && sizeof(Shared) + smem <= 232448, "shared memory of one CTA");
+  static_assert(TL::kShareB % kBoxB == 0 && TL::kStageBytes % 1024 == 0, "whole boxes, swizzle atoms aligned");
+  const auto kernel = expert_matmul_kernel<BN, CG, WGRAD, BF16>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   // At most this many tiles: every expert's last row tile may be ragged.
   const int64_t ct = (p.C + BN - 1) / BN;
-  int64_t rt = WGRAD ? int64_t(p.E) * ((p.R + kBM - 1) / kBM) : p.M / kBM + p.E;
+  int64_t rt = WGRAD ? int64_t(p.E) * ((p.R + TL::kRows - 1) / TL::kRows) : p.M / TL::kRows + p.E;
   if (!WGRAD && rt > p.M) rt = p.M;
-  const int grid = int(rt * ct < sms ? rt * ct : sms);
-  kernel<<<grid, kMmThreads, smem, stream>>>(p, ma, mb);
-  return cudaGetLastError();
+  const int64_t groups = sms / CG;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((rt * ct < groups ? rt * ct : groups) * CG));
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = CG;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = CG > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p, ma, mb);
 }
 
 }  // namespace
@@ -536,13 +664,13 @@ cudaError_t expert_matmul_errors(int* bits, cudaStream_t stream) {
 }
 
 cudaError_t launch_expert_matmul(const MatmulParams& p, int sms, const char** error, cudaStream_t stream) {
-  if (p.wgrad) return launch<256, true, false>(p, sms, error, stream);
+  if (p.wgrad) return launch<256, 2, true, false>(p, sms, error, stream);
   // Few rows an expert: reading the weights is what takes the time, and narrow
   // tiles spread them over more SMs.
   const bool narrow = p.M <= int64_t(p.E) * 64;
   if (p.out_bf16)
-    return narrow ? launch<128, false, true>(p, sms, error, stream) : launch<256, false, true>(p, sms, error, stream);
-  return narrow ? launch<128, false, false>(p, sms, error, stream) : launch<256, false, false>(p, sms, error, stream);
+    return narrow ? launch<128, 1, false, true>(p, sms, error, stream) : launch<256, 2, false, true>(p, sms, error, stream);
+  return narrow ? launch<128, 1, false, false>(p, sms, error, stream) : launch<256, 2, false, false>(p, sms, error, stream);
 }
 
 }  // namespace moe
