@@ -27,7 +27,7 @@ SOURCES = ["router_bf16_staged.cu", "router_bf16_direct.cu", "router_fp32_staged
            "router_step_ext_bf16_staged.cu", "router_step_ext_bf16_direct.cu", "router_step_ext_fp32_staged.cu",
            "router_step_ext_fp32_direct.cu",
            "router_dispatch.cu", "router_ext_bf16.cu", "router_ext_fp32.cu", "router_combine.cu", "sinkhorn.cu", "taot_match.cu", "eplb.cu", "abi.cu",
-           "route.cu", "quantize.cu", "expert_matmul.cu", "expert_combine.cu", "experts_abi.cu"]
+           "route_bf16.cu", "route_fp32.cu", "quantize.cu", "expert_matmul.cu", "expert_combine.cu", "experts_abi.cu"]
 
 
 def nvcc() -> str:

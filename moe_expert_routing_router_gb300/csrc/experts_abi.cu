@@ -112,7 +112,10 @@ moe_status moe_route_fwd(const void* logits, moe_dtype dt, int64_t T, int32_t E,
   p.keep = topk_groups;
   p.top2 = group_score == MOE_GROUP_TOP2;
   p.L = 1;
-  while (p.L * 2 * n_groups <= moe::kRouteLanes) p.L *= 2;
+  while (p.L * 2 * n_groups <= moe::kRouteLanes) {
+    p.L *= 2;
+    ++p.lshift;
+  }
   p.chunk = (p.gs + p.L - 1) / p.L;
   p.bias = bias;
   p.renorm = renorm < 0 ? k > 1 : renorm;
@@ -122,7 +125,7 @@ moe_status moe_route_fwd(const void* logits, moe_dtype dt, int64_t T, int32_t E,
   p.idx = idx;
   p.gate = gate;
   p.counts = counts;
-  return launched(moe::launch_route_fwd(p, dt == MOE_DTYPE_BF16, sms, stream), "moe_route_fwd launch");
+  return launched(dt == MOE_DTYPE_BF16 ? moe::launch_route_fwd_bf16(p, sms, stream) : moe::launch_route_fwd_fp32(p, sms, stream), "moe_route_fwd launch");
 }
 
 moe_status moe_route_bwd(const void* logits, moe_dtype dt, int64_t T, int32_t E, int32_t k,
@@ -139,7 +142,7 @@ moe_status moe_route_bwd(const void* logits, moe_dtype dt, int64_t T, int32_t E,
   int sms = 0;
   if ((s = moe::abi_sms(&sms)) != MOE_OK) return s;
   moe::RouteBwdParams p = {logits, T, E, k, score == MOE_SCORE_SOFTMAX, renorm < 0 ? k > 1 : renorm, scale, idx, dgate, dlogits};
-  return launched(moe::launch_route_bwd(p, dt == MOE_DTYPE_BF16, sms, stream), "moe_route_bwd launch");
+  return launched(dt == MOE_DTYPE_BF16 ? moe::launch_route_bwd_bf16(p, sms, stream) : moe::launch_route_bwd_fp32(p, sms, stream), "moe_route_bwd launch");
 }
 
 moe_status moe_quantize_rows(const void* x, moe_dtype dt, int64_t rows, int64_t M, int32_t K,

@@ -34,9 +34,6 @@ __device__ __forceinline__ Pow2Scale pow2_scale(float amax) {
   return {__uint_as_float(uint32_t(n + 127) << 23), __uint_as_float(uint32_t(127 - n) << 23)};
 }
 
-// bits of |x|, in the order of |x|, that keep a NaN (its bits are above those of every number).
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
 __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
@@ -74,6 +71,27 @@ struct Values {
     if constexpr (BF16) return __uint_as_float(i % 2 == 0 ? w[i / 2] << 16 : w[i / 2] & 0xffff0000u);
     else return __uint_as_float(w[i]);
   }
+  // Largest |x| so far, word by word: as unsigned integers (bf16: halves), so that a
+  // NaN is above every number.
+  __device__ __forceinline__ static uint32_t larger(uint32_t m, uint32_t w) {
+    if constexpr (BF16) return __vmaxu2(m, w & 0x7fff7fffu);
+    else return max(m, w & 0x7fffffffu);
+  }
+  // The fp32 bits of the larger half (bf16), or of the word.
+  __device__ __forceinline__ static uint32_t bits(uint32_t m) {
+    if constexpr (BF16) return max(m << 16, m & 0xffff0000u);
+    else return m;
+  }
+  __device__ __forceinline__ uint32_t largest() const {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) m = larger(m, w[i]);
+    return m;
+  }
+  // Four neighbouring values from the i-th on, scaled and rounded.
+  __device__ __forceinline__ uint32_t codes(int i, float inv) const {
+    return pack4(get(i) * inv, get(i + 1) * inv, get(i + 2) * inv, get(i + 3) * inv);
+  }
 };
 
 // The row of x that row r of the output holds, or -1: zeros.  All rows fit int32.
@@ -85,47 +103,43 @@ __device__ __forceinline__ int source_row(const int32_t* perm, int k, int64_t r,
 }
 
 // ---------------------------------------------------------------------------
-// Rows: blocks of 1 x 128.  A half warp holds a block, 8 values a lane.  A CTA
+// Rows: blocks of 1 x 128.  Eight lanes hold a block, 16 values each.  A CTA
 // takes 32 rows by 4 blocks of columns (512), so that the scales of a block
 // column, which lie one row after another, leave as whole 128-byte lines.
 // ---------------------------------------------------------------------------
-constexpr int kRowsTile = 32, kRowsBlocks = 4, kQuantThreads = 256;
+constexpr int kRowsTile = 32, kRowsBlocks = 4, kQuantThreads = 256, kRowLanes = 8, kRowVals = kScaleBlock / kRowLanes;
 
 template <bool BF16>
 __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const QuantRowsParams p) {
+  using V = Values<BF16, kRowVals>;
   __shared__ float s_scale[kRowsBlocks][kRowsTile];
   __shared__ int s_row[kRowsTile];
   const int64_t r0 = int64_t(blockIdx.x) * kRowsTile;
   if (threadIdx.x < kRowsTile)
     s_row[threadIdx.x] = r0 + threadIdx.x < p.M ? source_row(p.perm, p.k, r0 + threadIdx.x, p.rows) : -1;
   __syncthreads();
-  const int half = threadIdx.x / 16, hl = threadIdx.x % 16;      // 16 half warps
-  const int kb = blockIdx.y * kRowsBlocks + half % kRowsBlocks;
-  const int col = kb * kScaleBlock + hl * 8;
-  constexpr int kIter = kRowsTile * kRowsBlocks / (kQuantThreads / 16);
-  Values<BF16, 8> v[kIter];
+  constexpr int kTeams = kQuantThreads / kRowLanes, kIter = kRowsTile * kRowsBlocks / kTeams;   // 32 teams, 4 blocks each
+  const int team = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
+  const int kb = team % kRowsBlocks;
+  const int col = (blockIdx.y * kRowsBlocks + kb) * kScaleBlock + l * kRowVals;
+  V v[kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    const int t = s_row[i * (kRowsTile / kIter) + half / kRowsBlocks];
+    const int t = s_row[i * (kRowsTile / kIter) + team / kRowsBlocks];
     if (t >= 0 && col < p.K) v[i].load(p.x, int64_t(t) * p.K + col);
     else v[i].zero();
   }
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    const int row = i * (kRowsTile / kIter) + half / kRowsBlocks;
-    uint32_t m = 0;
+    const int row = i * (kRowsTile / kIter) + team / kRowsBlocks;
+    uint32_t m = v[i].largest();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i].get(j)));
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(kFull, m, off));
-    const Pow2Scale s = pow2_scale(__uint_as_float(m));
-    if (hl == 0) s_scale[half % kRowsBlocks][row] = s.scale;
-    if (r0 + row < p.M && col < p.K) {
-      uint2 o;
-      o.x = pack4(v[i].get(0) * s.inv, v[i].get(1) * s.inv, v[i].get(2) * s.inv, v[i].get(3) * s.inv);
-      o.y = pack4(v[i].get(4) * s.inv, v[i].get(5) * s.inv, v[i].get(6) * s.inv, v[i].get(7) * s.inv);
-      *reinterpret_cast<uint2*>(p.q + (r0 + row) * p.K + col) = o;
-    }
+    for (int off = kRowLanes / 2; off > 0; off >>= 1) m = V::larger(m, __shfl_xor_sync(kFull, m, off));
+    const Pow2Scale s = pow2_scale(__uint_as_float(V::bits(m)));
+    if (l == 0) s_scale[kb][row] = s.scale;
+    if (r0 + row < p.M && col < p.K)
+      *reinterpret_cast<uint4*>(p.q + (r0 + row) * p.K + col) =
+          make_uint4(v[i].codes(0, s.inv), v[i].codes(4, s.inv), v[i].codes(8, s.inv), v[i].codes(12, s.inv));
   }
   __syncthreads();
   for (int i = threadIdx.x; i < kRowsBlocks * kRowsTile; i += kQuantThreads) {
@@ -196,21 +210,23 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_cols_kernel(const Quan
     if (t >= 0 && col < p.K) v[i].load(p.x, int64_t(t) * p.K + col);
     else v[i].zero();
   }
-  uint32_t m[kColsLane] = {};
+  using V = Values<BF16, kColsLane>;
+  uint32_t m[V::kWords] = {};                                    // a column each, bf16: two
 #pragma unroll
   for (int i = 0; i < kColsRows; ++i)
 #pragma unroll
-    for (int j = 0; j < kColsLane; ++j) m[j] = max(m[j], abs_bits(v[i].get(j)));
-  *reinterpret_cast<uint4*>(&s_max[warp][lane * kColsLane]) = make_uint4(m[0], m[1], m[2], m[3]);
+    for (int j = 0; j < V::kWords; ++j) m[j] = V::larger(m[j], v[i].w[j]);
+#pragma unroll
+  for (int j = 0; j < V::kWords; ++j) s_max[warp][lane * V::kWords + j] = m[j];
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kColsWarps; ++w) {
-    const uint4 o = *reinterpret_cast<const uint4*>(&s_max[w][lane * kColsLane]);
-    m[0] = max(m[0], o.x); m[1] = max(m[1], o.y); m[2] = max(m[2], o.z); m[3] = max(m[3], o.w);
-  }
+  for (int w = 0; w < kColsWarps; ++w)
+#pragma unroll
+    for (int j = 0; j < V::kWords; ++j) m[j] = V::larger(m[j], s_max[w][lane * V::kWords + j]);
   Pow2Scale s[kColsLane];
 #pragma unroll
-  for (int j = 0; j < kColsLane; ++j) s[j] = pow2_scale(__uint_as_float(m[j]));
+  for (int j = 0; j < kColsLane; ++j)
+    s[j] = pow2_scale(__uint_as_float(BF16 ? (j % 2 == 0 ? m[j / 2] << 16 : m[j / 2] & 0xffff0000u) : m[j % V::kWords]));
   if (warp == 0 && col < p.K)
     *reinterpret_cast<float4*>(p.scale + blk * p.K + col) = make_float4(s[0].scale, s[1].scale, s[2].scale, s[3].scale);
 #pragma unroll
@@ -254,9 +270,8 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_weights_kernel(const Q
     else v[i].zero();
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i].get(j)));
+  for (int i = 0; i < 8; ++i) m = Values<BF16, 8>::larger(m, v[i].largest());
+  m = Values<BF16, 8>::bits(m);
   m = __reduce_max_sync(kFull, m);
   if (lane == 0) s_max[warp] = m;
   __syncthreads();
@@ -272,8 +287,8 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_weights_kernel(const Q
   for (int i = 0; i < 8; ++i) {
     const int row = nb * kScaleBlock + i * 16 + tr;
     uint2 o;
-    o.x = pack4(v[i].get(0) * s.inv, v[i].get(1) * s.inv, v[i].get(2) * s.inv, v[i].get(3) * s.inv);
-    o.y = pack4(v[i].get(4) * s.inv, v[i].get(5) * s.inv, v[i].get(6) * s.inv, v[i].get(7) * s.inv);
+    o.x = v[i].codes(0, s.inv);
+    o.y = v[i].codes(4, s.inv);
     if (p.q != nullptr && row < p.N && col < p.K)
       *reinterpret_cast<uint2*>(p.q + matrix + int64_t(row) * p.K + col) = o;
     if (p.qt != nullptr) {

@@ -1,4 +1,4 @@
-// Launchers of the scored, group-limited routing and its gradient (route.cu).
+// Launchers of the scored, group-limited routing and its gradient (route_kernels.cuh, per logit type).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -15,7 +15,7 @@ struct RouteParams {
   int softmax;            // scores: 0 sigmoid, 1 softmax
   int G, gs, keep;        // groups, experts per group, groups a token may use
   int top2;               // a group's score: 0 its largest choice value, 1 the sum of its two largest
-  int L, chunk;           // lanes per group, experts per lane
+  int L, lshift, chunk;   // lanes per group (a power of two, and its logarithm), experts per lane
   const float* bias;      // [E] or null
   int renorm;
   float scale;
@@ -26,7 +26,8 @@ struct RouteParams {
   int32_t* counts;        // [E]
 };
 
-cudaError_t launch_route_fwd(const RouteParams& p, bool bf16, int sms, cudaStream_t stream);
+cudaError_t launch_route_fwd_bf16(const RouteParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_route_fwd_fp32(const RouteParams& p, int sms, cudaStream_t stream);
 
 struct RouteBwdParams {
   const void* logits;     // [T, E]
@@ -39,6 +40,7 @@ struct RouteBwdParams {
   float* dlogits;         // [T, E]
 };
 
-cudaError_t launch_route_bwd(const RouteBwdParams& p, bool bf16, int sms, cudaStream_t stream);
+cudaError_t launch_route_bwd_bf16(const RouteBwdParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_route_bwd_fp32(const RouteBwdParams& p, int sms, cudaStream_t stream);
 
 }  // namespace moe

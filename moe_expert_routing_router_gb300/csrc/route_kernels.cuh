@@ -17,6 +17,8 @@
 // because their inputs are), the warp ranks them again in double.  That is a row
 // in some hundred, so the picks are those of the double-precision definition at
 // fp32 cost.
+#pragma once
+
 #include "device_common.cuh"
 #include "route.h"
 
@@ -84,29 +86,6 @@ __device__ __forceinline__ float pick_share(float w, int k) {
   float sum = 0.f;
   for (int j = 0; j < k; ++j) sum += pick_value(w, j);
   return sum > 0.f ? w / sum : 0.f;
-}
-
-// Descending order of NV keys: Batcher's merge exchange, unrolled.
-template <int NV>
-__device__ __forceinline__ void sort_keys(unsigned long long (&v)[NV]) {
-  constexpr int N = NV <= 4 ? 4 : NV <= 8 ? 8 : NV <= 16 ? 16 : NV <= 32 ? 32 : 64;
-#pragma unroll
-  for (int p = 1; p < N; p *= 2) {
-#pragma unroll
-    for (int q = p; q >= 1; q /= 2) {
-#pragma unroll
-      for (int a = 0; a < NV; ++a) {
-        const int b = a + q;
-        // pairs a, a + q whose distance from q % p falls into even runs of q, inside one block of 2p
-        if (b < NV && a >= q % p && (a - q % p) / q % 2 == 0 && a / (2 * p) == b / (2 * p)) {
-          const unsigned long long x = v[a], y = v[b];
-          const bool swap = x < y;
-          v[a] = swap ? y : x;
-          v[b] = swap ? x : y;
-        }
-      }
-    }
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -188,115 +167,185 @@ __device__ __noinline__ int route_row_double(const RouteParams& p, int64_t row, 
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  NV: experts per lane, at least `chunk`; VB: bytes per load.
+// The picks of a row where values that decide them are next to one another
+// (`close`), or where its groups' scores are (`unsure`).  Lane j holds the j-th
+// largest key and its expert, the k picks and two more.
+// ---------------------------------------------------------------------------
+template <class Elem>
+__device__ __noinline__ int route_settle(const RouteParams& p, int64_t row, int lane, uint32_t ck, int ce, int rounds,
+                                         float tol, bool close, bool unsure) {
+  const bool there = lane < rounds && ck != 0u;
+  const float zc = there ? load_logit<Elem>(p.logits, row * p.E + ce) : neg_inf();
+  const float bc = there && p.bias != nullptr ? p.bias[ce] : 0.f, c = key_float(ck);
+  const float c_up = __shfl_up_sync(kFull, c, 1), z_up = __shfl_up_sync(kFull, zc, 1), b_up = __shfl_up_sync(kFull, bc, 1);
+  // sure all the same where the inputs are equal
+  const bool open = close && lane >= 1 && lane <= p.k && there && c_up - c <= tol + 2.4e-7f * fabsf(c_up) &&
+                    !(zc == z_up && bc == b_up);
+  const float last = __shfl_sync(kFull, c, p.k - 1);
+  const bool beyond = lane == p.k + 1 && there && last - c <= tol + 2.4e-7f * fabsf(last);
+  const bool any_open = __any_sync(kFull, open), any_beyond = __any_sync(kFull, beyond);
+  if (unsure || (any_open && (any_beyond || p.softmax))) return route_row_double<Elem>(p, row, lane);
+  if (!any_open) return ce;
+  // The k + 1 largest are known as a set: one double-precision sigmoid a lane orders them.
+  const bool in = there && lane <= p.k;
+  const double d = in && zc > neg_inf() ? 1.0 / (1.0 + exp(-double(zc))) + double(bc) : double(neg_inf());
+  int rank = 0;
+  for (int o = 0; o <= p.k; ++o) {
+    const double od = __shfl_sync(kFull, d, o);
+    const int oe = __shfl_sync(kFull, ce, o);
+    rank += __shfl_sync(kFull, int(in), o) != 0 && (od > d || (od == d && oe < ce));
+  }
+  int to = ce;
+  for (int o = 0; o <= p.k; ++o) {
+    const int orank = __shfl_sync(kFull, in ? rank : kWarp, o), oe = __shfl_sync(kFull, ce, o);
+    if (orank == lane) to = oe;
+  }
+  return to;
+}
+
+// ---------------------------------------------------------------------------
+// Forward.
+//   NV    experts per lane, at least `chunk`
+//   VB    bytes per load; above the element's size only where every lane's NV
+//         experts are there and aligned (FULL: no lane has fewer)
+//   MODE  0: the order of the logits decides everything and gates need no sum over the
+//         row; 1: sigmoid scores; 2: softmax scores
 //
-// A lane sorts its experts' keys (value above the inverted place, so that ties
-// stand in expert order) into shared memory; a pick is then the largest head of
-// the 32 lists (one warp reduction, the lowest lane that has it), whose lane
-// goes on to its next entry.  With a bias two more than the k picks are taken,
-// to see what hangs on rounding.  A warp selects for `per` rows one after another and then
-// computes the gates of all of them, a pick a lane.
+// Selection: the k largest of the lanes' maxima bound the k-th choice value from
+// below (a warp reduction and two instructions each); the few experts that reach
+// the bound are gathered, one a lane in expert order, and ranked by counting.
+// With a bias two more than the k picks are ranked, to see what hangs on
+// rounding.  Should more than 32 experts reach the bound (whole groups in single
+// lanes, long ties), the warp takes the maximum again and again instead.  A warp
+// selects for `per` rows one after another, each loaded while the one before is
+// worked on; the rows that hang on rounding are settled behind them, and then
+// the gates of all of them are computed, a pick a lane.
+// The instructions bound it: sorting a lane's experts and popping them one by one
+// took 1145 a row of 256.
 // ---------------------------------------------------------------------------
 constexpr int kMaxRounds = 10;                                   // 8 picks and two more
+constexpr int kMaxPer = kWarp / kPickLanes;                      // rows a warp finishes at once
 
-template <class Elem, int NV, int VB>
-__global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
+template <class Elem, int NV, int VB, bool FULL, int MODE>
+__global__ void __launch_bounds__(kRouteThreads, NV <= 8 ? 4 : NV <= 16 ? 3 : NV <= 32 ? 2 : 1)
+route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
   using Raw = typename Elem::Raw;
   constexpr int kPer = VB / int(sizeof(Raw));                    // elements per load
-  constexpr int kList = NV < kMaxRounds ? NV : kMaxRounds;
-  __shared__ unsigned long long s_list[kRouteWarps][kList][kWarp];
+  constexpr bool kAhead = NV * int(sizeof(Raw)) <= 64;           // whether the next row fits beside this one
+  __shared__ __align__(16) uint2 s_cand[kRouteWarps][kWarp];     // key and expert of the candidates, in expert order
+  __shared__ uint2 s_ranked[kRouteWarps][kMaxPer][kMaxRounds];   // largest first
   extern __shared__ int s_hist[];                                // [E]
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   for (int e = threadIdx.x; e < p.E; e += kRouteThreads) s_hist[e] = 0;
   __syncthreads();
 
-  const int g = lane / p.L, sub = lane % p.L;
+  const int g = lane >> p.lshift, sub = lane & (p.L - 1);
   const int base = g * p.gs + sub * p.chunk;
   const int n = g < p.G ? max(0, min(p.chunk, p.gs - sub * p.chunk)) : 0;
   const bool has_bias = p.bias != nullptr;
   const bool grouped = p.keep < p.G;
-  const bool all_scores = has_bias || (p.top2 && grouped) || (p.softmax && !p.renorm);
   const int rounds = has_bias ? p.k + 2 : p.k;
   float bv[NV];
+  const auto fetch_bias = [&]() {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) bv[i] = has_bias && i < n ? p.bias[base + i] : 0.f;
+    for (int i = 0; i < NV; ++i) bv[i] = has_bias && i < n ? p.bias[base + i] : 0.f;
+  };
+  fetch_bias();
+
+  Raw raw[NV];
+  const auto fetch = [&](int64_t row) {
+    const Raw* src = static_cast<const Raw*>(p.logits) + row * p.E + base;
+#pragma unroll
+    for (int v = 0; v < NV / kPer; ++v) {
+      alignas(16) Raw part[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) part[i] = Elem::kNegInf;
+      if (FULL ? n > 0 : v * kPer < n) {
+        if constexpr (VB == 16) *reinterpret_cast<uint4*>(part) = *reinterpret_cast<const uint4*>(src + v * kPer);
+        else if constexpr (VB == 8) *reinterpret_cast<uint2*>(part) = *reinterpret_cast<const uint2*>(src + v * kPer);
+        else if constexpr (VB == 4) *reinterpret_cast<uint32_t*>(part) = *reinterpret_cast<const uint32_t*>(src + v * kPer);
+        else part[0] = src[v];
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) raw[v * kPer + i] = part[i];
+    }
+  };
 
   const int64_t stride = int64_t(gridDim.x) * kRouteWarps * per;
-  for (int64_t first = (int64_t(blockIdx.x) * kRouteWarps + warp) * per; first < p.T; first += stride) {
-    int my_e = 0;                                                // lane 8 r + j: pick j of row first + r
-    float my_max = 0.f, my_sum = 1.f;                            // and that row's softmax
-    for (int r = 0; r < per && first + r < p.T; ++r) {
+  const int64_t first0 = (int64_t(blockIdx.x) * kRouteWarps + warp) * per;
+  if (kAhead && first0 < p.T) fetch(first0);
+  for (int64_t first = first0; first < p.T; first += stride) {
+    float my_max = 0.f, my_sum = 1.f, my_tol = 0.f;              // of row first + lane / 8
+    unsigned close_rows = 0u, unsure_rows = 0u;
+    const int rows = int(min(int64_t(per), p.T - first));
+    for (int r = 0; r < rows; ++r) {
       const int64_t row = first + r;
+      if constexpr (!kAhead) fetch(row);
       float z[NV];
-      const Raw* src = static_cast<const Raw*>(p.logits) + row * p.E + base;
 #pragma unroll
-      for (int v = 0; v < NV / kPer; ++v) {
-        alignas(16) Raw raw[kPer];
-        if (v * kPer < n) {                                      // vector loads only where every lane's n is a multiple
-          if constexpr (VB == 16) *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(src + v * kPer);
-          else if constexpr (VB == 8) *reinterpret_cast<uint2*>(raw) = *reinterpret_cast<const uint2*>(src + v * kPer);
-          else raw[0] = src[v];
-        } else {
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) raw[i] = Elem::kNegInf;
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const float x = __uint_as_float(Elem::bits(raw[i]));
-          z[v * kPer + i] = x == x ? x : neg_inf();              // not a number: never preferred
-        }
+      for (int i = 0; i < NV; ++i) {
+        const float x = __uint_as_float(Elem::bits(raw[i]));
+        z[i] = x == x ? x : neg_inf();                           // not a number: never preferred
+      }
+      if constexpr (kAhead) {
+        const int64_t then = r + 1 < rows ? row + 1 : first + stride;
+        if (then < p.T) fetch(then);
       }
 
-      // Scores in fp32.  Their error is within tol / 2.
+      // Choice values in fp32.  Their error is within tol / 2.
       float s[NV], tol = 0.f;
-      if (all_scores) {
-        if (p.softmax) {
-          float m = z[0];
+      if constexpr (MODE == 2) {
+        float m = z[0];
 #pragma unroll
-          for (int i = 1; i < NV; ++i) m = fmaxf(m, z[i]);
-          const float row_max = warp_max_f(m);
-          m = row_max > neg_inf() ? row_max : 0.f;
-          float sum = 0.f;
+        for (int i = 1; i < NV; ++i) m = fmaxf(m, z[i]);
+        const float row_max = warp_max_f(m);
+        m = row_max > neg_inf() ? row_max : 0.f;
+        float sum = 0.f;
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            s[i] = ex2_approx((z[i] - m) * kLog2e);
-            sum += s[i];
-          }
-          sum = warp_sum_f(sum);
-          const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-          for (int i = 0; i < NV; ++i) s[i] *= inv;
-          if (lane / kPickLanes == r) {
-            my_max = row_max;
-            my_sum = sum;
-          }
-          // x e^-x <= 0.37: the rounded argument moves a score by 2^-23 * 0.37 * 1.45 of
-          // the row's largest, ex2.approx by 2^-22 of itself, the sum of at most 64
-          // values a lane and 5 steps by 69 * 2^-24 of itself: 5e-6 covers them
-          tol = 1e-5f * inv;
-        } else {
-#pragma unroll
-          for (int i = 0; i < NV; ++i) s[i] = rcp_approx(1.f + ex2_approx(z[i] * -kLog2e));
-          // e = exp(-z) is off by 2^-22 + 2^-24 * 1.45 |z| of itself; s moves by
-          // s (1 - s) of that, below 2^-23, and rcp.approx and 1 + e by 2^-22 of s: 6e-7 covers them
-          tol = 1.2e-6f;
+        for (int i = 0; i < NV; ++i) {
+          s[i] = ex2_approx((z[i] - m) * kLog2e);
+          sum += s[i];
         }
+        sum = warp_sum_f(sum);
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s[i] *= inv;
+        // x e^-x <= 0.37: the rounded argument moves a score by 2^-23 * 0.37 * 1.45 of
+        // the row's largest, ex2.approx by 2^-22 of itself, the sum of at most 64
+        // values a lane and 5 steps by 69 * 2^-24 of itself: 5e-6 covers them
+        tol = 1e-5f * inv;
+        if (lane / kPickLanes == r) {
+          my_max = row_max;
+          my_sum = sum;
+          my_tol = tol;
+        }
+      } else if constexpr (MODE == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s[i] = rcp_approx(1.f + ex2_approx(z[i] * -kLog2e));
+        // e = exp(-z) is off by 2^-22 + 2^-24 * 1.45 |z| of itself; s moves by
+        // s (1 - s) of that, below 2^-23, and rcp.approx and 1 + e by 2^-22 of s: 6e-7 covers them
+        tol = my_tol = 1.2e-6f;
+      }
+      if constexpr (MODE != 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) s[i] = z[i] > neg_inf() ? s[i] + bv[i] : neg_inf();
       }
       uint32_t key[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) key[i] = i < n ? float_key((has_bias ? s[i] : z[i]) + 0.f) : 0u;
+      for (int i = 0; i < NV; ++i) {
+        const float v = MODE != 0 && has_bias ? s[i] : z[i];
+        key[i] = FULL || i < n ? float_key(v + 0.f) : 0u;
+      }
 
-      bool unsure = false;                                       // whether the choice of groups hangs on rounding
+      bool open = g < p.G;                                       // whether the lane's group is a choice
       if (grouped) {
         uint32_t gkey;
         float gtol = tol;
-        if (p.top2) {
+        if (MODE != 0 && p.top2) {
           float a = neg_inf(), b = neg_inf();
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
-            const float v = i < n ? s[i] : neg_inf();
+            const float v = FULL || i < n ? s[i] : neg_inf();
             b = fmaxf(b, fminf(a, v));
             a = fmaxf(a, v);
           }
@@ -305,7 +354,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const __grid_c
             b = fmaxf(fminf(a, a2), fmaxf(b, b2));
             a = fmaxf(a, a2);
           }
-          gkey = g < p.G ? float_key((b > neg_inf() ? a + b : a) + 0.f) : 0u;
+          gkey = float_key((b > neg_inf() ? a + b : a) + 0.f);
           gtol = 2.f * tol;
         } else {
           gkey = key[0];
@@ -313,92 +362,110 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const __grid_c
           for (int i = 1; i < NV; ++i) gkey = max(gkey, key[i]);
           for (int off = 1; off < p.L; off <<= 1) gkey = max(gkey, __shfl_xor_sync(kFull, gkey, off));
         }
-        int rank = 0;
-        for (int o = 0; o < p.G; ++o) {
-          const uint32_t other = __shfl_sync(kFull, gkey, o * p.L);
-          rank += other > gkey || (other == gkey && o < g);
+        if (!open) gkey = 0u;
+        // The best group, `keep` times; groups that tie go by lane, the lower first.
+        open = false;
+        uint32_t worst = 0u;
+        for (int j = 0; j < p.keep; ++j) {
+          worst = __reduce_max_sync(kFull, gkey);
+          const int at = __ffs(__ballot_sync(kFull, gkey == worst)) - 1;
+          if (g == at >> p.lshift) {
+            open = true;
+            gkey = 0u;
+          }
         }
-        const bool kept = rank < p.keep;
-        if (has_bias || p.top2) {
-          const float lo = key_float(__reduce_min_sync(kFull, kept && g < p.G ? gkey : 0xffffffffu));
-          const float hi = key_float(__reduce_max_sync(kFull, kept || g >= p.G ? 0u : gkey));
-          unsure = lo - hi <= gtol + 4.8e-7f * fabsf(lo);        // + the sums' own roundings
+        if (MODE != 0 && (has_bias || p.top2)) {
+          const float lo = key_float(worst), hi = key_float(__reduce_max_sync(kFull, gkey));
+          if (lo - hi <= gtol + 4.8e-7f * fabsf(lo)) unsure_rows |= 1u << r;   // + the sums' own roundings
         }
-        if (!kept)
-#pragma unroll
-          for (int i = 0; i < NV; ++i) key[i] = 0u;
       }
 
-      unsigned long long v[NV];
+      uint32_t best = 0u;
+      if (open) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = (unsigned long long)(key[i]) << 32 | uint32_t(~i);
-      sort_keys<NV>(v);
+        for (int i = 0; i < NV; ++i) best = max(best, key[i]);
+      }
+      uint32_t rest = best, reach = 0u;
 #pragma unroll
-      for (int i = 1; i < kList; ++i) s_list[warp][i][lane] = v[i];
-      uint32_t head = uint32_t(v[0] >> 32), place = ~uint32_t(v[0]);
-      int next = 1;
-      uint32_t ck = 0;                                           // lane j: the j-th largest key and its expert
-      int ce = 0;
-      bool close = false;
-      float prev = __uint_as_float(0x7f800000u);
-      for (int j = 0; j < rounds; ++j) {
-        const uint32_t top = __reduce_max_sync(kFull, head);
-        const int from = __ffs(__ballot_sync(kFull, head == top)) - 1;
-        const int e = __shfl_sync(kFull, base + int(place), from);
-        if (lane == j) {
-          ck = top;
-          ce = e;
+      for (int j = 0; j < kMaxRounds; ++j) {
+        if (j >= rounds) break;
+        reach = __reduce_max_sync(kFull, rest);
+        rest = rest == reach ? 0u : rest;
+      }
+      reach = open ? max(reach, 1u) : 0xffffffffu;               // 0: places without an expert; the last: above every number
+      int count = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) count += key[i] >= reach;
+      int before = count;
+#pragma unroll
+      for (int off = 1; off < kWarp; off <<= 1) {
+        const int o = __shfl_up_sync(kFull, before, off);
+        if (lane >= off) before += o;
+      }
+      const int total = __shfl_sync(kFull, before, kWarp - 1);
+      uint2* ranked = s_ranked[warp][r];
+      if (total <= kWarp) {
+        uint2* at = &s_cand[warp][before - count];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (key[i] >= reach) *at++ = make_uint2(key[i], uint32_t(base + i));
+        if (lane >= total) s_cand[warp][lane] = make_uint2(0u, 0u);
+        __syncwarp();
+        const uint2 mine = s_cand[warp][lane];
+        int rank = 0;
+        for (int o = 0; o < total; o += 4) {
+          const uint4 two = *reinterpret_cast<const uint4*>(&s_cand[warp][o]), more = *reinterpret_cast<const uint4*>(&s_cand[warp][o + 2]);
+          rank += two.x > mine.x;
+          rank += two.z > mine.x;
+          rank += more.x > mine.x;
+          rank += more.z > mine.x;
         }
-        if (lane == from) {
-          const unsigned long long w = next < kList ? s_list[warp][next][lane] : 0ull;
-          head = uint32_t(w >> 32);
-          place = ~uint32_t(w);
-          ++next;
-        }
-        if (has_bias && j <= p.k) {
-          const float c = key_float(top);
-          close |= top != 0u && prev - c <= tol + 2.4e-7f * fabsf(prev);
-          prev = c;
+        rank += __popc(__match_any_sync(kFull, mine.x) & ((1u << lane) - 1u));
+        if (rank < rounds) ranked[rank] = mine;                  // the empty ones come last
+      } else {
+        for (int j = 0; j < rounds; ++j) {
+          const uint32_t top = __reduce_max_sync(kFull, best);
+          const int from = __ffs(__ballot_sync(kFull, best == top)) - 1;
+          if (lane == from) {
+            bool found = false;
+            best = 0u;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+              if (!found && key[i] == top) {
+                found = true;
+                ranked[j] = make_uint2(top, uint32_t(base + i));
+                key[i] = 0u;
+              }
+              best = max(best, key[i]);
+            }
+          }
         }
       }
-      if (close || unsure) {
-        // Values next to one another: sure all the same where their inputs are equal.
-        const bool there = lane < rounds && ck != 0u;
-        const float zc = there ? load_logit<Elem>(p.logits, row * p.E + ce) : neg_inf();
-        const float bc = there && has_bias ? p.bias[ce] : 0.f, c = key_float(ck);
-        const float c_up = __shfl_up_sync(kFull, c, 1), z_up = __shfl_up_sync(kFull, zc, 1), b_up = __shfl_up_sync(kFull, bc, 1);
-        const bool open = close && lane >= 1 && lane <= p.k && there && c_up - c <= tol + 2.4e-7f * fabsf(c_up) &&
-                          !(zc == z_up && bc == b_up);
-        const float last = __shfl_sync(kFull, c, p.k - 1);
-        const bool beyond = lane == p.k + 1 && there && last - c <= tol + 2.4e-7f * fabsf(last);
-        const bool any_open = __any_sync(kFull, open), any_beyond = __any_sync(kFull, beyond);
-        if (unsure || (any_open && (any_beyond || p.softmax))) {
-          ce = route_row_double<Elem>(p, row, lane);
-        } else if (any_open) {
-          // The k + 1 largest are known as a set: one double-precision sigmoid a lane orders them.
-          const bool in = there && lane <= p.k;
-          const double d = in && zc > neg_inf() ? 1.0 / (1.0 + exp(-double(zc))) + double(bc) : double(neg_inf());
-          int rank = 0;
-          for (int o = 0; o <= p.k; ++o) {
-            const double od = __shfl_sync(kFull, d, o);
-            const int oe = __shfl_sync(kFull, ce, o);
-            rank += __shfl_sync(kFull, int(in), o) != 0 && (od > d || (od == d && oe < ce));
-          }
-          int to = ce;
-          for (int o = 0; o <= p.k; ++o) {
-            const int orank = __shfl_sync(kFull, in ? rank : kWarp, o), oe = __shfl_sync(kFull, ce, o);
-            if (orank == lane) to = oe;
-          }
-          ce = to;
-        }
+      __syncwarp();
+      if (MODE != 0 && has_bias) {
+        const uint32_t ck = lane < rounds ? ranked[lane].x : 0u;
+        const float c = key_float(ck), c_up = __shfl_up_sync(kFull, c, 1);
+        if (__any_sync(kFull, lane >= 1 && lane <= p.k && ck != 0u && c_up - c <= tol + 2.4e-7f * fabsf(c_up))) close_rows |= 1u << r;
       }
-      const int pe = __shfl_sync(kFull, ce, lane % kPickLanes);
-      if (lane / kPickLanes == r) my_e = pe;
-      __syncwarp();                                              // the lists are read before the next row's are written
+    }
+    if (MODE != 0 && (close_rows | unsure_rows) != 0u) {
+      for (unsigned left = close_rows | unsure_rows; left != 0u; left &= left - 1u) {
+        const int r = __ffs(left) - 1;
+        const uint2 c = lane < rounds ? s_ranked[warp][r][lane] : make_uint2(0u, 0u);
+        const int e = route_settle<Elem>(p, first + r, lane, c.x, int(c.y), rounds, __shfl_sync(kFull, my_tol, r * kPickLanes),
+                                         close_rows >> r & 1, unsure_rows >> r & 1);
+        if (lane < p.k) s_ranked[warp][r][lane].y = uint32_t(e);
+        __syncwarp();
+      }
+      // Read again, so that nothing of a row's size is kept across the calls.
+      fetch_bias();
+      if (kAhead && first + stride < p.T) fetch(first + stride);
     }
 
     const int64_t row = first + lane / kPickLanes;
-    const bool pick = lane / kPickLanes < per && row < p.T && lane % kPickLanes < p.k;
+    const bool pick = lane / kPickLanes < rows && lane % kPickLanes < p.k;
+    const int my_e = pick ? int(s_ranked[warp][lane / kPickLanes][lane % kPickLanes].y) : 0;
+    __syncwarp();                                                // read before the next rows' are written
     const float zp = pick ? load_logit<Elem>(p.logits, row * p.E + my_e) : neg_inf();
     float w;
     if (p.renorm) {
@@ -445,11 +512,11 @@ __global__ void __launch_bounds__(256) route_bias_kernel(const RouteParams p) {
 // 16 warps an SM.
 int rows_per_warp(int64_t T, int sms) { return T >= int64_t(sms) * 64 ? 4 : 1; }
 
-template <class Elem, int NV, int VB>
+template <class Elem, int NV, int VB, bool FULL, int MODE>
 cudaError_t fwd_launch(const RouteParams& p, int sms, cudaStream_t stream) {
   const size_t smem = size_t(p.E) * sizeof(int);
   if (p.T <= kRouteOneCtaRows) {
-    route_fwd_kernel<Elem, NV, VB><<<1, kRouteThreads, smem, stream>>>(p, 1);
+    route_fwd_kernel<Elem, NV, VB, FULL, MODE><<<1, kRouteThreads, smem, stream>>>(p, 1);
     return cudaGetLastError();
   }
   cudaError_t e = cudaMemsetAsync(p.counts, 0, smem, stream);
@@ -457,37 +524,40 @@ cudaError_t fwd_launch(const RouteParams& p, int sms, cudaStream_t stream) {
   const int per = rows_per_warp(p.T, sms);
   const int64_t rows = int64_t(kRouteWarps) * per, want = (p.T + rows - 1) / rows;
   const int64_t most = int64_t(sms) * 8;
-  route_fwd_kernel<Elem, NV, VB><<<int(want < most ? want : most), kRouteThreads, smem, stream>>>(p, per);
+  route_fwd_kernel<Elem, NV, VB, FULL, MODE><<<int(want < most ? want : most), kRouteThreads, smem, stream>>>(p, per);
   if ((e = cudaGetLastError()) != cudaSuccess || p.bias_out == nullptr) return e;
   route_bias_kernel<<<(p.E + 255) / 256, 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <class Elem, int NV>
+template <class Elem, int NV, int MODE>
 cudaError_t fwd_width(const RouteParams& p, int sms, cudaStream_t stream) {
-  constexpr int kSize = int(sizeof(typename Elem::Raw));
-  // A load of VB bytes needs every lane's first expert on a multiple of VB and
-  // whole vectors: full groups and chunks, rows and the array aligned.
-  const bool full = p.gs == p.L * p.chunk;
-  const auto fits = [&](int vb) {
-    return full && p.chunk * kSize % vb == 0 && p.gs * kSize % vb == 0 && int64_t(p.E) * kSize % vb == 0 &&
-           reinterpret_cast<uintptr_t>(p.logits) % vb == 0;
-  };
-  if constexpr (NV * kSize % 16 == 0)
-    if (fits(16)) return fwd_launch<Elem, NV, 16>(p, sms, stream);
-  if constexpr (NV * kSize % 8 == 0)
-    if (fits(8)) return fwd_launch<Elem, NV, 8>(p, sms, stream);
-  return fwd_launch<Elem, NV, kSize>(p, sms, stream);
+  constexpr int kSize = int(sizeof(typename Elem::Raw)), kRow = NV * kSize;
+  constexpr int VB = kRow % 16 == 0 ? 16 : kRow % 8 == 0 ? 8 : 4;
+  // Loads of VB bytes: every lane has NV experts, and rows, groups and the array are aligned.
+  const bool full = p.chunk == NV && p.gs == p.L * p.chunk;
+  if (full && int64_t(p.E) * kSize % VB == 0 && reinterpret_cast<uintptr_t>(p.logits) % VB == 0)
+    return fwd_launch<Elem, NV, VB, true, MODE>(p, sms, stream);
+  return fwd_launch<Elem, NV, kSize, false, MODE>(p, sms, stream);
+}
+
+template <class Elem, int MODE>
+cudaError_t fwd_mode(const RouteParams& p, int sms, cudaStream_t stream) {
+  if (p.chunk <= 2) return fwd_width<Elem, 2, MODE>(p, sms, stream);
+  if (p.chunk <= 4) return fwd_width<Elem, 4, MODE>(p, sms, stream);
+  if (p.chunk <= 8) return fwd_width<Elem, 8, MODE>(p, sms, stream);
+  if (p.chunk <= 12) return fwd_width<Elem, 12, MODE>(p, sms, stream);
+  if (p.chunk <= 16) return fwd_width<Elem, 16, MODE>(p, sms, stream);
+  if (p.chunk <= 32) return fwd_width<Elem, 32, MODE>(p, sms, stream);
+  return fwd_launch<Elem, 64, int(sizeof(typename Elem::Raw)), false, MODE>(p, sms, stream);
 }
 
 template <class Elem>
 cudaError_t fwd_elem(const RouteParams& p, int sms, cudaStream_t stream) {
-  if (p.chunk <= 4) return fwd_width<Elem, 4>(p, sms, stream);
-  if (p.chunk <= 8) return fwd_width<Elem, 8>(p, sms, stream);
-  if (p.chunk <= 12) return fwd_width<Elem, 12>(p, sms, stream);
-  if (p.chunk <= 16) return fwd_width<Elem, 16>(p, sms, stream);
-  if (p.chunk <= 32) return fwd_width<Elem, 32>(p, sms, stream);
-  return fwd_width<Elem, 64>(p, sms, stream);
+  const bool grouped = p.keep < p.G;
+  if (p.softmax && (p.bias != nullptr || (p.top2 && grouped) || !p.renorm)) return fwd_mode<Elem, 2>(p, sms, stream);
+  if (!p.softmax && (p.bias != nullptr || (p.top2 && grouped))) return fwd_mode<Elem, 1>(p, sms, stream);
+  return fwd_mode<Elem, 0>(p, sms, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -609,13 +679,4 @@ cudaError_t bwd_elem(const RouteBwdParams& p, int sms, cudaStream_t stream) {
 }
 
 }  // namespace
-
-cudaError_t launch_route_fwd(const RouteParams& p, bool bf16, int sms, cudaStream_t stream) {
-  return bf16 ? fwd_elem<Bf16>(p, sms, stream) : fwd_elem<Fp32>(p, sms, stream);
-}
-
-cudaError_t launch_route_bwd(const RouteBwdParams& p, bool bf16, int sms, cudaStream_t stream) {
-  return bf16 ? bwd_elem<Bf16>(p, sms, stream) : bwd_elem<Fp32>(p, sms, stream);
-}
-
 }  // namespace moe

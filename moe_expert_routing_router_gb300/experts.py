@@ -26,9 +26,12 @@ __all__ = [
     "moe_expert_combine_bwd",
 ]
 
+_VALUES = tuple(_DTYPES)                       # fp32 and bf16
+_I32, _F32 = (torch.int32,), (torch.float32,)
 _SCORES = {"sigmoid": 0, "softmax": 1}
 _GROUP_SCORES = {"max": 0, "top2": 1}
 _F8 = torch.float8_e4m3fn
+_CODES = (_F8,)
 _BLOCK = 128
 
 
@@ -61,22 +64,29 @@ def _entry(fn):
     return call
 
 
-def _need(name: str, t: torch.Tensor, device: torch.device, dtype: torch.dtype, shape: tuple | None = None) -> None:
-    """A contiguous CUDA tensor on `device`, of `dtype` and `shape` (None in a shape: any length)."""
-    _need_cuda(name, t, dtype)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's tensors on {device}")
-    if shape is not None and t.shape != shape and (
-            t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
-        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-
-
-def _need_values(name: str, t: torch.Tensor, dim: int, device: torch.device | None = None) -> None:
+def _fault(name: str, t, index: int | None, dtypes, shape) -> None:
+    """Says what is wrong with an argument that `_ok` has refused."""
     _need_cuda(name, t)
-    if t.dtype not in _DTYPES or t.dim() != dim:
-        raise ValueError(f"{name} must be a {dim}-D float32 or bfloat16 tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's tensors on {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors on cuda:{index}")
+    raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+
+
+def _need(name: str, t: torch.Tensor, index: int, dtype: torch.dtype, shape: tuple) -> None:
+    """A contiguous CUDA tensor on device `index`, of `dtype` and `shape`."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _fault(name, t, index, (dtype,), shape)
+
+
+def _need_dims(name: str, t: torch.Tensor, dims: int, dtypes, index: int | None = None) -> torch.Size:
+    """As `_need` for a tensor whose lengths the call takes from it; returns them.  Without an index the tensor
+    decides the call's device."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == dims and t.is_contiguous()
+            and (index is None or t.get_device() == index)):
+        _fault(name, t, index, dtypes, f"{dims}-D")
+    return t.shape
 
 
 def _choice(name: str, value, table: dict) -> int:
@@ -99,17 +109,16 @@ def moe_route_fwd(logits: torch.Tensor, k: int, score: str = "sigmoid", bias: to
     Returns idx [T, k] int32 (largest choice value first), gate [T, k] fp32 and
     counts [E] int32; and ``bias_out`` when an update is asked for: a tensor to
     receive it (it may be ``bias`` itself), or True for a new one."""
-    _need_values("logits", logits, 2)
-    T, E = logits.shape
-    dev = logits.device
+    T, E = _need_dims("logits", logits, 2, _VALUES)
+    dev, at = logits.device, logits.get_device()
     if bias is not None:
-        _need("bias", bias, dev, torch.float32, (E,))
+        _need("bias", bias, at, torch.float32, (E,))
     if bias_out is True:
         bias_out = torch.empty(E, dtype=torch.float32, device=dev)
     elif bias_out is False:
         bias_out = None
     if bias_out is not None:
-        _need("bias_out", bias_out, dev, torch.float32, (E,))
+        _need("bias_out", bias_out, at, torch.float32, (E,))
     sc, gs = _choice("score", score, _SCORES), _choice("group_score", group_score, _GROUP_SCORES)
     k = int(k)
     o = {"idx": _out(out, "idx", (T, max(k, 0)), torch.int32, dev),
@@ -128,14 +137,14 @@ def moe_route_bwd(logits: torch.Tensor, idx: torch.Tensor, dgate: torch.Tensor, 
                   renorm: int = -1, scale: float = 1.0, dlogits: torch.Tensor | None = None,
                   stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """dL/dlogits [T, E] fp32 from the gates' gradient dgate [T, k], picks held constant (C: moe_route_bwd)."""
-    _need_values("logits", logits, 2)
-    T, E = logits.shape
-    dev = logits.device
-    _need("idx", idx, dev, torch.int32, (T, None))
-    _need("dgate", dgate, dev, torch.float32, tuple(idx.shape))
+    T, E = _need_dims("logits", logits, 2, _VALUES)
+    dev, at = logits.device, logits.get_device()
+    k = _need_dims("idx", idx, 2, _I32, at)[1]
+    _need("idx", idx, at, torch.int32, (T, k))
+    _need("dgate", dgate, at, torch.float32, (T, k))
     sc = _choice("score", score, _SCORES)
     dl = _out({"dlogits": dlogits}, "dlogits", (T, E), torch.float32, dev)
-    check(lib().moe_route_bwd(_ptr(logits), _DTYPES[logits.dtype], T, E, idx.shape[1], sc, int(renorm), float(scale),
+    check(lib().moe_route_bwd(_ptr(logits), _DTYPES[logits.dtype], T, E, k, sc, int(renorm), float(scale),
                               _ptr(idx), _ptr(dgate), _ptr(dl), _stream()), "moe_route_bwd")
     return dl
 
@@ -144,8 +153,7 @@ def _gathered(x: torch.Tensor, perm: torch.Tensor | None) -> int:
     """Rows of the quantised output."""
     if perm is None:
         return x.shape[0]
-    _need("perm", perm, x.device, torch.int32, (None,))
-    return perm.shape[0]
+    return _need_dims("perm", perm, 1, _I32, x.get_device())[0]
 
 
 @_entry
@@ -153,8 +161,7 @@ def moe_quantize_rows(x: torch.Tensor, perm: torch.Tensor | None = None, k: int 
                       stream: torch.cuda.Stream | None = None) -> dict:
     """q [M, K] e4m3 and scale [ceil(K/128), M] of the rows of x, or of rows perm[r] // k of x: the token rows in
     dispatch order (C: moe_quantize_rows)."""
-    _need_values("x", x, 2)
-    rows, K = x.shape
+    rows, K = _need_dims("x", x, 2, _VALUES)
     M = _gathered(x, perm)
     o = {"q": _out(out, "q", (M, K), _F8, x.device),
          "scale": _out(out, "scale", (_blocks(K), M), torch.float32, x.device)}
@@ -177,14 +184,12 @@ def moe_quantize_cols(x: torch.Tensor, offsets: torch.Tensor, kept: torch.Tensor
                       stream: torch.cuda.Stream | None = None) -> dict:
     """q [K, width] e4m3 and scale [width/128, K]: every expert's rows of x (or of rows perm[r] // k of x) in blocks of
     128 rows by one column, transposed, as moe_expert_wgrad takes them (C: moe_quantize_cols)."""
-    _need_values("x", x, 2)
-    rows, K = x.shape
-    dev = x.device
+    rows, K = _need_dims("x", x, 2, _VALUES)
+    dev, at = x.device, x.get_device()
     M = _gathered(x, perm)
-    _need("offsets", offsets, dev, torch.int32, (None,))
-    E = offsets.shape[0] - 1
+    E = _need_dims("offsets", offsets, 1, _I32, at)[0] - 1
     if kept is not None:
-        _need("kept", kept, dev, torch.int32, (E,))
+        _need("kept", kept, at, torch.int32, (E,))
     width = moe_quantize_cols_width(M, E)
     o = {"q": _out(out, "q", (K, width), _F8, dev),
          "scale": _out(out, "scale", (width // _BLOCK, K), torch.float32, dev)}
@@ -198,8 +203,7 @@ def moe_quantize_weights(w: torch.Tensor, transposed: bool = False, out: dict | 
                          stream: torch.cuda.Stream | None = None) -> dict:
     """q [E, N, K] e4m3 and scale [E, ceil(N/128), ceil(K/128)] of w [E, N, K]; with ``transposed`` also qt [E, K, N] and
     scalet [E, ceil(K/128), ceil(N/128)], the weights of the data gradient (C: moe_quantize_weights)."""
-    _need_values("w", w, 3)
-    E, N, K = w.shape
+    E, N, K = _need_dims("w", w, 3, _VALUES)
     dev = w.device
     o = {"q": _out(out, "q", (E, N, K), _F8, dev),
          "scale": _out(out, "scale", (E, _blocks(N), _blocks(K)), torch.float32, dev)}
@@ -219,24 +223,21 @@ def moe_expert_matmul(q: torch.Tensor, scale: torch.Tensor, wq: torch.Tensor, ws
     """out [M, N]: the rows offsets[e] .. offsets[e] + kept[e] of q (scaled) times expert e's weights wq [E, N, K]
     (scaled), transposed (C: moe_expert_matmul).  Other rows of ``out`` are left as they are.  Without offsets, one
     expert takes all rows.  ``out``, when given, decides the type."""
-    _need_cuda("q", q, _F8)
-    if q.dim() != 2:
-        raise ValueError("q must be [M, K]")
-    M, K = q.shape
-    dev = q.device
-    _need("wq", wq, dev, _F8, (None, None, K))
-    E, N, _ = wq.shape
-    _need("scale", scale, dev, torch.float32, (_blocks(K), M))
-    _need("wscale", wscale, dev, torch.float32, (E, _blocks(N), _blocks(K)))
+    M, K = _need_dims("q", q, 2, _CODES)
+    at = q.get_device()
+    E, N, _ = _need_dims("wq", wq, 3, _CODES, at)
+    _need("wq", wq, at, _F8, (E, N, K))
+    _need("scale", scale, at, torch.float32, (_blocks(K), M))
+    _need("wscale", wscale, at, torch.float32, (E, _blocks(N), _blocks(K)))
     if offsets is not None:
-        _need("offsets", offsets, dev, torch.int32, (E + 1,))
+        _need("offsets", offsets, at, torch.int32, (E + 1,))
     if kept is not None:
-        _need("kept", kept, dev, torch.int32, (E,))
+        _need("kept", kept, at, torch.int32, (E,))
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in _DTYPES:
         raise ValueError("the result must be float32 or bfloat16")
-    y = _out({"out": out}, "out", (M, N), out_dtype, dev)
+    y = _out({"out": out}, "out", (M, N), out_dtype, q.device)
     check(lib().moe_expert_matmul(_ptr(q), _ptr(scale), M, K, _ptr(wq), _ptr(wscale), E, N, _ptr(offsets), _ptr(kept),
                                   _DTYPES[out_dtype], _ptr(y), _stream()), "moe_expert_matmul")
     return y
@@ -246,20 +247,16 @@ def moe_expert_matmul(q: torch.Tensor, scale: torch.Tensor, wq: torch.Tensor, ws
 def moe_expert_wgrad(dyq: torch.Tensor, dyscale: torch.Tensor, xq: torch.Tensor, xscale: torch.Tensor, kept: torch.Tensor,
                      out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """dw [E, N, K] fp32 = sum over every expert's rows of dy^T x, from moe_quantize_cols of dy and x (C: moe_expert_wgrad)."""
-    _need_cuda("dyq", dyq, _F8)
-    if dyq.dim() != 2:
-        raise ValueError("dyq must be [N, width]")
-    N, width = dyq.shape
-    dev = dyq.device
+    N, width = _need_dims("dyq", dyq, 2, _CODES)
+    at = dyq.get_device()
     if width % _BLOCK != 0:
         raise ValueError("the columns of dyq must be whole blocks of 128")
-    _need("xq", xq, dev, _F8, (None, width))
-    K = xq.shape[0]
-    _need("dyscale", dyscale, dev, torch.float32, (width // _BLOCK, N))
-    _need("xscale", xscale, dev, torch.float32, (width // _BLOCK, K))
-    _need("kept", kept, dev, torch.int32, (None,))
-    E = kept.shape[0]
-    dw = _out({"out": out}, "out", (E, N, K), torch.float32, dev)
+    K = _need_dims("xq", xq, 2, _CODES, at)[0]
+    _need("xq", xq, at, _F8, (K, width))
+    _need("dyscale", dyscale, at, torch.float32, (width // _BLOCK, N))
+    _need("xscale", xscale, at, torch.float32, (width // _BLOCK, K))
+    E = _need_dims("kept", kept, 1, _I32, at)[0]
+    dw = _out({"out": out}, "out", (E, N, K), torch.float32, dyq.device)
     check(lib().moe_expert_wgrad(_ptr(dyq), _ptr(dyscale), _ptr(xq), _ptr(xscale), width, N, K, E, _ptr(kept), _ptr(dw),
                                  _stream()), "moe_expert_wgrad")
     return dw
@@ -275,16 +272,15 @@ def moe_expert_device_status(stream: torch.cuda.Stream | None = None) -> int:
     return int(flags.value)
 
 
-def _assignments(idx, slot, offsets, gate, dev) -> tuple[int, int, int]:
-    _need("idx", idx, dev, torch.int32, (None, None))
-    T, k = idx.shape
-    _need("slot", slot, dev, torch.int32)
+def _assignments(idx, slot, offsets, gate, at: int) -> tuple[int, int, int]:
+    T, k = _need_dims("idx", idx, 2, _I32, at)
     if slot.numel() != T * k:
         raise ValueError("slot must have T*k elements")
-    _need("offsets", offsets, dev, torch.int32, (None,))
+    _need("slot", slot, at, torch.int32, slot.shape)
+    E = _need_dims("offsets", offsets, 1, _I32, at)[0] - 1
     if gate is not None:
-        _need("gate", gate, dev, torch.float32, (T, k))
-    return T, k, offsets.shape[0] - 1
+        _need("gate", gate, at, torch.float32, (T, k))
+    return T, k, E
 
 
 @_entry
@@ -292,9 +288,8 @@ def moe_expert_combine(y: torch.Tensor, idx: torch.Tensor, slot: torch.Tensor, o
                        gate: torch.Tensor | None = None, out: torch.Tensor | None = None,
                        stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """out [T, H]: every token's kept rows of y [M, H], summed by gate, or plainly without one (C: moe_expert_combine)."""
-    _need_values("y", y, 2)
-    M, H = y.shape
-    T, k, E = _assignments(idx, slot, offsets, gate, y.device)
+    M, H = _need_dims("y", y, 2, _VALUES)
+    T, k, E = _assignments(idx, slot, offsets, gate, y.get_device())
     o = _out({"out": out}, "out", (T, H), y.dtype, y.device)
     check(lib().moe_expert_combine(_ptr(y), _DTYPES[y.dtype], M, H, T, k, E, _ptr(idx), _ptr(slot), _ptr(offsets),
                                    _ptr(gate), _ptr(o), _stream()), "moe_expert_combine")
@@ -307,16 +302,13 @@ def moe_expert_combine_bwd(dout: torch.Tensor, y: torch.Tensor, idx: torch.Tenso
                            stream: torch.cuda.Stream | None = None) -> dict:
     """dy [M, H] (rows of kept assignments; others are left as they are) and dgate [T, k] fp32 of
     moe_expert_combine (C: moe_expert_combine_bwd)."""
-    _need_values("dout", dout, 2)
-    dev = dout.device
-    _need_values("y", y, 2, dev)
-    if y.dtype != dout.dtype:
-        raise ValueError("dout and y must have one type")
-    M, H = y.shape
-    _need_cuda("gate", gate, torch.float32)
-    T, k, E = _assignments(idx, slot, offsets, gate, dev)
-    if tuple(dout.shape) != (T, H):
-        raise ValueError(f"dout must be {(T, H)}, got {tuple(dout.shape)}")
+    _need_dims("dout", dout, 2, _VALUES)
+    dev, at = dout.device, dout.get_device()
+    M, H = _need_dims("y", y, 2, (dout.dtype,), at)
+    if gate is None:
+        raise ValueError("gate must be a CUDA tensor")
+    T, k, E = _assignments(idx, slot, offsets, gate, at)
+    _need("dout", dout, at, y.dtype, (T, H))
     o = {"dy": _out(out, "dy", (M, H), y.dtype, dev), "dgate": _out(out, "dgate", (T, k), torch.float32, dev)}
     check(lib().moe_expert_combine_bwd(_ptr(dout), _ptr(y), _DTYPES[y.dtype], M, H, T, k, E, _ptr(idx), _ptr(slot),
                                        _ptr(offsets), _ptr(gate), _ptr(o["dy"]), _ptr(o["dgate"]), _stream()),
