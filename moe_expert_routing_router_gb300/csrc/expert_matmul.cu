@@ -34,7 +34,8 @@ namespace {
 
 constexpr int kBM = 128;                      // rows of a tile
 constexpr int kBK = 128;                      // block along the contraction: bytes of e4m3, and one scale
-constexpr int kBoxA = 32, kBoxB = 64;         // rows of one copy: a ragged tile copies only the boxes that it needs
+constexpr int kBox = 32;                      // rows of one copy of a ragged tile, which copies only those it needs; a whole
+                                              // one takes one copy of 128 rows (an issue costs some 30 ns)
 constexpr int kEpiWarps = 16, kFirstEpi = 4;
 constexpr int kMmThreads = (kFirstEpi + kEpiWarps) * kWarp;
 constexpr int kTmemCols = 512;
@@ -236,6 +237,8 @@ __device__ __forceinline__ void expert_rows(const MatmulParams& p, int e, int64_
   *n = p.kept != nullptr ? min(hi - lo, max(int64_t(p.kept[e]), int64_t(0))) : hi - lo;
 }
 
+__device__ __forceinline__ int boxes(int rows) { return (rows + kBox - 1) / kBox; }
+
 // A tile of the persistent loop, walked in ascending order by every role.
 struct Walk {
   int e = 0;
@@ -283,7 +286,8 @@ struct Walk {
 
 template <int BN, int CG, bool WGRAD, bool BF16>
 __global__ void __launch_bounds__(kMmThreads, 1)
-expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
+expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                     const __grid_constant__ CUtensorMap whole_a, const __grid_constant__ CUtensorMap whole_b) {
   using TL = Tile<BN, CG>;
   extern __shared__ uint8_t s_dyn[];
   __shared__ Shared sh;
@@ -370,13 +374,11 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       Walk w;
       for (int tile = first_tile; tile < n_tiles && ok; tile += tile_step) {
         w.at<BN, CG, WGRAD>(p, sh, tile, rank);
-        const int na = (w.rows + kBoxA - 1) / kBoxA;
-        const int nb = (Walk::share(w.cols, rank, TL::kShareB) + kBoxB - 1) / kBoxB;
+        const int na = boxes(w.rows), nb = boxes(Walk::share(w.cols, rank, TL::kShareB));
         const int b_row = (WGRAD ? w.col0 : w.e * p.C + w.col0) + rank * TL::kShareB;
         int bytes = 0;                                           // of both CTAs: the first one's barrier counts them
         for (int r = 0; r < CG; ++r)
-          bytes += ((Walk::share(w.pair_rows, r, kBM) + kBoxA - 1) / kBoxA * kBoxA +
-                    (Walk::share(w.cols, r, TL::kShareB) + kBoxB - 1) / kBoxB * kBoxB) * kBK;
+          bytes += (boxes(Walk::share(w.pair_rows, r, kBM)) + boxes(Walk::share(w.cols, r, TL::kShareB))) * kBox * kBK;
         for (int b = 0; b < w.blocks; ++b) {
           ok = __all_sync(kFull, mm_wait(sh, p, &sh.done[s], phase ^ 1u));
           if (!ok) break;
@@ -386,8 +388,10 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
             if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], uint32_t(bytes));
             const uint32_t bar = CG == 2 ? first_cta_addr(&sh.full[s]) : smem_addr(&sh.full[s]);
             const int x = (w.block0 + b) * kBK;
-            for (int i = 0; i < na; ++i) tma_2d<CG>(sa + i * kBoxA * kBK, &map_a, x, w.row0 + i * kBoxA, bar);
-            for (int i = 0; i < nb; ++i) tma_2d<CG>(sb + i * kBoxB * kBK, &map_b, x, b_row + i * kBoxB, bar);
+            if (na == kBM / kBox) tma_2d<CG>(sa, &whole_a, x, w.row0, bar);
+            else for (int i = 0; i < na; ++i) tma_2d<CG>(sa + i * kBox * kBK, &map_a, x, w.row0 + i * kBox, bar);
+            if (nb == TL::kShareB / kBox) tma_2d<CG>(sb, &whole_b, x, b_row, bar);
+            else for (int i = 0; i < nb; ++i) tma_2d<CG>(sb + i * kBox * kBK, &map_b, x, b_row + i * kBox, bar);
           }
           __syncwarp();
           ++issued;
@@ -615,17 +619,18 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, 
 
 template <int BN, int CG, bool WGRAD, bool BF16>
 cudaError_t launch(const MatmulParams& p, int sms, const char** error, cudaStream_t stream) {
-  CUtensorMap ma, mb;
+  using TL = Tile<BN, CG>;
+  CUtensorMap ma, mb, wa, wb;
   const uint64_t cols = WGRAD ? uint64_t(p.blocks) * kBK : uint64_t(p.K);
   const uint64_t rows_a = WGRAD ? uint64_t(p.R) : uint64_t(p.M), rows_b = WGRAD ? uint64_t(p.C) : uint64_t(p.E) * p.C;
-  if (!make_map(&ma, p.a, rows_a, cols, kBoxA) || !make_map(&mb, p.b, rows_b, cols, kBoxB)) {
+  if (!make_map(&ma, p.a, rows_a, cols, kBox) || !make_map(&mb, p.b, rows_b, cols, kBox) ||
+      !make_map(&wa, p.a, rows_a, cols, kBM) || !make_map(&wb, p.b, rows_b, cols, TL::kShareB)) {
     *error = "cuTensorMapEncodeTiled refused an operand";
     return cudaErrorUnknown;
   }
-  using TL = Tile<BN, CG>;
   constexpr size_t smem = size_t(TL::kStages) * TL::kStageBytes + 1024;
   static_assert(TL::kStages <= 8 && TL::kBufs <= 8 && sizeof(Shared) + smem <= 232448, "shared memory of one CTA");
-  static_assert(TL::kShareB % kBoxB == 0 && TL::kStageBytes % 1024 == 0, "whole boxes, swizzle atoms aligned");
+  static_assert(TL::kShareB % kBox == 0 && TL::kStageBytes % 1024 == 0, "whole boxes, swizzle atoms aligned");
   const auto kernel = expert_matmul_kernel<BN, CG, WGRAD, BF16>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
@@ -646,7 +651,7 @@ cudaError_t launch(const MatmulParams& p, int sms, const char** error, cudaStrea
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = CG > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p, ma, mb);
+  return cudaLaunchKernelEx(&cfg, kernel, p, ma, mb, wa, wb);
 }
 
 }  // namespace
