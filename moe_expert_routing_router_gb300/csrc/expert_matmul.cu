@@ -178,13 +178,15 @@ __device__ __forceinline__ void turn(uint4* v, int lane) {
 }
 
 // ---- the kernel ----------------------------------------------------------------
-template <int BN, int CG>
+// RB: blocks that share a stage, its barriers and its place in tensor memory.
+template <int BN, int CG, int RB>
 struct Tile {
   static constexpr int kRows = kBM * CG;                       // of the CTAs together
   static constexpr int kShareB = BN / CG;                      // rows of b that a CTA holds
-  static constexpr int kStageBytes = (kBM + kShareB) * kBK;
+  static constexpr int kBlockBytes = (kBM + kShareB) * kBK;
+  static constexpr int kStageBytes = RB * kBlockBytes;
   static constexpr int kStages = 196608 / kStageBytes;         // 192 KB of operands
-  static constexpr int kBufs = kTmemCols / BN;                 // block products in tensor memory
+  static constexpr int kBufs = kTmemCols / (BN * RB);          // stages' products in tensor memory
   static constexpr int kCols = BN / 4;                         // columns of one epilogue warp
 };
 
@@ -251,9 +253,9 @@ struct Walk {
   // The part of n that CTA `rank` has when each has `each`.
   __device__ __forceinline__ static int share(int n, int rank, int each) { return max(0, min(each, n - rank * each)); }
 
-  template <int BN, int CG, bool WGRAD>
+  template <class TL, int BN, bool WGRAD>
   __device__ __forceinline__ void at(const MatmulParams& p, const Shared& sh, int tile, int rank) {
-    constexpr int kRows = Tile<BN, CG>::kRows;
+    constexpr int kRows = TL::kRows;
     while (sh.first[e + 1] <= tile) ++e;
     const int i = tile - sh.first[e];
     const int ct = (p.C + BN - 1) / BN;
@@ -284,11 +286,11 @@ struct Walk {
   }
 };
 
-template <int BN, int CG, bool WGRAD, bool BF16>
+template <int BN, int CG, int RB, bool WGRAD, bool BF16>
 __global__ void __launch_bounds__(kMmThreads, 1)
 expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                      const __grid_constant__ CUtensorMap whole_a, const __grid_constant__ CUtensorMap whole_b) {
-  using TL = Tile<BN, CG>;
+  using TL = Tile<BN, CG, RB>;
   extern __shared__ uint8_t s_dyn[];
   __shared__ Shared sh;
   uint8_t* ring = s_dyn + (1024 - smem_addr(s_dyn) % 1024) % 1024;     // the same place in both CTAs of a pair
@@ -373,25 +375,28 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       bool ok = true;
       Walk w;
       for (int tile = first_tile; tile < n_tiles && ok; tile += tile_step) {
-        w.at<BN, CG, WGRAD>(p, sh, tile, rank);
+        w.at<TL, BN, WGRAD>(p, sh, tile, rank);
         const int na = boxes(w.rows), nb = boxes(Walk::share(w.cols, rank, TL::kShareB));
         const int b_row = (WGRAD ? w.col0 : w.e * p.C + w.col0) + rank * TL::kShareB;
         int bytes = 0;                                           // of both CTAs: the first one's barrier counts them
         for (int r = 0; r < CG; ++r)
           bytes += (boxes(Walk::share(w.pair_rows, r, kBM)) + boxes(Walk::share(w.cols, r, TL::kShareB))) * kBox * kBK;
-        for (int b = 0; b < w.blocks; ++b) {
+        for (int b = 0; b < w.blocks; b += RB) {
+          const int now = RB == 1 ? 1 : min(RB, w.blocks - b);
           ok = __all_sync(kFull, mm_wait(sh, p, &sh.done[s], phase ^ 1u));
           if (!ok) break;
           if (elect_one()) {
-            uint8_t* sa = ring + s * TL::kStageBytes;
-            uint8_t* sb = sa + kBM * kBK;
-            if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], uint32_t(bytes));
+            if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], uint32_t(bytes * now));
             const uint32_t bar = CG == 2 ? first_cta_addr(&sh.full[s]) : smem_addr(&sh.full[s]);
-            const int x = (w.block0 + b) * kBK;
-            if (na == kBM / kBox) tma_2d<CG>(sa, &whole_a, x, w.row0, bar);
-            else for (int i = 0; i < na; ++i) tma_2d<CG>(sa + i * kBox * kBK, &map_a, x, w.row0 + i * kBox, bar);
-            if (nb == TL::kShareB / kBox) tma_2d<CG>(sb, &whole_b, x, b_row, bar);
-            else for (int i = 0; i < nb; ++i) tma_2d<CG>(sb + i * kBox * kBK, &map_b, x, b_row + i * kBox, bar);
+            for (int j = 0; j < now; ++j) {
+              uint8_t* sa = ring + s * TL::kStageBytes + j * TL::kBlockBytes;
+              uint8_t* sb = sa + kBM * kBK;
+              const int x = (w.block0 + b + j) * kBK;
+              if (na == kBM / kBox) tma_2d<CG>(sa, &whole_a, x, w.row0, bar);
+              else for (int i = 0; i < na; ++i) tma_2d<CG>(sa + i * kBox * kBK, &map_a, x, w.row0 + i * kBox, bar);
+              if (nb == TL::kShareB / kBox) tma_2d<CG>(sb, &whole_b, x, b_row, bar);
+              else for (int i = 0; i < nb; ++i) tma_2d<CG>(sb + i * kBox * kBK, &map_b, x, b_row + i * kBox, bar);
+            }
           }
           __syncwarp();
           ++issued;
@@ -419,16 +424,20 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       bool ok = true;
       Walk w;
       for (int tile = first_tile; tile < n_tiles && ok; tile += tile_step) {
-        w.at<BN, CG, WGRAD>(p, sh, tile, rank);
-        for (int b = 0; b < w.blocks; ++b) {
+        w.at<TL, BN, WGRAD>(p, sh, tile, rank);
+        for (int b = 0; b < w.blocks; b += RB) {
           ok = __all_sync(kFull, mm_wait(sh, p, &sh.full[s], phase, &sh.tempty[t], tphase ^ 1u));
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t da = desc0 + uint64_t(s * (TL::kStageBytes >> 4)), db = da + (kBM * kBK >> 4);
 #pragma unroll
-            for (int k = 0; k < kBK / 32; ++k)                   // 32 bytes along the row: 2 units of 16
-              tc_mma_f8<CG>(tmem + t * BN, da + k * 2, db + k * 2, idesc, k > 0);
+            for (int j = 0; j < RB; ++j) {
+              if (j > 0 && b + j >= w.blocks) break;
+              const uint64_t da = desc0 + uint64_t((s * TL::kStageBytes + j * TL::kBlockBytes) >> 4), db = da + (kBM * kBK >> 4);
+#pragma unroll
+              for (int k = 0; k < kBK / 32; ++k)                 // 32 bytes along the row: 2 units of 16
+                tc_mma_f8<CG>(tmem + (t * RB + j) * BN, da + k * 2, db + k * 2, idesc, k > 0);
+            }
             tc_commit<CG>(&sh.done[s]);                          // the stage is free, and the product there
           }
           __syncwarp();
@@ -460,7 +469,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
     bool ok = true;
     Walk w;
     for (int tile = first_tile; tile < n_tiles && ok; tile += tile_step) {
-      w.at<BN, CG, WGRAD>(p, sh, tile, rank);
+      w.at<TL, BN, WGRAD>(p, sh, tile, rank);
       const int c0 = w.col0 + cg * CW;                           // the warp's first column of out
       const bool busy = quad * 32 < w.rows && c0 < p.C;          // warp-uniform: whether it has anything to add
       const bool live = row < w.rows;
@@ -482,28 +491,34 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
         step_b = 1;
       }
       const bool col = lane * 4 < CW && c0 + lane * 4 < p.C;     // weight gradient: a lane's four column scales
-      float sa = 0.f, sb = 0.f;
+      float sa[RB] = {}, sb[RB] = {};
       float4 sb4 = make_float4(0.f, 0.f, 0.f, 0.f);
-      const auto fetch = [&]() {
-        if (busy) {
-          sa = live ? *pa : 0.f;
-          if constexpr (WGRAD) {
-            if (col) sb4 = *reinterpret_cast<const float4*>(pb);
-          } else {
-            sb = *pb;
+      const auto fetch = [&](int b) {                            // the scales of a stage's blocks
+#pragma unroll
+        for (int j = 0; j < RB; ++j) {
+          if (busy && b + j < w.blocks) {
+            sa[j] = live ? *pa : 0.f;
+            if constexpr (WGRAD) {
+              if (col) sb4 = *reinterpret_cast<const float4*>(pb);
+            } else {
+              sb[j] = *pb;
+            }
           }
+          pa += step_a;
+          pb += step_b;
         }
-        pa += step_a;
-        pb += step_b;
       };
-      if (w.blocks > 0) fetch();
-      for (int b = 0; b < w.blocks; ++b) {
-        const float ra = sa, rb = sb;
+      fetch(0);
+      for (int b = 0; b < w.blocks; b += RB) {
+        float scale[RB];
+#pragma unroll
+        for (int j = 0; j < RB; ++j) scale[j] = WGRAD ? sa[j] : sa[j] * sb[j];
         if constexpr (WGRAD) {
+          static_assert(!WGRAD || RB == 1, "two buffers of column scales serve single blocks");
           if (lane * 4 < CW) *reinterpret_cast<float4*>(&s_bs[b & 1][lane * 4]) = sb4;
           __syncwarp();
         }
-        if (b + 1 < w.blocks) fetch();
+        fetch(b + RB);
         ok = __all_sync(kFull, mm_wait(sh, p, &sh.done[s], phase));   // one answer for the warp
         if (!ok) break;
         tc_fence_after();
@@ -517,27 +532,32 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
           }
         };
         if (busy) {
-          const uint32_t addr = tmem + t * BN + cg * CW + (uint32_t(quad * 32) << 16);
-          const float2 s2 = WGRAD ? make_float2(ra, ra) : make_float2(ra * rb, ra * rb);
 #pragma unroll
-          for (int c = 0; c < CW; c += 16) {
-            uint32_t u[16];
-            tmem_ld16(addr + c, u);
-            tmem_ld_wait(u);
-            if (c + 16 == CW) release();
+          for (int j = 0; j < RB; ++j) {
+            const bool last = j + 1 == RB || b + j + 1 >= w.blocks;
+            const uint32_t addr = tmem + (t * RB + j) * BN + cg * CW + (uint32_t(quad * 32) << 16);
+            const float2 s2 = make_float2(scale[j], scale[j]);
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const float2 x = make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1]));
-              const float2 y = make_float2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3]));
-              if constexpr (WGRAD) {
-                const float4 q = *reinterpret_cast<const float4*>(&s_bs[b & 1][c + i]);
-                acc[(c + i) / 2] = fma2(mul2(x, s2), make_float2(q.x, q.y), acc[(c + i) / 2]);
-                acc[(c + i) / 2 + 1] = fma2(mul2(y, s2), make_float2(q.z, q.w), acc[(c + i) / 2 + 1]);
-              } else {
-                acc[(c + i) / 2] = fma2(x, s2, acc[(c + i) / 2]);
-                acc[(c + i) / 2 + 1] = fma2(y, s2, acc[(c + i) / 2 + 1]);
+            for (int c = 0; c < CW; c += 16) {
+              uint32_t u[16];
+              tmem_ld16(addr + c, u);
+              tmem_ld_wait(u);
+              if (last && c + 16 == CW) release();
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const float2 x = make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1]));
+                const float2 y = make_float2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3]));
+                if constexpr (WGRAD) {
+                  const float4 q = *reinterpret_cast<const float4*>(&s_bs[b & 1][c + i]);
+                  acc[(c + i) / 2] = fma2(mul2(x, s2), make_float2(q.x, q.y), acc[(c + i) / 2]);
+                  acc[(c + i) / 2 + 1] = fma2(mul2(y, s2), make_float2(q.z, q.w), acc[(c + i) / 2 + 1]);
+                } else {
+                  acc[(c + i) / 2] = fma2(x, s2, acc[(c + i) / 2]);
+                  acc[(c + i) / 2 + 1] = fma2(y, s2, acc[(c + i) / 2 + 1]);
+                }
               }
             }
+            if (last) break;
           }
         } else {
           release();
@@ -617,9 +637,9 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, 
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, int CG, bool WGRAD, bool BF16>
+template <int BN, int CG, int RB, bool WGRAD, bool BF16>
 cudaError_t launch(const MatmulParams& p, int sms, const char** error, cudaStream_t stream) {
-  using TL = Tile<BN, CG>;
+  using TL = Tile<BN, CG, RB>;
   CUtensorMap ma, mb, wa, wb;
   const uint64_t cols = WGRAD ? uint64_t(p.blocks) * kBK : uint64_t(p.K);
   const uint64_t rows_a = WGRAD ? uint64_t(p.R) : uint64_t(p.M), rows_b = WGRAD ? uint64_t(p.C) : uint64_t(p.E) * p.C;
@@ -629,9 +649,9 @@ cudaError_t launch(const MatmulParams& p, int sms, const char** error, cudaStrea
     return cudaErrorUnknown;
   }
   constexpr size_t smem = size_t(TL::kStages) * TL::kStageBytes + 1024;
-  static_assert(TL::kStages <= 8 && TL::kBufs <= 8 && sizeof(Shared) + smem <= 232448, "shared memory of one CTA");
+  static_assert(TL::kStages <= 8 && TL::kBufs <= 8 && TL::kBufs >= 2 && sizeof(Shared) + smem <= 232448, "shared memory of one CTA");
   static_assert(TL::kShareB % kBox == 0 && TL::kStageBytes % 1024 == 0, "whole boxes, swizzle atoms aligned");
-  const auto kernel = expert_matmul_kernel<BN, CG, WGRAD, BF16>;
+  const auto kernel = expert_matmul_kernel<BN, CG, RB, WGRAD, BF16>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   // At most this many tiles: every expert's last row tile may be ragged.
@@ -669,13 +689,13 @@ cudaError_t expert_matmul_errors(int* bits, cudaStream_t stream) {
 }
 
 cudaError_t launch_expert_matmul(const MatmulParams& p, int sms, const char** error, cudaStream_t stream) {
-  if (p.wgrad) return launch<256, 2, true, false>(p, sms, error, stream);
+  if (p.wgrad) return launch<256, 2, 1, true, false>(p, sms, error, stream);
   // Few rows an expert: reading the weights is what takes the time, and narrow
   // tiles spread them over more SMs.
   const bool narrow = p.M <= int64_t(p.E) * 64;
   if (p.out_bf16)
-    return narrow ? launch<128, 1, false, true>(p, sms, error, stream) : launch<256, 2, false, true>(p, sms, error, stream);
-  return narrow ? launch<128, 1, false, false>(p, sms, error, stream) : launch<256, 2, false, false>(p, sms, error, stream);
+    return narrow ? launch<128, 1, 2, false, true>(p, sms, error, stream) : launch<256, 2, 1, false, true>(p, sms, error, stream);
+  return narrow ? launch<128, 1, 2, false, false>(p, sms, error, stream) : launch<256, 2, 1, false, false>(p, sms, error, stream);
 }
 
 }  // namespace moe
