@@ -197,7 +197,8 @@ struct alignas(16) Shared {
   uint32_t tmem;
   int abort;
   int first[kMaxE + 1];                                        // tiles before expert e
-  int block[kMaxE + 1];                                        // weight gradient: column blocks before expert e
+  int block[kMaxE + 1];                                        // weight gradient: column blocks before expert e; product: its first row
+  int count[kMaxE];                                            // product: its rows
   alignas(16) float bscale[kEpiWarps][2][64];                  // weight gradient: a block's column scales, per warp
 };
 
@@ -256,7 +257,12 @@ struct Walk {
   template <class TL, int BN, bool WGRAD>
   __device__ __forceinline__ void at(const MatmulParams& p, const Shared& sh, int tile, int rank) {
     constexpr int kRows = TL::kRows;
-    while (sh.first[e + 1] <= tile) ++e;
+    for (;;) {                                                   // the expert that has the tile: 32 at a time, by the whole warp
+      const int next = e + 1 + int(threadIdx.x % kWarp);
+      const unsigned past = __ballot_sync(kFull, next <= p.E && sh.first[next] <= tile);
+      e += __popc(past);
+      if (past != kFull) break;
+    }
     const int i = tile - sh.first[e];
     const int ct = (p.C + BN - 1) / BN;
     const int rt = (sh.first[e + 1] - sh.first[e]) / ct;
@@ -275,10 +281,8 @@ struct Walk {
       block0 = sh.block[e];
       blocks = sh.block[e + 1] - block0;
     } else {
-      int64_t start, n;
-      expert_rows(p, e, &start, &n);
-      row0 = int(start) + r0;
-      pair_rows = int(min(n - tile_r0, int64_t(kRows)));
+      row0 = sh.block[e] + r0;
+      pair_rows = min(sh.count[e] - tile_r0, kRows);
       block0 = 0;
       blocks = (p.K + kBK - 1) / kBK;
     }
@@ -300,6 +304,8 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
 
   if (warp == 0) {
     if (lane == 0) {
+      for (const CUtensorMap* m : {&map_a, &map_b, &whole_a, &whole_b})
+        asm volatile("prefetch.tensormap [%0];" :: "l"(m) : "memory");
       for (int i = 0; i < TL::kStages; ++i) {
         mbar_init(&sh.full[i], 1 + p.extra);
         mbar_init(&sh.done[i], 1);
@@ -327,6 +333,8 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
         } else {
           int64_t start, n;
           expert_rows(p, e0 + lane, &start, &n);
+          sh.block[e0 + lane] = int(start);
+          sh.count[e0 + lane] = int(n);
           t = int((n + TL::kRows - 1) / TL::kRows) * ct;
         }
       }
@@ -348,7 +356,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
     }
     if (lane == 0) {
       sh.first[p.E] = tiles;
-      sh.block[p.E] = blocks;
+      if constexpr (WGRAD) sh.block[p.E] = blocks;
     }
   }
   __syncthreads();
