@@ -14,15 +14,8 @@
 // products, so that the tensor core forms block b + 1 while the epilogue adds
 // block b, and runs ahead into the next tile while a tile is stored.
 //
-// Wide tiles are worked on by two CTAs of a cluster (cta_group::2): 256 rows by
-// 256 columns, each CTA with its 128 rows of a, half of b's rows, and its rows'
-// sums.  A block then brings 32 KB into an SM instead of 48 KB; with single CTAs
-// the operands' way from L2 is the bound (at 128 x 256 tiles, 131 us of 16,384 x
-// 4096 x 2048 with an empty epilogue).  The first CTA issues the products; both
-// CTAs' copies count on its barriers, its commits arrive in both.
-//
 // Every wait is bounded: when one runs out, the CTA records the pipeline's error
-// bit, drains its copies and returns; a pair leaves together.
+// bit, drains its copies and returns.
 #include "device_common.cuh"
 #include "expert_matmul.h"
 
@@ -47,87 +40,42 @@ constexpr unsigned kFull = 0xffffffffu;
 // so calls on any streams, and captured ones, share the word.
 __device__ int g_mm_errors;
 
-// ---- tcgen05 / TMA primitives (CG: CTAs that work on a tile) -------------------
-template <int CG>
+// ---- tcgen05 / TMA primitives ------------------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
-  if constexpr (CG == 2) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(slot)), "r"(kTmemCols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(slot)), "r"(kTmemCols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(slot)), "r"(kTmemCols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
-template <int CG>
 __device__ __forceinline__ void tmem_free(uint32_t addr) {
-  if constexpr (CG == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(kTmemCols) : "memory");
-  else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(kTmemCols) : "memory");
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(kTmemCols) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Arrives on the barrier (of a pair: in both CTAs) when the products issued so far have ended.
-template <int CG>
+// Arrives on the barrier when the products issued so far have ended.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  if constexpr (CG == 2)
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 :: "r"(smem_addr(bar)), "h"(uint16_t(3)) : "memory");
-  else
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_addr(bar)) : "memory");
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_addr(bar)) : "memory");
 }
 
-template <int CG>
 __device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (CG == 2)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// `bar`: a shared::cluster address; of a pair, the first CTA's barrier.
-template <int CG>
-__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  if constexpr (CG == 2)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
-        :: "r"(smem_addr(dst)), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
-        :: "r"(smem_addr(dst)), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
+__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+      :: "r"(smem_addr(dst)), "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y) : "memory");
 }
 
+// One thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
   return ok != 0;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// The address of the first CTA's copy of a shared variable.
-__device__ __forceinline__ uint32_t first_cta_addr(const void* p) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_addr(p)));
-  return a;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-// Arrives on a barrier of either CTA.  What it orders lies in tensor memory
-// (tcgen05.fence on both sides), so no wider scope than the default is asked for.
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
-}
 // Shared-memory matrix descriptor of a K-major operand in rows of 128 bytes,
 // 128-byte swizzle: groups of 8 rows lie 1024 bytes apart.
 __device__ __forceinline__ uint64_t smem_desc(const void* p) {
@@ -179,11 +127,9 @@ __device__ __forceinline__ void turn(uint4* v, int lane) {
 
 // ---- the kernel ----------------------------------------------------------------
 // RB: blocks that share a stage, its barriers and its place in tensor memory.
-template <int BN, int CG, int RB>
+template <int BN, int RB>
 struct Tile {
-  static constexpr int kRows = kBM * CG;                       // of the CTAs together
-  static constexpr int kShareB = BN / CG;                      // rows of b that a CTA holds
-  static constexpr int kBlockBytes = (kBM + kShareB) * kBK;
+  static constexpr int kBlockBytes = (kBM + BN) * kBK;
   static constexpr int kStageBytes = RB * kBlockBytes;
   static constexpr int kStages = 196608 / kStageBytes;         // 192 KB of operands
   static constexpr int kBufs = kTmemCols / (BN * RB);          // stages' products in tensor memory
@@ -245,18 +191,13 @@ __device__ __forceinline__ int boxes(int rows) { return (rows + kBox - 1) / kBox
 // A tile of the persistent loop, walked in ascending order by every role.
 struct Walk {
   int e = 0;
-  int row0 = 0, rows = 0;         // rows of a: the CTA's first one, and how many of its 128 are in the tile
+  int row0 = 0, rows = 0;         // rows of a: the first one and how many are the tile's
   int col0 = 0, cols = 0;         // columns of out within the expert
-  int r0 = 0;                     // the CTA's first row within the expert's out
-  int pair_rows = 0;              // rows of both CTAs
+  int r0 = 0;                     // the tile's first row within the expert's out
   int block0 = 0, blocks = 0;     // blocks along the contraction
 
-  // The part of n that CTA `rank` has when each has `each`.
-  __device__ __forceinline__ static int share(int n, int rank, int each) { return max(0, min(each, n - rank * each)); }
-
-  template <class TL, int BN, bool WGRAD>
-  __device__ __forceinline__ void at(const MatmulParams& p, const Shared& sh, int tile, int rank) {
-    constexpr int kRows = TL::kRows;
+  template <int BN, bool WGRAD>
+  __device__ __forceinline__ void at(const MatmulParams& p, const Shared& sh, int tile) {
     for (;;) {                                                   // the expert that has the tile: 32 at a time, by the whole warp
       const int next = e + 1 + int(threadIdx.x % kWarp);
       const unsigned past = __ballot_sync(kFull, next <= p.E && sh.first[next] <= tile);
@@ -273,34 +214,30 @@ struct Walk {
     const int m = group * kGroupM + in % gm;
     col0 = in / gm * BN;
     cols = min(BN, p.C - col0);
-    const int tile_r0 = m * kRows;
-    r0 = tile_r0 + rank * kBM;
+    r0 = m * kBM;
     if constexpr (WGRAD) {
       row0 = r0;
-      pair_rows = min(kRows, p.R - tile_r0);
+      rows = min(kBM, p.R - r0);
       block0 = sh.block[e];
       blocks = sh.block[e + 1] - block0;
     } else {
       row0 = sh.block[e] + r0;
-      pair_rows = min(sh.count[e] - tile_r0, kRows);
+      rows = min(kBM, sh.count[e] - r0);
       block0 = 0;
       blocks = (p.K + kBK - 1) / kBK;
     }
-    rows = share(pair_rows, rank, kBM);
   }
 };
 
-template <int BN, int CG, int RB, bool WGRAD, bool BF16>
+template <int BN, int RB, bool WGRAD, bool BF16>
 __global__ void __launch_bounds__(kMmThreads, 1)
 expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                      const __grid_constant__ CUtensorMap whole_a, const __grid_constant__ CUtensorMap whole_b) {
-  using TL = Tile<BN, CG, RB>;
+  using TL = Tile<BN, RB>;
   extern __shared__ uint8_t s_dyn[];
   __shared__ Shared sh;
-  uint8_t* ring = s_dyn + (1024 - smem_addr(s_dyn) % 1024) % 1024;     // the same place in both CTAs of a pair
+  uint8_t* ring = s_dyn + (1024 - smem_addr(s_dyn) % 1024) % 1024;
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-  const int rank = CG == 2 ? int(cluster_rank()) : 0;
-  const int first_tile = int(blockIdx.x) / CG, tile_step = int(gridDim.x) / CG;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -311,7 +248,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
         mbar_init(&sh.done[i], 1);
       }
       for (int i = 0; i < TL::kBufs; ++i) {
-        mbar_init(&sh.tempty[i], kEpiWarps * CG);
+        mbar_init(&sh.tempty[i], kEpiWarps);
       }
       mbar_init(&sh.drain, 1);
       mbar_fence_init();
@@ -319,7 +256,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       sh.abort = *static_cast<volatile int*>(&g_mm_errors) != 0;
     }
   } else if (warp == 1) {
-    tmem_alloc<CG>(&sh.tmem);
+    tmem_alloc(&sh.tmem);
     tc_fence_before();
   } else if (warp == 2) {                                        // tiles and blocks before each expert
     const int ct = (p.C + BN - 1) / BN;
@@ -328,14 +265,14 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       int t = 0, b = 0;
       if (e0 + lane < p.E) {
         if constexpr (WGRAD) {
-          t = (p.R + TL::kRows - 1) / TL::kRows * ct;
+          t = (p.R + kBM - 1) / kBM * ct;
           b = int((max(int64_t(p.kept[e0 + lane]), int64_t(0)) + kBK - 1) / kBK);
         } else {
           int64_t start, n;
           expert_rows(p, e0 + lane, &start, &n);
           sh.block[e0 + lane] = int(start);
           sh.count[e0 + lane] = int(n);
-          t = int((n + TL::kRows - 1) / TL::kRows) * ct;
+          t = int((n + kBM - 1) / kBM) * ct;
         }
       }
       int ti = t, bi = b;
@@ -363,10 +300,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const int n_tiles = sh.abort != 0 ? 0 : sh.first[p.E];
-  // Every thread has seen abort before a role sets it, and a pair's barriers are
-  // set up before the other CTA arrives on them.
-  if constexpr (CG == 2) cluster_sync();
-  else __syncthreads();
+  __syncthreads();                                               // every thread has seen abort before a role sets it
 
   // The epilogue's sums want more registers than an even split gives: of the
   // launch's 640 x 96, the first four warps keep 32 a thread and the others take 112.
@@ -382,28 +316,25 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       uint32_t phase = 0;
       bool ok = true;
       Walk w;
-      for (int tile = first_tile; tile < n_tiles && ok; tile += tile_step) {
-        w.at<TL, BN, WGRAD>(p, sh, tile, rank);
-        const int na = boxes(w.rows), nb = boxes(Walk::share(w.cols, rank, TL::kShareB));
-        const int b_row = (WGRAD ? w.col0 : w.e * p.C + w.col0) + rank * TL::kShareB;
-        int bytes = 0;                                           // of both CTAs: the first one's barrier counts them
-        for (int r = 0; r < CG; ++r)
-          bytes += (boxes(Walk::share(w.pair_rows, r, kBM)) + boxes(Walk::share(w.cols, r, TL::kShareB))) * kBox * kBK;
+      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
+        w.at<BN, WGRAD>(p, sh, tile);
+        const int na = boxes(w.rows), nb = boxes(w.cols);
+        const int b_row = WGRAD ? w.col0 : w.e * p.C + w.col0;
         for (int b = 0; b < w.blocks; b += RB) {
           const int now = RB == 1 ? 1 : min(RB, w.blocks - b);
           ok = __all_sync(kFull, mm_wait(sh, p, &sh.done[s], phase ^ 1u));
           if (!ok) break;
           if (elect_one()) {
-            if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], uint32_t(bytes * now));
-            const uint32_t bar = CG == 2 ? first_cta_addr(&sh.full[s]) : smem_addr(&sh.full[s]);
+            uint64_t* bar = &sh.full[s];
+            mbar_arrive_expect_tx(bar, uint32_t((na + nb) * now * kBox * kBK));
             for (int j = 0; j < now; ++j) {
               uint8_t* sa = ring + s * TL::kStageBytes + j * TL::kBlockBytes;
               uint8_t* sb = sa + kBM * kBK;
               const int x = (w.block0 + b + j) * kBK;
-              if (na == kBM / kBox) tma_2d<CG>(sa, &whole_a, x, w.row0, bar);
-              else for (int i = 0; i < na; ++i) tma_2d<CG>(sa + i * kBox * kBK, &map_a, x, w.row0 + i * kBox, bar);
-              if (nb == TL::kShareB / kBox) tma_2d<CG>(sb, &whole_b, x, b_row, bar);
-              else for (int i = 0; i < nb; ++i) tma_2d<CG>(sb + i * kBox * kBK, &map_b, x, b_row + i * kBox, bar);
+              if (na == kBM / kBox) tma_2d(sa, &whole_a, x, w.row0, bar);
+              else for (int i = 0; i < na; ++i) tma_2d(sa + i * kBox * kBK, &map_a, x, w.row0 + i * kBox, bar);
+              if (nb == BN / kBox) tma_2d(sb, &whole_b, x, b_row, bar);
+              else for (int i = 0; i < nb; ++i) tma_2d(sb + i * kBox * kBK, &map_b, x, b_row + i * kBox, bar);
             }
           }
           __syncwarp();
@@ -414,25 +345,23 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
           }
         }
       }
-      // Copies in flight land before shared memory goes; those of a pair's second
-      // CTA count on the first one's barriers, and the pair leaves together.
-      if (!ok && rank == 0) {
+      if (!ok) {                                                 // copies in flight land before shared memory goes
         for (int i = 0; i < TL::kStages && i < issued; ++i) {
           const int back = issued - 1 - i;
           mbar_wait(&sh.full[back % TL::kStages], uint32_t(back / TL::kStages) & 1u, p.timeout_ns);
         }
       }
-    } else if (warp == 1 && rank == 0) {
-      // ---- MMA issuer: of a pair, the first CTA's ----
-      // D fp32, A and B e4m3, both K-major, N = BN, M = the tile's rows
-      constexpr uint32_t idesc = (1u << 4) | uint32_t(BN / 8) << 17 | uint32_t(TL::kRows / 16) << 24;
+    } else if (warp == 1) {
+      // ---- MMA issuer ----
+      // D fp32, A and B e4m3, both K-major, N = BN, M = 128
+      constexpr uint32_t idesc = (1u << 4) | uint32_t(BN / 8) << 17 | uint32_t(kBM / 16) << 24;
       const uint64_t desc0 = smem_desc(ring);
       int s = 0, t = 0;
       uint32_t phase = 0, tphase = 0;
       bool ok = true;
       Walk w;
-      for (int tile = first_tile; tile < n_tiles && ok; tile += tile_step) {
-        w.at<TL, BN, WGRAD>(p, sh, tile, rank);
+      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
+        w.at<BN, WGRAD>(p, sh, tile);
         for (int b = 0; b < w.blocks; b += RB) {
           ok = __all_sync(kFull, mm_wait(sh, p, &sh.full[s], phase, &sh.tempty[t], tphase ^ 1u));
           if (!ok) break;
@@ -444,9 +373,9 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
               const uint64_t da = desc0 + uint64_t((s * TL::kStageBytes + j * TL::kBlockBytes) >> 4), db = da + (kBM * kBK >> 4);
 #pragma unroll
               for (int k = 0; k < kBK / 32; ++k)                 // 32 bytes along the row: 2 units of 16
-                tc_mma_f8<CG>(tmem + (t * RB + j) * BN, da + k * 2, db + k * 2, idesc, k > 0);
+                tc_mma_f8(tmem + (t * RB + j) * BN, da + k * 2, db + k * 2, idesc, k > 0);
             }
-            tc_commit<CG>(&sh.done[s]);                          // the stage is free, and the product there
+            tc_commit(&sh.done[s]);                          // the stage is free, and the product there
           }
           __syncwarp();
           if (++s == TL::kStages) {
@@ -460,7 +389,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
         }
       }
       if (!ok) {                                                 // products in flight end before tensor memory goes
-        if (elect_one()) tc_commit<CG>(&sh.drain);
+        if (elect_one()) tc_commit(&sh.drain);
         __syncwarp();
         mbar_wait(&sh.drain, 0, p.timeout_ns);
       }
@@ -476,8 +405,8 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
     uint32_t phase = 0;
     bool ok = true;
     Walk w;
-    for (int tile = first_tile; tile < n_tiles && ok; tile += tile_step) {
-      w.at<TL, BN, WGRAD>(p, sh, tile, rank);
+    for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
+      w.at<BN, WGRAD>(p, sh, tile);
       const int c0 = w.col0 + cg * CW;                           // the warp's first column of out
       const bool busy = quad * 32 < w.rows && c0 < p.C;          // warp-uniform: whether it has anything to add
       const bool live = row < w.rows;
@@ -534,10 +463,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
         const auto release = [&]() {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            if constexpr (CG == 2) arrive_cluster(first_cta_addr(&sh.tempty[t]));
-            else mbar_arrive(&sh.tempty[t]);
-          }
+          if (lane == 0) mbar_arrive(&sh.tempty[t]);
         };
         if (busy) {
 #pragma unroll
@@ -611,10 +537,9 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
   }
   __syncwarp();                                                  // the roles' single threads are back
   tc_fence_before();
-  if constexpr (CG == 2) cluster_sync();                         // nothing of the other CTA's is on its way here any more
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_free<CG>(tmem);
+  if (warp == 1) tmem_free(tmem);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -645,41 +570,29 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, 
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, int CG, int RB, bool WGRAD, bool BF16>
+template <int BN, int RB, bool WGRAD, bool BF16>
 cudaError_t launch(const MatmulParams& p, int sms, const char** error, cudaStream_t stream) {
-  using TL = Tile<BN, CG, RB>;
+  using TL = Tile<BN, RB>;
   CUtensorMap ma, mb, wa, wb;
   const uint64_t cols = WGRAD ? uint64_t(p.blocks) * kBK : uint64_t(p.K);
   const uint64_t rows_a = WGRAD ? uint64_t(p.R) : uint64_t(p.M), rows_b = WGRAD ? uint64_t(p.C) : uint64_t(p.E) * p.C;
   if (!make_map(&ma, p.a, rows_a, cols, kBox) || !make_map(&mb, p.b, rows_b, cols, kBox) ||
-      !make_map(&wa, p.a, rows_a, cols, kBM) || !make_map(&wb, p.b, rows_b, cols, TL::kShareB)) {
+      !make_map(&wa, p.a, rows_a, cols, kBM) || !make_map(&wb, p.b, rows_b, cols, BN)) {
     *error = "cuTensorMapEncodeTiled refused an operand";
     return cudaErrorUnknown;
   }
   constexpr size_t smem = size_t(TL::kStages) * TL::kStageBytes + 1024;
   static_assert(TL::kStages <= 8 && TL::kBufs <= 8 && TL::kBufs >= 2 && sizeof(Shared) + smem <= 232448, "shared memory of one CTA");
-  static_assert(TL::kShareB % kBox == 0 && TL::kStageBytes % 1024 == 0, "whole boxes, swizzle atoms aligned");
-  const auto kernel = expert_matmul_kernel<BN, CG, RB, WGRAD, BF16>;
+  static_assert(BN % kBox == 0 && TL::kStageBytes % 1024 == 0, "whole boxes, swizzle atoms aligned");
+  const auto kernel = expert_matmul_kernel<BN, RB, WGRAD, BF16>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   // At most this many tiles: every expert's last row tile may be ragged.
   const int64_t ct = (p.C + BN - 1) / BN;
-  int64_t rt = WGRAD ? int64_t(p.E) * ((p.R + TL::kRows - 1) / TL::kRows) : p.M / TL::kRows + p.E;
+  int64_t rt = WGRAD ? int64_t(p.E) * ((p.R + kBM - 1) / kBM) : p.M / kBM + p.E;
   if (!WGRAD && rt > p.M) rt = p.M;
-  const int64_t groups = sms / CG;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((rt * ct < groups ? rt * ct : groups) * CG));
-  cfg.blockDim = dim3(kMmThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = CG;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = CG > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p, ma, mb, wa, wb);
+  kernel<<<unsigned(rt * ct < sms ? rt * ct : sms), kMmThreads, smem, stream>>>(p, ma, mb, wa, wb);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -697,13 +610,16 @@ cudaError_t expert_matmul_errors(int* bits, cudaStream_t stream) {
 }
 
 cudaError_t launch_expert_matmul(const MatmulParams& p, int sms, const char** error, cudaStream_t stream) {
-  if (p.wgrad) return launch<256, 2, 1, true, false>(p, sms, error, stream);
-  // Few rows an expert: reading the weights is what takes the time, and narrow
-  // tiles spread them over more SMs.
-  const bool narrow = p.M <= int64_t(p.E) * 64;
+  if (p.wgrad) return launch<256, 1, true, false>(p, sms, error, stream);
+  // Tiles of 128 columns, two blocks a stage, up to 200 rows an expert; beyond, 256
+  // columns.  The narrow ones spread few rows' weights over more SMs (rows x experts,
+  // 4096 -> 2048: 87 x 64 109 us against 138, 175 x 64 150 against 158, 300 x 16 60
+  // against 64); the wide ones halve the reads of the rows (600 x 16 96 us against
+  // 98, 1024 x 64 490 against 559).
+  const bool narrow = p.M <= int64_t(p.E) * 200;
   if (p.out_bf16)
-    return narrow ? launch<128, 1, 2, false, true>(p, sms, error, stream) : launch<256, 2, 1, false, true>(p, sms, error, stream);
-  return narrow ? launch<128, 1, 2, false, false>(p, sms, error, stream) : launch<256, 2, 1, false, false>(p, sms, error, stream);
+    return narrow ? launch<128, 2, false, true>(p, sms, error, stream) : launch<256, 1, false, true>(p, sms, error, stream);
+  return narrow ? launch<128, 2, false, false>(p, sms, error, stream) : launch<256, 1, false, false>(p, sms, error, stream);
 }
 
 }  // namespace moe
