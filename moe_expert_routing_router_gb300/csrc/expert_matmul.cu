@@ -33,6 +33,8 @@ constexpr int kEpiWarps = 16, kFirstEpi = 4;
 constexpr int kMmThreads = (kFirstEpi + kEpiWarps) * kWarp;
 constexpr int kTmemCols = 512;
 constexpr int kMaxE = 1024;
+constexpr int kOutCols = 16;                  // columns of a tensor copy of results: 64 bytes of fp32
+constexpr int kWarpOutBytes = 32 * kOutCols * 4;
 constexpr int kGroupM = 16;                   // row tiles of an expert that are taken before the next column tile
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -68,6 +70,18 @@ __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x,
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
       :: "r"(smem_addr(dst)), "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y) : "memory");
 }
+
+// Shared memory to a box of out [E, R, C]; what lies outside is not written.
+__device__ __forceinline__ void tma_store_3d(const void* src, const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+               :: "l"(map), "r"(smem_addr(src)), "r"(x), "r"(y), "r"(z) : "memory");
+}
+// Ends a group of stores; a group may be empty.
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// Until all but the thread's last group have read their shared memory / all have ended.
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // One thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -127,11 +141,14 @@ __device__ __forceinline__ void turn(uint4* v, int lane) {
 
 // ---- the kernel ----------------------------------------------------------------
 // RB: blocks that share a stage, its barriers and its place in tensor memory.
-template <int BN, int RB>
+// STORE: the tile leaves through shared memory by tensor copies (two buffers of
+// 2 KB a warp), which costs a stage.
+template <int BN, int RB, bool STORE>
 struct Tile {
   static constexpr int kBlockBytes = (kBM + BN) * kBK;
   static constexpr int kStageBytes = RB * kBlockBytes;
-  static constexpr int kStages = 196608 / kStageBytes;         // 192 KB of operands
+  static constexpr int kOutBytes = STORE ? kEpiWarps * 2 * kWarpOutBytes : 0;
+  static constexpr int kStages = 196608 / kStageBytes - (STORE ? 1 : 0);   // 192 KB, or 144 KB, of operands
   static constexpr int kBufs = kTmemCols / (BN * RB);          // stages' products in tensor memory
   static constexpr int kCols = BN / 4;                         // columns of one epilogue warp
 };
@@ -144,8 +161,10 @@ struct alignas(16) Shared {
   int abort;
   int first[kMaxE + 1];                                        // tiles before expert e
   int block[kMaxE + 1];                                        // weight gradient: column blocks before expert e; product: its first row
-  int count[kMaxE];                                            // product: its rows
-  alignas(16) float bscale[kEpiWarps][2][64];                  // weight gradient: a block's column scales, per warp
+  union {
+    int count[kMaxE];                                          // product: an expert's rows
+    float4 bscale[kEpiWarps][2][16];                           // weight gradient: a block's column scales, per warp
+  };
 };
 
 // Bounded wait that every role uses: false once it, or another role's, ran out.
@@ -232,8 +251,9 @@ struct Walk {
 template <int BN, int RB, bool WGRAD, bool BF16>
 __global__ void __launch_bounds__(kMmThreads, 1)
 expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                     const __grid_constant__ CUtensorMap whole_a, const __grid_constant__ CUtensorMap whole_b) {
-  using TL = Tile<BN, RB>;
+                     const __grid_constant__ CUtensorMap whole_a, const __grid_constant__ CUtensorMap whole_b,
+                     const __grid_constant__ CUtensorMap map_out) {
+  using TL = Tile<BN, RB, WGRAD>;
   extern __shared__ uint8_t s_dyn[];
   __shared__ Shared sh;
   uint8_t* ring = s_dyn + (1024 - smem_addr(s_dyn) % 1024) % 1024;
@@ -399,66 +419,71 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
     // ---- epilogue: rows 32 * quad + lane, kCols columns ----
     constexpr int CW = TL::kCols;
     const int quad = warp % 4, cg = (warp - kFirstEpi) / 4, row = quad * 32 + lane;
-    float(*s_bs)[64] = sh.bscale[warp - kFirstEpi];
+    float4(*s_bs)[16] = sh.bscale[warp - kFirstEpi];
     const int kblocks = (p.K + kBK - 1) / kBK, cblocks = (p.C + kBK - 1) / kBK;
     int s = 0, t = 0;
     uint32_t phase = 0;
     bool ok = true;
     Walk w;
-    for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
-      w.at<BN, WGRAD>(p, sh, tile);
-      const int c0 = w.col0 + cg * CW;                           // the warp's first column of out
-      const bool busy = quad * 32 < w.rows && c0 < p.C;          // warp-uniform: whether it has anything to add
-      const bool live = row < w.rows;
-      float2 acc[CW / 2];
+    int c0 = 0;                                                  // the warp's first column of out
+    bool busy = false, live = false, col = false;                // whether the warp has anything to add, the lane a row,
+    const float *pa = nullptr, *pb = nullptr;                    // and (weight gradient) four column scales
+    const int64_t step_a = WGRAD ? int64_t(p.R) : p.M, step_b = WGRAD ? p.C : 1;
+    float sa[RB] = {}, sb[RB] = {};
+    float4 sb4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto fetch = [&](int b) {                              // the scales of a stage's blocks
 #pragma unroll
-      for (int i = 0; i < CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      const float* pa = nullptr;
-      const float* pb = nullptr;
-      int64_t step_a = 0, step_b = 0;
+      for (int j = 0; j < RB; ++j) {
+        if (busy && b + j < w.blocks) {
+          sa[j] = live ? *pa : 0.f;
+          if constexpr (WGRAD) {
+            if (col) sb4 = *reinterpret_cast<const float4*>(pb);
+          } else {
+            sb[j] = *pb;
+          }
+        }
+        pa += step_a;
+        pb += step_b;
+      }
+    };
+    const auto begin = [&](int tile) {                           // a tile's place and its first scales
+      w.at<BN, WGRAD>(p, sh, tile);
+      c0 = w.col0 + cg * CW;
+      busy = quad * 32 < w.rows && c0 < p.C;                     // warp-uniform
+      live = row < w.rows;
       if constexpr (WGRAD) {
+        col = lane * 4 < CW && c0 + lane * 4 < p.C;
         pa = p.a_scale + int64_t(w.block0) * p.R + w.r0 + row;
         pb = p.b_scale + int64_t(w.block0) * p.C + c0 + lane * 4;
-        step_a = p.R;
-        step_b = p.C;
       } else {
         pa = p.a_scale + w.row0 + row;
         pb = p.b_scale + (int64_t(w.e) * cblocks + c0 / kBK) * kblocks;
-        step_a = p.M;
-        step_b = 1;
       }
-      const bool col = lane * 4 < CW && c0 + lane * 4 < p.C;     // weight gradient: a lane's four column scales
-      float sa[RB] = {}, sb[RB] = {};
-      float4 sb4 = make_float4(0.f, 0.f, 0.f, 0.f);
-      const auto fetch = [&](int b) {                            // the scales of a stage's blocks
-#pragma unroll
-        for (int j = 0; j < RB; ++j) {
-          if (busy && b + j < w.blocks) {
-            sa[j] = live ? *pa : 0.f;
-            if constexpr (WGRAD) {
-              if (col) sb4 = *reinterpret_cast<const float4*>(pb);
-            } else {
-              sb[j] = *pb;
-            }
-          }
-          pa += step_a;
-          pb += step_b;
-        }
-      };
       fetch(0);
+    };
+    if (!WGRAD && int(blockIdx.x) < n_tiles) begin(blockIdx.x);
+    for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
+      if constexpr (WGRAD) begin(tile);
+      float2 acc[CW / 2];
+#pragma unroll
+      for (int i = 0; i < CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
       for (int b = 0; b < w.blocks; b += RB) {
         float scale[RB];
 #pragma unroll
         for (int j = 0; j < RB; ++j) scale[j] = WGRAD ? sa[j] : sa[j] * sb[j];
         if constexpr (WGRAD) {
           static_assert(!WGRAD || RB == 1, "two buffers of column scales serve single blocks");
-          if (lane * 4 < CW) *reinterpret_cast<float4*>(&s_bs[b & 1][lane * 4]) = sb4;
+          if (lane * 4 < CW) s_bs[b & 1][lane] = sb4;
           __syncwarp();
         }
-        fetch(b + RB);
+        // The next scales: in front of the wait (508 us against 535 at 65,536 rows), but
+        // behind it for the weight gradient, whose loads of column scales hold it up (280
+        // us against 297).
+        if constexpr (!WGRAD) fetch(b + RB);
         ok = __all_sync(kFull, mm_wait(sh, p, &sh.done[s], phase));   // one answer for the warp
         if (!ok) break;
         tc_fence_after();
+        if constexpr (WGRAD) fetch(b + RB);
         // The buffer is free as soon as its last columns have been read.
         const auto release = [&]() {
           tc_fence_before();
@@ -482,7 +507,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
                 const float2 x = make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1]));
                 const float2 y = make_float2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3]));
                 if constexpr (WGRAD) {
-                  const float4 q = *reinterpret_cast<const float4*>(&s_bs[b & 1][c + i]);
+                  const float4 q = s_bs[b & 1][(c + i) / 4];
                   acc[(c + i) / 2] = fma2(mul2(x, s2), make_float2(q.x, q.y), acc[(c + i) / 2]);
                   acc[(c + i) / 2 + 1] = fma2(mul2(y, s2), make_float2(q.z, q.w), acc[(c + i) / 2 + 1]);
                 } else {
@@ -502,38 +527,67 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
         }
         if (++t == TL::kBufs) t = 0;
       }
-      if (!ok || !busy) continue;
-      // Pieces of 16 bytes, NP of which are turned among NP lanes at a time.
-      constexpr int kPer = BF16 ? 8 : 4, NP = CW / kPer < 8 ? CW / kPer : 8;
-      const int64_t out_row = WGRAD ? int64_t(w.e) * p.R + w.r0 : int64_t(w.row0);
+      if (!ok) break;
+      // The next tile's first scales are on their way while this one is stored.  (The
+      // weight gradient has no registers left for that: 280 us without, 307 with.)
+      const bool store = busy;
+      const int to_c0 = c0, to_rows = w.rows, to_row0 = WGRAD ? w.r0 : w.row0, to_e = w.e;
+      if (!WGRAD && tile + int(gridDim.x) < n_tiles) begin(tile + gridDim.x);
+      if (!store) continue;
+      if constexpr (WGRAD) {
+        // 32 x 16 values at a time through the warp's part of shared memory, whose
+        // 64-byte rows hold their 16-byte pieces in the tensor copy's swizzled order.
+        uint8_t* stage = ring + TL::kStages * TL::kStageBytes + (warp - kFirstEpi) * 2 * kWarpOutBytes;
 #pragma unroll
-      for (int h = 0; h < CW; h += NP * kPer) {
-        uint4 v[NP];
+        for (int h = 0; h < CW; h += kOutCols) {
+          uint8_t* half = stage + h / kOutCols % 2 * kWarpOutBytes;
+          tma_store_read();                                      // the copy before the last has read it (lane 0 issued it)
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const float2* a = &acc[(h + i * kPer) / 2];
-          if constexpr (BF16) {
-            uint32_t b2[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 q = __floats2bfloat162_rn(a[j].x, a[j].y);
-              b2[j] = *reinterpret_cast<const uint32_t*>(&q);
-            }
-            v[i] = make_uint4(b2[0], b2[1], b2[2], b2[3]);
-          } else {
-            v[i] = make_uint4(__float_as_uint(a[0].x), __float_as_uint(a[0].y), __float_as_uint(a[1].x), __float_as_uint(a[1].y));
+          for (int i = 0; i < kOutCols / 4; ++i) {
+            const float2 x = acc[(h + 4 * i) / 2], y = acc[(h + 4 * i) / 2 + 1];
+            *reinterpret_cast<float4*>(half + lane * 64 + (i ^ (lane >> 1 & 3)) * 16) = make_float4(x.x, x.y, y.x, y.y);
+          }
+          async_proxy_fence();
+          __syncwarp();
+          if (lane == 0) {                                       // a group every time: the buffers are counted by groups
+            if (to_c0 + h < p.C) tma_store_3d(half, &map_out, to_c0 + h, to_row0 + quad * 32, to_e);
+            tma_store_commit();
           }
         }
-        turn<NP>(v, lane);
-        const int c = c0 + h + lane % NP * kPer;                 // C is a multiple of 16: a piece is whole
+      } else {
+        // Pieces of 16 bytes, NP of which are turned among NP lanes at a time.
+        constexpr int kPer = BF16 ? 8 : 4, NP = CW / kPer < 8 ? CW / kPer : 8;
 #pragma unroll
-        for (int r = 0; r < NP; ++r) {
-          const int to = quad * 32 + lane / NP * NP + r;
-          if (to < w.rows && c < p.C)
-            *reinterpret_cast<uint4*>(static_cast<char*>(p.out) + ((out_row + to) * p.C + c) * (BF16 ? 2 : 4)) = v[r];
+        for (int h = 0; h < CW; h += NP * kPer) {
+          uint4 v[NP];
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const float2* a = &acc[(h + i * kPer) / 2];
+            if constexpr (BF16) {
+              uint32_t b2[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 q = __floats2bfloat162_rn(a[j].x, a[j].y);
+                b2[j] = *reinterpret_cast<const uint32_t*>(&q);
+              }
+              v[i] = make_uint4(b2[0], b2[1], b2[2], b2[3]);
+            } else {
+              v[i] = make_uint4(__float_as_uint(a[0].x), __float_as_uint(a[0].y), __float_as_uint(a[1].x), __float_as_uint(a[1].y));
+            }
+          }
+          turn<NP>(v, lane);
+          const int c = to_c0 + h + lane % NP * kPer;               // C is a multiple of 16: a piece is whole
+#pragma unroll
+          for (int r = 0; r < NP; ++r) {
+            const int to = quad * 32 + lane / NP * NP + r;
+            if (to < to_rows && c < p.C)
+              *reinterpret_cast<uint4*>(static_cast<char*>(p.out) + (int64_t(to_row0 + to) * p.C + c) * (BF16 ? 2 : 4)) = v[r];
+          }
         }
       }
     }
+    if constexpr (WGRAD) tma_store_done();                       // shared memory is read, and the results are there
   }
   __syncwarp();                                                  // the roles' single threads are back
   tc_fence_before();
@@ -570,18 +624,28 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, 
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// fp32 results [E, R, C] written in boxes of 32 rows by 16 columns.
+bool make_out_map(CUtensorMap* map, void* base, uint64_t E, uint64_t R, uint64_t C) {
+  const cuuint64_t dims[3] = {C, R, E}, strides[2] = {C * 4, R * C * 4};
+  const cuuint32_t boxes[3] = {kOutCols, 32, 1}, ones[3] = {1, 1, 1};
+  return encode_fn() != nullptr &&
+         encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int BN, int RB, bool WGRAD, bool BF16>
 cudaError_t launch(const MatmulParams& p, int sms, const char** error, cudaStream_t stream) {
-  using TL = Tile<BN, RB>;
-  CUtensorMap ma, mb, wa, wb;
+  using TL = Tile<BN, RB, WGRAD>;
+  CUtensorMap ma, mb, wa, wb, mo = {};
   const uint64_t cols = WGRAD ? uint64_t(p.blocks) * kBK : uint64_t(p.K);
   const uint64_t rows_a = WGRAD ? uint64_t(p.R) : uint64_t(p.M), rows_b = WGRAD ? uint64_t(p.C) : uint64_t(p.E) * p.C;
   if (!make_map(&ma, p.a, rows_a, cols, kBox) || !make_map(&mb, p.b, rows_b, cols, kBox) ||
-      !make_map(&wa, p.a, rows_a, cols, kBM) || !make_map(&wb, p.b, rows_b, cols, BN)) {
+      !make_map(&wa, p.a, rows_a, cols, kBM) || !make_map(&wb, p.b, rows_b, cols, BN) ||
+      (WGRAD && !make_out_map(&mo, p.out, uint64_t(p.E), uint64_t(p.R), uint64_t(p.C)))) {
     *error = "cuTensorMapEncodeTiled refused an operand";
     return cudaErrorUnknown;
   }
-  constexpr size_t smem = size_t(TL::kStages) * TL::kStageBytes + 1024;
+  constexpr size_t smem = size_t(TL::kStages) * TL::kStageBytes + TL::kOutBytes + 1024;
   static_assert(TL::kStages <= 8 && TL::kBufs <= 8 && TL::kBufs >= 2 && sizeof(Shared) + smem <= 232448, "shared memory of one CTA");
   static_assert(BN % kBox == 0 && TL::kStageBytes % 1024 == 0, "whole boxes, swizzle atoms aligned");
   const auto kernel = expert_matmul_kernel<BN, RB, WGRAD, BF16>;
@@ -591,7 +655,7 @@ cudaError_t launch(const MatmulParams& p, int sms, const char** error, cudaStrea
   const int64_t ct = (p.C + BN - 1) / BN;
   int64_t rt = WGRAD ? int64_t(p.E) * ((p.R + kBM - 1) / kBM) : p.M / kBM + p.E;
   if (!WGRAD && rt > p.M) rt = p.M;
-  kernel<<<unsigned(rt * ct < sms ? rt * ct : sms), kMmThreads, smem, stream>>>(p, ma, mb, wa, wb);
+  kernel<<<unsigned(rt * ct < sms ? rt * ct : sms), kMmThreads, smem, stream>>>(p, ma, mb, wa, wb, mo);
   return cudaGetLastError();
 }
 
