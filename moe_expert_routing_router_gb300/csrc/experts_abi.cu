@@ -112,10 +112,7 @@ moe_status moe_route_fwd(const void* logits, moe_dtype dt, int64_t T, int32_t E,
   p.keep = topk_groups;
   p.top2 = group_score == MOE_GROUP_TOP2;
   p.L = 1;
-  while (p.L * 2 * n_groups <= moe::kRouteLanes) {
-    p.L *= 2;
-    ++p.lshift;
-  }
+  while (p.L * 2 * n_groups <= moe::kRouteLanes) p.L *= 2;
   p.chunk = (p.gs + p.L - 1) / p.L;
   p.bias = bias;
   p.renorm = renorm < 0 ? k > 1 : renorm;

@@ -15,7 +15,8 @@ struct RouteParams {
   int softmax;            // scores: 0 sigmoid, 1 softmax
   int G, gs, keep;        // groups, experts per group, groups a token may use
   int top2;               // a group's score: 0 its largest choice value, 1 the sum of its two largest
-  int L, lshift, chunk;   // lanes per group (a power of two, and its logarithm), experts per lane
+  int L, chunk;           // of a warp a row (the double-precision path): lanes per group (a power of two), experts per lane
+  int tshift, tchunk;     // of the kernel's lanes a row: logarithm of the lanes per group, experts per lane
   const float* bias;      // [E] or null
   int renorm;
   float scale;

@@ -6,10 +6,10 @@
 // values within the best groups are picked; gates are the picks' scores,
 // renormalised over the picks if asked, times a scale.
 //
-// One warp works on one row.  A group's experts lie in L consecutive lanes
-// (L the largest power of two with G * L <= 32), `chunk` consecutive experts
-// in each, so that the lane order is the expert order (ties go to the lowest
-// lane) and a group's score is a butterfly over its lanes.
+// A row is worked on by 8, 16 or 32 lanes, so that a warp's steps serve up to
+// four rows.  A group's experts lie in consecutive lanes and an expert's lane and
+// place rise with its index, so that ties go to the lowest lane and place, and a
+// group's score is a butterfly over its lanes.
 //
 // Picks are integers, decided by comparing sums of exponentials.  The fast path
 // compares them in fp32 and bounds what its rounding can have changed: where
@@ -23,27 +23,18 @@
 #include "route.h"
 
 #include <cstddef>
+#include <type_traits>
 
 namespace moe {
 namespace {
 
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / kWarp;
-// Rows that one CTA takes alone, in one launch that also writes the counts and
-// the bias.  Beyond them, more CTAs and a cleared counter array in front.
-constexpr int kRouteOneCtaRows = 32;
 constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
-
-// Order-preserving key of a float that is not NaN; 0 is below every key.
-__device__ __forceinline__ uint32_t float_key(float v) {
-  const uint32_t u = __float_as_uint(v);
-  return u ^ (uint32_t(int(u) >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float key_float(uint32_t k) {
-  return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
-}
+// No choice value: above and below nothing, and passed over by fmaxf.
+__device__ __forceinline__ float none() { return __uint_as_float(0x7fc00000u); }
 
 template <class Elem>
 __device__ __forceinline__ float load_logit(const void* logits, int64_t at) {
@@ -169,14 +160,14 @@ __device__ __noinline__ int route_row_double(const RouteParams& p, int64_t row, 
 // ---------------------------------------------------------------------------
 // The picks of a row where values that decide them are next to one another
 // (`close`), or where its groups' scores are (`unsure`).  Lane j holds the j-th
-// largest key and its expert, the k picks and two more.
+// largest choice value and its expert, the k picks and two more.
 // ---------------------------------------------------------------------------
 template <class Elem>
-__device__ __noinline__ int route_settle(const RouteParams& p, int64_t row, int lane, uint32_t ck, int ce, int rounds,
-                                         float tol, bool close, bool unsure) {
-  const bool there = lane < rounds && ck != 0u;
+__device__ __noinline__ int route_settle(const RouteParams& p, int64_t row, int lane, float c, int ce, int rounds, float tol,
+                                         bool close, bool unsure) {
+  const bool there = lane < rounds && c == c;
   const float zc = there ? load_logit<Elem>(p.logits, row * p.E + ce) : neg_inf();
-  const float bc = there && p.bias != nullptr ? p.bias[ce] : 0.f, c = key_float(ck);
+  const float bc = there && p.bias != nullptr ? p.bias[ce] : 0.f;
   const float c_up = __shfl_up_sync(kFull, c, 1), z_up = __shfl_up_sync(kFull, zc, 1), b_up = __shfl_up_sync(kFull, bc, 1);
   // sure all the same where the inputs are equal
   const bool open = close && lane >= 1 && lane <= p.k && there && c_up - c <= tol + 2.4e-7f * fabsf(c_up) &&
@@ -205,52 +196,69 @@ __device__ __noinline__ int route_settle(const RouteParams& p, int64_t row, int 
 
 // ---------------------------------------------------------------------------
 // Forward.
-//   NV    experts per lane, at least `chunk`
-//   VB    bytes per load; above the element's size only where every lane's NV
-//         experts are there and aligned (FULL: no lane has fewer)
+//   LPR   lanes of a row; NV: experts of a lane, at least `tchunk`
+//   VB    bytes per load; above the element's size only with FULL: every lane has
+//         NV experts or none, and rows, groups and the array are aligned
 //   MODE  0: the order of the logits decides everything and gates need no sum over the
 //         row; 1: sigmoid scores; 2: softmax scores
 //
-// Selection: the k largest of the lanes' maxima bound the k-th choice value from
-// below (a warp reduction and two instructions each); the few experts that reach
-// the bound are gathered, one a lane in expert order, and ranked by counting.
-// With a bias two more than the k picks are ranked, to see what hangs on
-// rounding.  Should more than 32 experts reach the bound (whole groups in single
-// lanes, long ties), the warp takes the maximum again and again instead.  A warp
-// selects for `per` rows one after another, each loaded while the one before is
-// worked on; the rows that hang on rounding are settled behind them, and then
-// the gates of all of them are computed, a pick a lane.
-// The instructions bound it: sorting a lane's experts and popping them one by one
-// took 1145 a row of 256.
+// Selection: the k largest of the maxima of eight experts each bound the k-th
+// choice value from below; the few experts that reach the bound (lowered by what
+// rounding can have done, where there is a bias) are gathered in expert order and
+// ranked by counting.  Should more than 32 reach it (long ties, masked rows), the
+// row's lanes take the maximum again and again instead.  The rows that hang on
+// rounding are settled behind a warp's four rows, and then the gates of all of
+// them are computed, a pick a lane.
+// Instructions bound it.  For a row of 256 in 8 groups: 1145 with a warp a row whose
+// lanes sort their experts, 728 with a warp a row and this selection.
 // ---------------------------------------------------------------------------
 constexpr int kMaxRounds = 10;                                   // 8 picks and two more
 constexpr int kMaxPer = kWarp / kPickLanes;                      // rows a warp finishes at once
+constexpr int kCand = 32;                                        // candidates of a row
 
-template <class Elem, int NV, int VB, bool FULL, int MODE>
+template <int LPR>
+__device__ __forceinline__ float row_max(float x) {
+#pragma unroll
+  for (int off = LPR / 2; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, off));
+  return x;
+}
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int off = LPR / 2; off > 0; off >>= 1) x += __shfl_xor_sync(kFull, x, off);
+  return x;
+}
+
+template <class Elem, int LPR, int NV, int VB, bool FULL, int MODE>
 __global__ void __launch_bounds__(kRouteThreads, NV <= 8 ? 4 : NV <= 16 ? 3 : NV <= 32 ? 2 : 1)
 route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
   using Raw = typename Elem::Raw;
+  constexpr int R = kWarp / LPR;                                 // rows of a pass
   constexpr int kPer = VB / int(sizeof(Raw));                    // elements per load
-  constexpr bool kAhead = NV * int(sizeof(Raw)) <= 64;           // whether the next row fits beside this one
-  __shared__ __align__(16) uint2 s_cand[kRouteWarps][kWarp];     // key and expert of the candidates, in expert order
-  __shared__ uint2 s_ranked[kRouteWarps][kMaxPer][kMaxRounds];   // largest first
-  extern __shared__ int s_hist[];                                // [E]
+  constexpr bool kAhead = NV * int(sizeof(Raw)) <= 64;           // whether the next pass fits beside this one
+  constexpr int kMaxima = (NV + 7) / 8;
+  constexpr bool kSpread = NV <= 32;                             // values go through shared memory to be picked by place
+  using Mask = typename std::conditional<NV <= 32, uint32_t, unsigned long long>::type;
+  __shared__ __align__(16) float s_val[kRouteWarps][kSpread ? NV * kWarp : 4];
+  __shared__ __align__(16) float s_cv[kRouteWarps][R][kCand];    // candidates, in expert order
+  __shared__ int s_ce[kRouteWarps][R][kCand];
+  __shared__ float2 s_ranked[kRouteWarps][kMaxPer][kMaxRounds];  // value and expert (as bits), largest first
+  extern __shared__ __align__(16) float s_bias[];                // in lane order, NV (rounded up to 4) a lane; then
+  int* s_hist = reinterpret_cast<int*>(s_bias + LPR * ((NV + 3) / 4 * 4));   // the counts [E]
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
-  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) s_hist[e] = 0;
-  __syncthreads();
-
-  const int g = lane >> p.lshift, sub = lane & (p.L - 1);
-  const int base = g * p.gs + sub * p.chunk;
-  const int n = g < p.G ? max(0, min(p.chunk, p.gs - sub * p.chunk)) : 0;
+  const int li = lane % LPR, rr = lane / LPR;
+  const int g = li >> p.tshift, sub = li & ((1 << p.tshift) - 1);
+  const int base = g * p.gs + sub * p.tchunk;
+  const int n = g < p.G ? max(0, min(p.tchunk, p.gs - sub * p.tchunk)) : 0;
   const bool has_bias = p.bias != nullptr;
   const bool grouped = p.keep < p.G;
   const int rounds = has_bias ? p.k + 2 : p.k;
-  float bv[NV];
-  const auto fetch_bias = [&]() {
+  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) s_hist[e] = 0;
+  if (MODE != 0 && warp < NV / 4 && rr == 0)                     // [i / 4][li][i % 4]: a lane reads four at a time
+    for (int i4 = warp; i4 < (NV + 3) / 4; i4 += kRouteWarps)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) bv[i] = has_bias && i < n ? p.bias[base + i] : 0.f;
-  };
-  fetch_bias();
+      for (int j = 0; j < 4; ++j) s_bias[(i4 * LPR + li) * 4 + j] = has_bias && i4 * 4 + j < n ? p.bias[base + i4 * 4 + j] : 0.f;
+  __syncthreads();
 
   Raw raw[NV];
   const auto fetch = [&](int64_t row) {
@@ -260,7 +268,7 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
       alignas(16) Raw part[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) part[i] = Elem::kNegInf;
-      if (FULL ? n > 0 : v * kPer < n) {
+      if (row < p.T && (FULL ? n > 0 : v * kPer < n)) {
         if constexpr (VB == 16) *reinterpret_cast<uint4*>(part) = *reinterpret_cast<const uint4*>(src + v * kPer);
         else if constexpr (VB == 8) *reinterpret_cast<uint2*>(part) = *reinterpret_cast<const uint2*>(src + v * kPer);
         else if constexpr (VB == 4) *reinterpret_cast<uint32_t*>(part) = *reinterpret_cast<const uint32_t*>(src + v * kPer);
@@ -270,201 +278,256 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
       for (int i = 0; i < kPer; ++i) raw[v * kPer + i] = part[i];
     }
   };
+  const auto logit = [&](int i) {
+    const float x = __uint_as_float(Elem::bits(raw[i]));
+    return x == x ? x : neg_inf();                               // not a number: masked
+  };
 
   const int64_t stride = int64_t(gridDim.x) * kRouteWarps * per;
   const int64_t first0 = (int64_t(blockIdx.x) * kRouteWarps + warp) * per;
-  if (kAhead && first0 < p.T) fetch(first0);
+  if (kAhead && first0 < p.T) fetch(first0 + rr);
   for (int64_t first = first0; first < p.T; first += stride) {
     float my_max = 0.f, my_sum = 1.f, my_tol = 0.f;              // of row first + lane / 8
     unsigned close_rows = 0u, unsure_rows = 0u;
     const int rows = int(min(int64_t(per), p.T - first));
-    for (int r = 0; r < rows; ++r) {
-      const int64_t row = first + r;
-      if constexpr (!kAhead) fetch(row);
-      float z[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const float x = __uint_as_float(Elem::bits(raw[i]));
-        z[i] = x == x ? x : neg_inf();                           // not a number: never preferred
-      }
-      if constexpr (kAhead) {
-        const int64_t then = r + 1 < rows ? row + 1 : first + stride;
-        if (then < p.T) fetch(then);
-      }
+    for (int r0 = 0; r0 < rows; r0 += R) {
+      if constexpr (!kAhead) fetch(first + r0 + rr);
 
       // Choice values in fp32.  Their error is within tol / 2.
-      float s[NV], tol = 0.f;
+      float c[NV], tol = 0.f;
       if constexpr (MODE == 2) {
-        float m = z[0];
+        float m = logit(0);
 #pragma unroll
-        for (int i = 1; i < NV; ++i) m = fmaxf(m, z[i]);
-        const float row_max = warp_max_f(m);
-        m = row_max > neg_inf() ? row_max : 0.f;
+        for (int i = 1; i < NV; ++i) m = fmaxf(m, logit(i));
+        const float top = row_max<LPR>(m);
+        m = top > neg_inf() ? top : 0.f;
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          s[i] = ex2_approx((z[i] - m) * kLog2e);
-          sum += s[i];
+          c[i] = ex2_approx((logit(i) - m) * kLog2e);
+          sum += c[i];
         }
-        sum = warp_sum_f(sum);
+        sum = row_sum<LPR>(sum);
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) s[i] *= inv;
+        for (int i = 0; i < NV; ++i) c[i] *= inv;
         // x e^-x <= 0.37: the rounded argument moves a score by 2^-23 * 0.37 * 1.45 of
         // the row's largest, ex2.approx by 2^-22 of itself, the sum of at most 64
         // values a lane and 5 steps by 69 * 2^-24 of itself: 5e-6 covers them
         tol = 1e-5f * inv;
-        if (lane / kPickLanes == r) {
-          my_max = row_max;
-          my_sum = sum;
-          my_tol = tol;
+        const int from = (lane / kPickLanes - r0) * LPR;         // the row whose pick the lane will hold
+        const bool mine = lane / kPickLanes >= r0 && lane / kPickLanes < r0 + R;
+        const float t = __shfl_sync(kFull, top, from & 31), u = __shfl_sync(kFull, sum, from & 31), v = __shfl_sync(kFull, tol, from & 31);
+        if (mine) {
+          my_max = t;
+          my_sum = u;
+          my_tol = v;
         }
       } else if constexpr (MODE == 1) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) s[i] = rcp_approx(1.f + ex2_approx(z[i] * -kLog2e));
+        for (int i = 0; i < NV; ++i) c[i] = rcp_approx(1.f + ex2_approx(logit(i) * -kLog2e));
         // e = exp(-z) is off by 2^-22 + 2^-24 * 1.45 |z| of itself; s moves by
         // s (1 - s) of that, below 2^-23, and rcp.approx and 1 + e by 2^-22 of s: 6e-7 covers them
         tol = my_tol = 1.2e-6f;
       }
       if constexpr (MODE != 0) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) s[i] = z[i] > neg_inf() ? s[i] + bv[i] : neg_inf();
-      }
-      uint32_t key[NV];
+        for (int i = 0; i < NV; i += 4) {
+          const float4 b = *reinterpret_cast<const float4*>(&s_bias[(i / 4 * LPR + li) * 4]);
+          const float bi[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const float v = MODE != 0 && has_bias ? s[i] : z[i];
-        key[i] = FULL || i < n ? float_key(v + 0.f) : 0u;
+          for (int j = 0; j < 4; ++j)
+            if (i + j < NV) c[i + j] = logit(i + j) > neg_inf() && (FULL || i + j < n) ? c[i + j] + bi[j] : neg_inf();
+        }
       }
 
       bool open = g < p.G;                                       // whether the lane's group is a choice
-      if (grouped) {
-        uint32_t gkey;
-        float gtol = tol;
-        if (MODE != 0 && p.top2) {
-          float a = neg_inf(), b = neg_inf();
+      float score = neg_inf();
+      if (grouped && MODE != 0 && p.top2) {
+        float a = neg_inf(), b = neg_inf();
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const float v = FULL || i < n ? s[i] : neg_inf();
-            b = fmaxf(b, fminf(a, v));
-            a = fmaxf(a, v);
-          }
-          for (int off = 1; off < p.L; off <<= 1) {
-            const float a2 = __shfl_xor_sync(kFull, a, off), b2 = __shfl_xor_sync(kFull, b, off);
-            b = fmaxf(fminf(a, a2), fmaxf(b, b2));
-            a = fmaxf(a, a2);
-          }
-          gkey = float_key((b > neg_inf() ? a + b : a) + 0.f);
-          gtol = 2.f * tol;
-        } else {
-          gkey = key[0];
+        for (int i = 0; i < NV; ++i) {
+          b = fmaxf(b, fminf(a, c[i]));
+          a = fmaxf(a, c[i]);
+        }
+        for (int off = 1 << p.tshift >> 1; off > 0; off >>= 1) {
+          const float a2 = __shfl_xor_sync(kFull, a, off), b2 = __shfl_xor_sync(kFull, b, off);
+          b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+          a = fmaxf(a, a2);
+        }
+        score = b > neg_inf() ? a + b : a;
+      }
+      if (MODE == 0 || !has_bias) {                              // without a bias the logits' order is the scores'
 #pragma unroll
-          for (int i = 1; i < NV; ++i) gkey = max(gkey, key[i]);
-          for (int off = 1; off < p.L; off <<= 1) gkey = max(gkey, __shfl_xor_sync(kFull, gkey, off));
-        }
-        if (!open) gkey = 0u;
-        // The best group, `keep` times; groups that tie go by lane, the lower first.
-        open = false;
-        uint32_t worst = 0u;
-        for (int j = 0; j < p.keep; ++j) {
-          worst = __reduce_max_sync(kFull, gkey);
-          const int at = __ffs(__ballot_sync(kFull, gkey == worst)) - 1;
-          if (g == at >> p.lshift) {
-            open = true;
-            gkey = 0u;
-          }
-        }
-        if (MODE != 0 && (has_bias || p.top2)) {
-          const float lo = key_float(worst), hi = key_float(__reduce_max_sync(kFull, gkey));
-          if (lo - hi <= gtol + 4.8e-7f * fabsf(lo)) unsure_rows |= 1u << r;   // + the sums' own roundings
-        }
+        for (int i = 0; i < NV; ++i) c[i] = logit(i);
+      }
+      if constexpr (!FULL) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) c[i] = i < n ? c[i] : none();
+      }
+      if constexpr (kAhead) {
+        const int64_t then = r0 + R < rows ? first + r0 + R : first + stride;
+        fetch(then + rr);
       }
 
-      uint32_t best = 0u;
-      if (open) {
+      float best[kMaxima];                                       // the maxima of eight
 #pragma unroll
-        for (int i = 0; i < NV; ++i) best = max(best, key[i]);
+      for (int j = 0; j < kMaxima; ++j) {
+        best[j] = c[8 * j];
+#pragma unroll
+        for (int i = 8 * j + 1; i < 8 * j + 8 && i < NV; ++i) best[j] = fmaxf(best[j], c[i]);
       }
-      uint32_t rest = best, reach = 0u;
+      bool hangs = false;                                        // whether the choice of groups hangs on rounding
+      if (grouped) {
+        if (MODE == 0 || !p.top2) {
+          score = best[0];
 #pragma unroll
-      for (int j = 0; j < kMaxRounds; ++j) {
-        if (j >= rounds) break;
-        reach = __reduce_max_sync(kFull, rest);
-        rest = rest == reach ? 0u : rest;
+          for (int j = 1; j < kMaxima; ++j) score = fmaxf(score, best[j]);
+          for (int off = 1 << p.tshift >> 1; off > 0; off >>= 1) score = fmaxf(score, __shfl_xor_sync(kFull, score, off));
+        }
+        if (!open) score = none();
+        // The groups above this one; of equal ones the lower index is above.
+        int rank = 0;
+        for (int o = 1 << p.tshift; o < LPR; o += 1 << p.tshift) {
+          const float other = __shfl_xor_sync(kFull, score, o);
+          rank += other > score || (other == score && (li ^ o) < li);
+        }
+        const bool kept = open && rank < p.keep;
+        if (MODE != 0 && (has_bias || p.top2)) {
+          const float lo = -row_max<LPR>(kept ? -score : none()), hi = row_max<LPR>(kept ? none() : score);
+          hangs = lo - hi <= (p.top2 ? 2.f * tol : tol) + 4.8e-7f * fabsf(lo);   // + the sums' own roundings
+        }
+        open = kept;
       }
-      reach = open ? max(reach, 1u) : 0xffffffffu;               // 0: places without an expert; the last: above every number
-      int count = 0;
+
+      // The bound.
+      float reach = none();
 #pragma unroll
-      for (int i = 0; i < NV; ++i) count += key[i] >= reach;
+      for (int j = 0; j < kMaxima; ++j) best[j] = open ? best[j] : none();
+      for (int j = 0; j < p.k; ++j) {
+        float m = best[0];
+#pragma unroll
+        for (int i = 1; i < kMaxima; ++i) m = fmaxf(m, best[i]);
+        reach = row_max<LPR>(m);
+#pragma unroll
+        for (int i = 0; i < kMaxima; ++i) best[i] = best[i] == reach ? none() : best[i];
+      }
+      reach = reach == reach ? reach : neg_inf();                // fewer maxima than picks: everything
+      if (MODE != 0 && has_bias) reach -= tol + 2.4e-7f * fabsf(reach);
+      Mask mask = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) mask |= c[i] >= reach ? Mask(1) << i : Mask(0);
+      if (!open) mask = 0;
+      const int count = NV <= 32 ? __popc(uint32_t(mask)) : __popcll((unsigned long long)mask);
       int before = count;
 #pragma unroll
-      for (int off = 1; off < kWarp; off <<= 1) {
-        const int o = __shfl_up_sync(kFull, before, off);
-        if (lane >= off) before += o;
+      for (int off = 1; off < LPR; off <<= 1) {
+        const int o = __shfl_up_sync(kFull, before, off, LPR);
+        if (li >= off) before += o;
       }
-      const int total = __shfl_sync(kFull, before, kWarp - 1);
-      uint2* ranked = s_ranked[warp][r];
-      if (total <= kWarp) {
-        uint2* at = &s_cand[warp][before - count];
+      const int total = __shfl_sync(kFull, before, LPR - 1, LPR);
+      float2* ranked = s_ranked[warp][r0 + rr];
+      const bool fits = total <= kCand;
+      if (fits) {
+        int at = before - count;
+        if constexpr (kSpread) {
+          float* val = &s_val[warp][lane * 4];
+          if (count > 0) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (key[i] >= reach) *at++ = make_uint2(key[i], uint32_t(base + i));
-        if (lane >= total) s_cand[warp][lane] = make_uint2(0u, 0u);
-        __syncwarp();
-        const uint2 mine = s_cand[warp][lane];
-        int rank = 0;
-        for (int o = 0; o < total; o += 4) {
-          const uint4 two = *reinterpret_cast<const uint4*>(&s_cand[warp][o]), more = *reinterpret_cast<const uint4*>(&s_cand[warp][o + 2]);
-          rank += two.x > mine.x;
-          rank += two.z > mine.x;
-          rank += more.x > mine.x;
-          rank += more.z > mine.x;
-        }
-        rank += __popc(__match_any_sync(kFull, mine.x) & ((1u << lane) - 1u));
-        if (rank < rounds) ranked[rank] = mine;                  // the empty ones come last
-      } else {
-        for (int j = 0; j < rounds; ++j) {
-          const uint32_t top = __reduce_max_sync(kFull, best);
-          const int from = __ffs(__ballot_sync(kFull, best == top)) - 1;
-          if (lane == from) {
-            bool found = false;
-            best = 0u;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-              if (!found && key[i] == top) {
-                found = true;
-                ranked[j] = make_uint2(top, uint32_t(base + i));
-                key[i] = 0u;
-              }
-              best = max(best, key[i]);
+            for (int i = 0; i < NV; i += 4)
+              *reinterpret_cast<float4*>(val + i * kWarp) =
+                  make_float4(c[i], i + 1 < NV ? c[i + 1 < NV ? i + 1 : i] : 0.f, i + 2 < NV ? c[i + 2 < NV ? i + 2 : i] : 0.f, i + 3 < NV ? c[i + 3 < NV ? i + 3 : i] : 0.f);
+            while (mask != 0) {                                  // the lane's own values: no other lane's writes are read
+              const int i = __ffs(int(mask)) - 1;
+              mask &= mask - 1;
+              s_cv[warp][rr][at] = val[(i & ~3) * kWarp + (i & 3)];
+              s_ce[warp][rr][at] = base + i;
+              ++at;
             }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (mask >> i & 1) {
+              s_cv[warp][rr][at] = c[i];
+              s_ce[warp][rr][at] = base + i;
+              ++at;
+            }
+        }
+        for (int q = li; q < kCand; q += LPR)
+          if (q >= total) s_cv[warp][rr][q] = none();
+        for (int j = li; j < rounds; j += LPR)
+          if (j >= total) ranked[j] = make_float2(none(), 0.f);
+      }
+      __syncwarp();
+      if (fits) {
+        for (int q = li; q < total; q += LPR) {
+          const float mine = s_cv[warp][rr][q];
+          int rank = 0;
+          for (int o = 0; o < total; o += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(&s_cv[warp][rr][o]);
+            rank += v.x > mine || (v.x == mine && o < q);
+            rank += v.y > mine || (v.y == mine && o + 1 < q);
+            rank += v.z > mine || (v.z == mine && o + 2 < q);
+            rank += v.w > mine || (v.w == mine && o + 3 < q);
+          }
+          if (rank < rounds) ranked[rank] = make_float2(mine, __int_as_float(s_ce[warp][rr][q]));
+        }
+      }
+      if (!__all_sync(kFull, fits)) {
+        for (int j = 0; j < rounds; ++j) {
+          float m = none();
+          if (open) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) m = fmaxf(m, c[i]);
+          }
+          const float top = row_max<LPR>(m);
+          const unsigned have = __ballot_sync(kFull, open && m == top) >> (rr * LPR) & (LPR == 32 ? kFull : (1u << (LPR & 31)) - 1u);
+          if (have != 0u ? li == __ffs(have) - 1 : li == 0) {    // the lowest lane that has it, or none is left
+            bool found = have == 0u;
+            if (!fits && found) ranked[j] = make_float2(none(), 0.f);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+              if (!found && c[i] == top) {
+                found = true;
+                if (!fits) ranked[j] = make_float2(top, __int_as_float(base + i));
+                c[i] = none();
+              }
           }
         }
       }
       __syncwarp();
       if (MODE != 0 && has_bias) {
-        const uint32_t ck = lane < rounds ? ranked[lane].x : 0u;
-        const float c = key_float(ck), c_up = __shfl_up_sync(kFull, c, 1);
-        if (__any_sync(kFull, lane >= 1 && lane <= p.k && ck != 0u && c_up - c <= tol + 2.4e-7f * fabsf(c_up))) close_rows |= 1u << r;
+        const float v = li < p.k ? ranked[li].x : none(), next = li < p.k ? ranked[li + 1].x : none();
+        const unsigned close = __ballot_sync(kFull, v - next <= tol + 2.4e-7f * fabsf(v));
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+          if (close >> (q * LPR) & (LPR == 32 ? kFull : (1u << (LPR & 31)) - 1u)) close_rows |= 1u << (r0 + q);
+      }
+      if (MODE != 0 && grouped && (has_bias || p.top2)) {
+        const unsigned unsure = __ballot_sync(kFull, hangs);
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+          if (unsure >> (q * LPR) & 1u) unsure_rows |= 1u << (r0 + q);
       }
     }
-    if (MODE != 0 && (close_rows | unsure_rows) != 0u) {
-      for (unsigned left = close_rows | unsure_rows; left != 0u; left &= left - 1u) {
+    const unsigned real = (1u << rows) - 1u;
+    if (MODE != 0 && ((close_rows | unsure_rows) & real) != 0u) {
+      for (unsigned left = (close_rows | unsure_rows) & real; left != 0u; left &= left - 1u) {
         const int r = __ffs(left) - 1;
-        const uint2 c = lane < rounds ? s_ranked[warp][r][lane] : make_uint2(0u, 0u);
-        const int e = route_settle<Elem>(p, first + r, lane, c.x, int(c.y), rounds, __shfl_sync(kFull, my_tol, r * kPickLanes),
+        const float2 v = lane < rounds ? s_ranked[warp][r][lane] : make_float2(none(), 0.f);
+        const int e = route_settle<Elem>(p, first + r, lane, v.x, __float_as_int(v.y), rounds, __shfl_sync(kFull, my_tol, r * kPickLanes),
                                          close_rows >> r & 1, unsure_rows >> r & 1);
-        if (lane < p.k) s_ranked[warp][r][lane].y = uint32_t(e);
+        if (lane < p.k) s_ranked[warp][r][lane].y = __int_as_float(e);
         __syncwarp();
       }
       // Read again, so that nothing of a row's size is kept across the calls.
-      fetch_bias();
-      if (kAhead && first + stride < p.T) fetch(first + stride);
+      if (kAhead) fetch(first + stride + rr);
     }
 
     const int64_t row = first + lane / kPickLanes;
     const bool pick = lane / kPickLanes < rows && lane % kPickLanes < p.k;
-    const int my_e = pick ? int(s_ranked[warp][lane / kPickLanes][lane % kPickLanes].y) : 0;
+    const int my_e = pick ? __float_as_int(s_ranked[warp][lane / kPickLanes][lane % kPickLanes].y) : 0;
     __syncwarp();                                                // read before the next rows' are written
     const float zp = pick ? load_logit<Elem>(p.logits, row * p.E + my_e) : neg_inf();
     float w;
@@ -512,44 +575,58 @@ __global__ void __launch_bounds__(256) route_bias_kernel(const RouteParams p) {
 // 16 warps an SM.
 int rows_per_warp(int64_t T, int sms) { return T >= int64_t(sms) * 64 ? 4 : 1; }
 
-template <class Elem, int NV, int VB, bool FULL, int MODE>
+template <class Elem, int LPR, int NV, int VB, bool FULL, int MODE>
 cudaError_t fwd_launch(const RouteParams& p, int sms, cudaStream_t stream) {
-  const size_t smem = size_t(p.E) * sizeof(int);
-  if (p.T <= kRouteOneCtaRows) {
-    route_fwd_kernel<Elem, NV, VB, FULL, MODE><<<1, kRouteThreads, smem, stream>>>(p, 1);
+  const size_t counts = size_t(p.E) * sizeof(int), smem = counts + size_t(LPR) * ((NV + 3) / 4 * 4) * sizeof(float);
+  constexpr int R = kWarp / LPR;
+  if (p.T <= kRouteWarps * R) {                                  // one pass of one CTA, which then writes counts and bias
+    route_fwd_kernel<Elem, LPR, NV, VB, FULL, MODE><<<1, kRouteThreads, smem, stream>>>(p, R);
     return cudaGetLastError();
   }
-  cudaError_t e = cudaMemsetAsync(p.counts, 0, smem, stream);
+  cudaError_t e = cudaMemsetAsync(p.counts, 0, counts, stream);
   if (e != cudaSuccess) return e;
-  const int per = rows_per_warp(p.T, sms);
+  const int per = rows_per_warp(p.T, sms) > R ? rows_per_warp(p.T, sms) : R;
   const int64_t rows = int64_t(kRouteWarps) * per, want = (p.T + rows - 1) / rows;
   const int64_t most = int64_t(sms) * 8;
-  route_fwd_kernel<Elem, NV, VB, FULL, MODE><<<int(want < most ? want : most), kRouteThreads, smem, stream>>>(p, per);
+  route_fwd_kernel<Elem, LPR, NV, VB, FULL, MODE><<<int(want < most ? want : most), kRouteThreads, smem, stream>>>(p, per);
   if ((e = cudaGetLastError()) != cudaSuccess || p.bias_out == nullptr) return e;
   route_bias_kernel<<<(p.E + 255) / 256, 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <class Elem, int NV, int MODE>
+template <class Elem, int LPR, int NV, int MODE>
 cudaError_t fwd_width(const RouteParams& p, int sms, cudaStream_t stream) {
   constexpr int kSize = int(sizeof(typename Elem::Raw)), kRow = NV * kSize;
-  constexpr int VB = kRow % 16 == 0 ? 16 : kRow % 8 == 0 ? 8 : 4;
-  // Loads of VB bytes: every lane has NV experts, and rows, groups and the array are aligned.
-  const bool full = p.chunk == NV && p.gs == p.L * p.chunk;
+  constexpr int VB = kRow % 16 == 0 ? 16 : 8;
+  // Loads of VB bytes: every lane has NV experts or none, and rows, groups and the array are aligned.
+  const bool full = p.tchunk == NV && p.gs == (p.tchunk << p.tshift);
   if (full && int64_t(p.E) * kSize % VB == 0 && reinterpret_cast<uintptr_t>(p.logits) % VB == 0)
-    return fwd_launch<Elem, NV, VB, true, MODE>(p, sms, stream);
-  return fwd_launch<Elem, NV, kSize, false, MODE>(p, sms, stream);
+    return fwd_launch<Elem, LPR, NV, VB, true, MODE>(p, sms, stream);
+  return fwd_launch<Elem, LPR, NV, kSize, false, MODE>(p, sms, stream);
 }
 
+template <class Elem, int LPR, int MODE>
+cudaError_t fwd_lanes(const RouteParams& p, int sms, cudaStream_t stream) {
+  if (p.tchunk <= 8) return fwd_width<Elem, LPR, 8, MODE>(p, sms, stream);
+  if (p.tchunk <= 16) return fwd_width<Elem, LPR, 16, MODE>(p, sms, stream);
+  return fwd_width<Elem, LPR, 32, MODE>(p, sms, stream);
+}
+
+// The fewest lanes of a row that hold its groups apart with at most 32 experts a
+// lane: steps across lanes then serve the most rows.
 template <class Elem, int MODE>
-cudaError_t fwd_mode(const RouteParams& p, int sms, cudaStream_t stream) {
-  if (p.chunk <= 2) return fwd_width<Elem, 2, MODE>(p, sms, stream);
-  if (p.chunk <= 4) return fwd_width<Elem, 4, MODE>(p, sms, stream);
-  if (p.chunk <= 8) return fwd_width<Elem, 8, MODE>(p, sms, stream);
-  if (p.chunk <= 12) return fwd_width<Elem, 12, MODE>(p, sms, stream);
-  if (p.chunk <= 16) return fwd_width<Elem, 16, MODE>(p, sms, stream);
-  if (p.chunk <= 32) return fwd_width<Elem, 32, MODE>(p, sms, stream);
-  return fwd_launch<Elem, 64, int(sizeof(typename Elem::Raw)), false, MODE>(p, sms, stream);
+cudaError_t fwd_mode(RouteParams p, int sms, cudaStream_t stream) {
+  int groups = 1;                                                // rounded up to a power of two
+  while (groups < p.G) groups *= 2;
+  int lpr = groups < 8 ? 8 : groups;
+  while (lpr < kWarp && (p.gs + lpr / groups - 1) / (lpr / groups) > 32) lpr *= 2;
+  p.tshift = 0;
+  while (groups << (p.tshift + 1) <= lpr) ++p.tshift;
+  p.tchunk = (p.gs + (1 << p.tshift) - 1) >> p.tshift;
+  if (lpr == 8) return fwd_lanes<Elem, 8, MODE>(p, sms, stream);
+  if (lpr == 16) return fwd_lanes<Elem, 16, MODE>(p, sms, stream);
+  if (p.tchunk <= 32) return fwd_lanes<Elem, 32, MODE>(p, sms, stream);
+  return fwd_launch<Elem, 32, 64, int(sizeof(typename Elem::Raw)), false, MODE>(p, sms, stream);
 }
 
 template <class Elem>
