@@ -79,63 +79,76 @@ __device__ __forceinline__ float pick_share(float w, int k) {
   return sum > 0.f ? w / sum : 0.f;
 }
 
+// Doubles as integers in the same order (double comparisons share the few units
+// that double arithmetic has); what is not a number ranks lowest.
+__device__ __forceinline__ long long ordered(double v) {
+  const long long b = __double_as_longlong(v + 0.0);
+  return v == v ? b ^ (b >> 63 & 0x7fffffffffffffffll) : -0x7fffffffffffffffll - 1;
+}
+__device__ __forceinline__ double from_ordered(long long k) {
+  return __longlong_as_double(k ^ (k >> 63 & 0x7fffffffffffffffll));
+}
+
 // ---------------------------------------------------------------------------
 // The row ranked in double: the definition, by all lanes of the warp.  Lane j
 // gets pick j.  `bias` and the row are read again (they are in the caches).
 // ---------------------------------------------------------------------------
 template <class Elem>
 __device__ __noinline__ int route_row_double(const RouteParams& p, int64_t row, int lane) {
-  double c[64];                                                  // choice values of the lane's experts
+  long long c[64];                                               // choice values of the lane's experts
   const int g = lane / p.L, base = g * p.gs + (lane % p.L) * p.chunk;
   const int n = g < p.G ? max(0, min(p.chunk, p.gs - (lane % p.L) * p.chunk)) : 0;
-  const double ninf = double(neg_inf());
+  const long long masked = ordered(double(neg_inf()));
   float m = neg_inf();
-  for (int i = 0; i < n; ++i) m = fmaxf(m, load_logit<Elem>(p.logits, row * p.E + base + i));
-  m = warp_max_f(m);
-  double sum = 0.0;
-  for (int i = 0; i < n; ++i) {
-    const float z = load_logit<Elem>(p.logits, row * p.E + base + i);
-    double s = 0.0;
-    if (z > neg_inf()) s = p.softmax ? exp(double(z) - double(m)) : 1.0 / (1.0 + exp(-double(z)));
-    c[i] = s;
-    sum += s;
-  }
+  double sum = 1.0;
+  if (p.softmax) {
+    for (int i = 0; i < n; ++i) m = fmaxf(m, load_logit<Elem>(p.logits, row * p.E + base + i));
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-  double a = ninf, b = ninf;                                     // the two largest of the lane, then of the group
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+    sum = 0.0;
+    for (int i = 0; i < n; ++i) {
+      const float z = load_logit<Elem>(p.logits, row * p.E + base + i);
+      if (z > neg_inf()) sum += exp(double(z) - double(m));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+  }
+  long long a = masked, b = masked;                              // the two largest of the lane, then of the group
   unsigned long long gone = 0;
   for (int i = 0; i < n; ++i) {
     const float z = load_logit<Elem>(p.logits, row * p.E + base + i);
-    double v = p.softmax ? c[i] / sum : c[i];
-    if (p.bias != nullptr) v += double(p.bias[base + i]);
-    if (!(z > neg_inf())) v = ninf;
-    const double order = p.bias != nullptr || !(z > neg_inf()) ? v : double(z);
-    const double u = p.top2 ? v : order;
-    if (u > a) {
-      b = a;
-      a = u;
-    } else if (u > b) {
-      b = u;
+    long long v = masked, order = masked;
+    if (z > neg_inf()) {
+      double s = 0.0;
+      if (p.bias != nullptr || p.top2) {
+        s = p.softmax ? exp(double(z) - double(m)) / sum : 1.0 / (1.0 + exp(-double(z)));
+        if (p.bias != nullptr) s += double(p.bias[base + i]);
+      }
+      v = ordered(s);
+      order = p.bias != nullptr ? v : ordered(double(z));
     }
+    const long long u = p.top2 ? v : order;
+    b = max(b, min(a, u));
+    a = max(a, u);
     c[i] = order;
   }
   if (p.G > 1) {
     for (int off = 1; off < p.L; off <<= 1) {
-      const double a2 = __shfl_xor_sync(kFull, a, off), b2 = __shfl_xor_sync(kFull, b, off);
-      b = fmax(fmin(a, a2), fmax(b, b2));
-      a = fmax(a, a2);
+      const long long a2 = __shfl_xor_sync(kFull, a, off), b2 = __shfl_xor_sync(kFull, b, off);
+      b = max(min(a, a2), max(b, b2));
+      a = max(a, a2);
     }
-    const double score = p.top2 && b > ninf ? a + b : a;
+    const long long score = p.top2 && b > masked ? ordered(from_ordered(a) + from_ordered(b)) : a;
     int rank = 0;
     for (int o = 0; o < p.G; ++o) {
-      const double other = __shfl_sync(kFull, score, o * p.L);
+      const long long other = __shfl_sync(kFull, score, o * p.L);
       rank += other > score || (other == score && o < g);
     }
     if (rank >= p.keep) gone = ~0ull;
   }
   int mine = 0;
   for (int j = 0; j < p.k; ++j) {
-    double v = ninf;
+    long long v = masked;
     int e = 0x7fffffff;
     for (int i = 0; i < n; ++i)
       if (!(gone >> i & 1) && (e == 0x7fffffff || c[i] > v)) {
@@ -143,10 +156,9 @@ __device__ __noinline__ int route_row_double(const RouteParams& p, int64_t row, 
         e = base + i;
       }
     for (int off = 16; off > 0; off >>= 1) {
-      const double v2 = __shfl_xor_sync(kFull, v, off);
+      const long long v2 = __shfl_xor_sync(kFull, v, off);
       const int e2 = __shfl_xor_sync(kFull, e, off);
-      const bool take = e == 0x7fffffff ? e2 != 0x7fffffff : e2 != 0x7fffffff && (v2 > v || (v2 == v && e2 < e));
-      if (take) {
+      if (e2 != 0x7fffffff && (e == 0x7fffffff || v2 > v || (v2 == v && e2 < e))) {
         v = v2;
         e = e2;
       }
@@ -179,10 +191,10 @@ __device__ __noinline__ int route_settle(const RouteParams& p, int64_t row, int 
   if (!any_open) return ce;
   // The k + 1 largest are known as a set: one double-precision sigmoid a lane orders them.
   const bool in = there && lane <= p.k;
-  const double d = in && zc > neg_inf() ? 1.0 / (1.0 + exp(-double(zc))) + double(bc) : double(neg_inf());
+  const long long d = ordered(in && zc > neg_inf() ? 1.0 / (1.0 + exp(-double(zc))) + double(bc) : double(neg_inf()));
   int rank = 0;
   for (int o = 0; o <= p.k; ++o) {
-    const double od = __shfl_sync(kFull, d, o);
+    const long long od = __shfl_sync(kFull, d, o);
     const int oe = __shfl_sync(kFull, ce, o);
     rank += __shfl_sync(kFull, int(in), o) != 0 && (od > d || (od == d && oe < ce));
   }
@@ -313,7 +325,7 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
         for (int i = 0; i < NV; ++i) c[i] *= inv;
         // x e^-x <= 0.37: the rounded argument moves a score by 2^-23 * 0.37 * 1.45 of
         // the row's largest, ex2.approx by 2^-22 of itself, the sum of at most 64
-        // values a lane and 5 steps by 69 * 2^-24 of itself: 5e-6 covers them
+        // values a lane and 5 steps by 69 * 2^-24 of itself, the quotients by 2^-23: 5e-6 covers them
         tol = 1e-5f * inv;
         const int from = (lane / kPickLanes - r0) * LPR;         // the row whose pick the lane will hold
         const bool mine = lane / kPickLanes >= r0 && lane / kPickLanes < r0 + R;
@@ -326,9 +338,10 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
       } else if constexpr (MODE == 1) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) c[i] = rcp_approx(1.f + ex2_approx(logit(i) * -kLog2e));
-        // e = exp(-z) is off by 2^-22 + 2^-24 * 1.45 |z| of itself; s moves by
-        // s (1 - s) of that, below 2^-23, and rcp.approx and 1 + e by 2^-22 of s: 6e-7 covers them
-        tol = my_tol = 1.2e-6f;
+        // e = exp(-z) is off by 2^-22 (ex2.approx) + 1.5 |z| 2^-24 (its rounded argument and
+        // log2 e) of itself, which moves s by s (1 - s) of that, at most 0.7e-7; 1 + e is
+        // rounded (2^-24 of s), rcp.approx is off by 2^-23 of s: 2.6e-7 covers them
+        tol = my_tol = 5.2e-7f;
       }
       if constexpr (MODE != 0) {
 #pragma unroll
@@ -395,7 +408,8 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
         const bool kept = open && rank < p.keep;
         if (MODE != 0 && (has_bias || p.top2)) {
           const float lo = -row_max<LPR>(kept ? -score : none()), hi = row_max<LPR>(kept ? none() : score);
-          hangs = lo - hi <= (p.top2 ? 2.f * tol : tol) + 4.8e-7f * fabsf(lo);   // + the sums' own roundings
+          // 2.4e-7: four roundings of 2^-24 in the two sums with the bias and of two values
+          hangs = lo - hi <= (p.top2 ? 2.f * tol : tol) + 2.4e-7f * fabsf(lo);
         }
         open = kept;
       }
