@@ -313,20 +313,20 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
         for (int i = 1; i < NV; ++i) m = fmaxf(m, logit(i));
         const float top = row_max<LPR>(m);
         m = top > neg_inf() ? top : 0.f;
-        float sum = 0.f;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           c[i] = ex2_approx((logit(i) - m) * kLog2e);
-          sum += c[i];
+          part[i % 4] += c[i];
         }
-        sum = row_sum<LPR>(sum);
+        const float sum = row_sum<LPR>((part[0] + part[1]) + (part[2] + part[3]));
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) c[i] *= inv;
-        // x e^-x <= 0.37: the rounded argument moves a score by 2^-23 * 0.37 * 1.45 of
-        // the row's largest, ex2.approx by 2^-22 of itself, the sum of at most 64
-        // values a lane and 5 steps by 69 * 2^-24 of itself, the quotients by 2^-23: 5e-6 covers them
-        tol = 1e-5f * inv;
+        // In units of the row's largest score, 1 / sum: a score's rounded argument moves
+        // it by 3 * 2^-24 x e^-x <= 0.7e-7, ex2.approx by 2^-22 of itself and of the
+        // sum, the sum's NV / 4 + 7 additions by 2^-24 each, the quotient by 2^-23
+        tol = (2.f * 6.7e-7f + (NV / 4 + 7) * 2.f * 6e-8f) * inv;
         const int from = (lane / kPickLanes - r0) * LPR;         // the row whose pick the lane will hold
         const bool mine = lane / kPickLanes >= r0 && lane / kPickLanes < r0 + R;
         const float t = __shfl_sync(kFull, top, from & 31), u = __shfl_sync(kFull, sum, from & 31), v = __shfl_sync(kFull, tol, from & 31);
