@@ -113,19 +113,19 @@ template <bool BF16>
 __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const QuantRowsParams p) {
   using V = Values<BF16, kRowVals>;
   __shared__ float s_scale[kRowsBlocks][kRowsTile];
-  __shared__ int s_row[kRowsTile];
   const int64_t r0 = int64_t(blockIdx.x) * kRowsTile;
-  if (threadIdx.x < kRowsTile)
-    s_row[threadIdx.x] = r0 + threadIdx.x < p.M ? source_row(p.perm, p.k, r0 + threadIdx.x, p.rows) : -1;
-  __syncthreads();
   constexpr int kTeams = kQuantThreads / kRowLanes, kIter = kRowsTile * kRowsBlocks / kTeams;   // 32 teams, 4 blocks each
   const int team = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
   const int kb = team % kRowsBlocks;
   const int col = (blockIdx.y * kRowsBlocks + kb) * kScaleBlock + l * kRowVals;
+  // Lane i of the team finds the source of its i-th block.
+  static_assert(kIter <= kRowLanes, "a lane a block");
+  const int64_t r = r0 + l * (kRowsTile / kIter) + team / kRowsBlocks;
+  const int token = l < kIter && r < p.M ? source_row(p.perm, p.k, r, p.rows) : -1;
   V v[kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    const int t = s_row[i * (kRowsTile / kIter) + team / kRowsBlocks];
+    const int t = __shfl_sync(kFull, token, i, kRowLanes);
     if (t >= 0 && col < p.K) v[i].load(p.x, int64_t(t) * p.K + col);
     else v[i].zero();
   }
@@ -162,7 +162,6 @@ constexpr int kColsTile = 128, kColsLane = kColsTile / kWarp, kColsWarps = kQuan
 template <bool BF16>
 __global__ void __launch_bounds__(kQuantThreads) quantize_cols_kernel(const QuantColsParams p) {
   __shared__ int s_where[3];                                     // first row, rows, found
-  __shared__ int s_row[kScaleBlock];
   __shared__ __align__(16) uint32_t s_max[kColsWarps][kColsTile];
   __shared__ __align__(16) uint8_t s_q[kColsTile][kScaleBlock + 16];
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
@@ -199,14 +198,14 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_cols_kernel(const Quan
   }
   __syncthreads();
   if (s_where[2] == 0) return;                                   // behind the last expert: left as it is
-  if (threadIdx.x < kScaleBlock)
-    s_row[threadIdx.x] = threadIdx.x < s_where[1] ? source_row(p.perm, p.k, int64_t(s_where[0]) + threadIdx.x, p.rows) : -1;
-  __syncthreads();
+  // Lane i finds the source of the warp's i-th row.
+  const int r = warp * kColsRows + lane;
+  const int token = lane < kColsRows && r < s_where[1] ? source_row(p.perm, p.k, int64_t(s_where[0]) + r, p.rows) : -1;
   const int col = blockIdx.y * kColsTile + lane * kColsLane;
   Values<BF16, kColsLane> v[kColsRows];
 #pragma unroll
   for (int i = 0; i < kColsRows; ++i) {
-    const int t = s_row[warp * kColsRows + i];
+    const int t = __shfl_sync(kFull, token, i);
     if (t >= 0 && col < p.K) v[i].load(p.x, int64_t(t) * p.K + col);
     else v[i].zero();
   }
