@@ -170,24 +170,85 @@ __device__ __noinline__ int route_row_double(const RouteParams& p, int64_t row, 
 }
 
 // ---------------------------------------------------------------------------
+// Whether the row's best groups in double are those that fp32 has taken
+// (`kept`: bit g << tshift for group g), for sigmoid scores.  Only the experts
+// that can be among a group's two largest are evaluated, one a lane; false where
+// there are more than 32 of them.  `list`: 32 ints of shared memory.
+// ---------------------------------------------------------------------------
+template <class Elem>
+__device__ __noinline__ bool route_groups_hold(const RouteParams& p, int64_t row, int lane, float tol, unsigned kept, int* list) {
+  const int g = lane / p.L, base = g * p.gs + (lane % p.L) * p.chunk;
+  const int n = g < p.G ? max(0, min(p.chunk, p.gs - (lane % p.L) * p.chunk)) : 0;
+  const auto value = [&](int i) {
+    const float z = load_logit<Elem>(p.logits, row * p.E + base + i);
+    return z > neg_inf() ? rcp_approx(1.f + ex2_approx(z * -kLog2e)) + (p.bias != nullptr ? p.bias[base + i] : 0.f) : neg_inf();
+  };
+  float a = neg_inf(), b = neg_inf();
+  for (int i = 0; i < n; ++i) {
+    const float v = value(i);
+    b = fmaxf(b, fminf(a, v));
+    a = fmaxf(a, v);
+  }
+  for (int off = 1; off < p.L; off <<= 1) {
+    const float a2 = __shfl_xor_sync(kFull, a, off), b2 = __shfl_xor_sync(kFull, b, off);
+    b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+    a = fmaxf(a, a2);
+  }
+  const float last = p.top2 ? b : a, reach = last - (tol + 2.4e-7f * fabsf(last));
+  int total = 0;
+  for (int i = 0; i < p.chunk; ++i) {
+    const float v = i < n ? value(i) : neg_inf();
+    const bool in = v > neg_inf() && !(v < reach);               // a group without a second: every expert that is not masked
+    const unsigned m = __ballot_sync(kFull, in);
+    const int at = total + __popc(m & ((1u << lane) - 1u));
+    if (in && at < kWarp) list[at] = base + i;
+    total += __popc(m);
+  }
+  __syncwarp();
+  if (total > kWarp) return false;
+  const long long masked = ordered(double(neg_inf()));
+  const int e = lane < total ? list[lane] : 0, of = lane < total ? e / p.gs : -1;
+  long long v = masked;
+  if (lane < total)
+    v = ordered(1.0 / (1.0 + exp(-double(load_logit<Elem>(p.logits, row * p.E + e)))) + (p.bias != nullptr ? double(p.bias[e]) : 0.0));
+  long long a2 = masked, b2 = masked;                            // of group `lane`
+  for (int o = 0; o < total; ++o) {
+    const long long w = __shfl_sync(kFull, v, o);
+    if (__shfl_sync(kFull, of, o) == lane) {
+      b2 = max(b2, min(a2, w));
+      a2 = max(a2, w);
+    }
+  }
+  const long long score = p.top2 && b2 > masked ? ordered(from_ordered(a2) + from_ordered(b2)) : a2;
+  int rank = 0;
+  for (int o = 0; o < p.G; ++o) {
+    const long long other = __shfl_sync(kFull, score, o);
+    rank += other > score || (other == score && o < lane);
+  }
+  return __all_sync(kFull, lane >= p.G || (rank < p.keep) == ((kept >> ((lane << p.tshift) & 31) & 1u) != 0u));
+}
+
+// ---------------------------------------------------------------------------
 // The picks of a row where values that decide them are next to one another
 // (`close`), or where its groups' scores are (`unsure`).  Lane j holds the j-th
 // largest choice value and its expert, the k picks and two more.
 // ---------------------------------------------------------------------------
 template <class Elem>
 __device__ __noinline__ int route_settle(const RouteParams& p, int64_t row, int lane, float c, int ce, int rounds, float tol,
-                                         bool close, bool unsure) {
+                                         bool close, bool unsure, unsigned kept, int* list) {
+  if (unsure && (p.softmax || !route_groups_hold<Elem>(p, row, lane, tol, kept, list))) return route_row_double<Elem>(p, row, lane);
+  if (!close) return ce;
   const bool there = lane < rounds && c == c;
   const float zc = there ? load_logit<Elem>(p.logits, row * p.E + ce) : neg_inf();
   const float bc = there && p.bias != nullptr ? p.bias[ce] : 0.f;
   const float c_up = __shfl_up_sync(kFull, c, 1), z_up = __shfl_up_sync(kFull, zc, 1), b_up = __shfl_up_sync(kFull, bc, 1);
   // sure all the same where the inputs are equal
-  const bool open = close && lane >= 1 && lane <= p.k && there && c_up - c <= tol + 2.4e-7f * fabsf(c_up) &&
+  const bool open = lane >= 1 && lane <= p.k && there && c_up - c <= tol + 2.4e-7f * fabsf(c_up) &&
                     !(zc == z_up && bc == b_up);
   const float last = __shfl_sync(kFull, c, p.k - 1);
   const bool beyond = lane == p.k + 1 && there && last - c <= tol + 2.4e-7f * fabsf(last);
   const bool any_open = __any_sync(kFull, open), any_beyond = __any_sync(kFull, beyond);
-  if (unsure || (any_open && (any_beyond || p.softmax))) return route_row_double<Elem>(p, row, lane);
+  if (any_open && (any_beyond || p.softmax)) return route_row_double<Elem>(p, row, lane);
   if (!any_open) return ce;
   // The k + 1 largest are known as a set: one double-precision sigmoid a lane orders them.
   const bool in = there && lane <= p.k;
@@ -222,7 +283,8 @@ __device__ __noinline__ int route_settle(const RouteParams& p, int64_t row, int 
 // rounding are settled behind a warp's four rows, and then the gates of all of
 // them are computed, a pick a lane.
 // Instructions bound it.  For a row of 256 in 8 groups: 1145 with a warp a row whose
-// lanes sort their experts, 728 with a warp a row and this selection.
+// lanes sort their experts, 728 with a warp a row and this selection, 436 with 8 lanes
+// a row: 131,072 rows of bf16 in 90 us (0.8 TB/s), where the bytes alone would take 11.
 // ---------------------------------------------------------------------------
 constexpr int kMaxRounds = 10;                                   // 8 picks and two more
 constexpr int kMaxPer = kWarp / kPickLanes;                      // rows a warp finishes at once
@@ -255,6 +317,7 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
   __shared__ __align__(16) float s_cv[kRouteWarps][R][kCand];    // candidates, in expert order
   __shared__ int s_ce[kRouteWarps][R][kCand];
   __shared__ float2 s_ranked[kRouteWarps][kMaxPer][kMaxRounds];  // value and expert (as bits), largest first
+  __shared__ unsigned s_kept[kRouteWarps][kMaxPer];              // lanes of the groups taken
   extern __shared__ __align__(16) float s_bias[];                // in lane order, NV (rounded up to 4) a lane; then
   int* s_hist = reinterpret_cast<int*>(s_bias + LPR * ((NV + 3) / 4 * 4));   // the counts [E]
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
@@ -412,6 +475,8 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
           hangs = lo - hi <= (p.top2 ? 2.f * tol : tol) + 2.4e-7f * fabsf(lo);
         }
         open = kept;
+        const unsigned lanes = __ballot_sync(kFull, kept);
+        if (li == 0) s_kept[warp][r0 + rr] = lanes >> (rr * LPR);
       }
 
       // The bound.
@@ -531,7 +596,7 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
         const int r = __ffs(left) - 1;
         const float2 v = lane < rounds ? s_ranked[warp][r][lane] : make_float2(none(), 0.f);
         const int e = route_settle<Elem>(p, first + r, lane, v.x, __float_as_int(v.y), rounds, __shfl_sync(kFull, my_tol, r * kPickLanes),
-                                         close_rows >> r & 1, unsure_rows >> r & 1);
+                                         close_rows >> r & 1, unsure_rows >> r & 1, s_kept[warp][r], &s_ce[warp][0][0]);
         if (lane < p.k) s_ranked[warp][r][lane].y = __int_as_float(e);
         __syncwarp();
       }
@@ -585,15 +650,20 @@ __global__ void __launch_bounds__(256) route_bias_kernel(const RouteParams p) {
   p.bias_out[e] = over > 0 ? b + p.bias_gamma : over < 0 ? b - p.bias_gamma : b;
 }
 
-// Four rows a warp share the work on the picks; one row where that leaves fewer than
-// 16 warps an SM.
+// Four rows a warp share the work on the picks; where a pass has fewer, only from 64 rows
+// an SM on (1024 experts, a row a pass: 2048 rows 24.7 us with one row a warp and 32.8 with
+// four, 8192 rows 39.7 and 38.8, 32,768 rows 112 and 99).
 int rows_per_warp(int64_t T, int sms) { return T >= int64_t(sms) * 64 ? 4 : 1; }
+// Passes of one CTA alone, which writes counts and bias without a second and third
+// launch (256 experts, 32 rows a pass, with a bias: 33 rows 14.0 us against 15.2 with
+// more CTAs, 64 rows 10.6 against 11.2, 96 rows 14.4 against 12.3).
+constexpr int kOneCtaPasses = 2;
 
 template <class Elem, int LPR, int NV, int VB, bool FULL, int MODE>
 cudaError_t fwd_launch(const RouteParams& p, int sms, cudaStream_t stream) {
   const size_t counts = size_t(p.E) * sizeof(int), smem = counts + size_t(LPR) * ((NV + 3) / 4 * 4) * sizeof(float);
   constexpr int R = kWarp / LPR;
-  if (p.T <= kRouteWarps * R) {                                  // one pass of one CTA, which then writes counts and bias
+  if (p.T <= kOneCtaPasses * kRouteWarps * R) {
     route_fwd_kernel<Elem, LPR, NV, VB, FULL, MODE><<<1, kRouteThreads, smem, stream>>>(p, R);
     return cudaGetLastError();
   }
@@ -668,15 +738,17 @@ __device__ __forceinline__ float sum_same(float v, int e, int k) {
   return total;
 }
 
-// `per` rows a warp, lane 8 r + j with pick j of row r.
+// Four rows a warp, lane 8 r + j with pick j of row r.  (One row a warp is no faster even
+// for few rows: 4096 x 256 3.7 us against 3.0, 65,536 30 us against 15.)
 template <class Elem, bool VEC>
-__global__ void __launch_bounds__(kRouteThreads) route_bwd_picks_kernel(const RouteBwdParams p, const int per) {
+__global__ void __launch_bounds__(kRouteThreads) route_bwd_picks_kernel(const RouteBwdParams p) {
+  constexpr int per = kMaxPer;
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   const int j = lane % kPickLanes;
   const int64_t stride = int64_t(gridDim.x) * kRouteWarps * per;
   for (int64_t first = (int64_t(blockIdx.x) * kRouteWarps + warp) * per; first < p.T; first += stride) {
     const int64_t row = first + lane / kPickLanes;
-    const bool there = lane / kPickLanes < per && row < p.T && j < p.k;
+    const bool there = row < p.T && j < p.k;
     const int e = there ? p.idx[row * p.k + j] : -1;
     const bool live = e >= 0 && e < p.E;
     const float dg = live ? p.scale * p.dgate[row * p.k + j] : 0.f;
@@ -748,15 +820,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_softmax_kernel(const 
 template <class Elem>
 cudaError_t bwd_elem(const RouteBwdParams& p, int sms, cudaStream_t stream) {
   const bool picks = !p.softmax || p.renorm;
-  const int per = picks ? rows_per_warp(p.T, sms) : 1;
-  const int64_t rows = int64_t(kRouteWarps) * per, want = (p.T + rows - 1) / rows;
+  const int64_t rows = int64_t(kRouteWarps) * (picks ? kMaxPer : 1), want = (p.T + rows - 1) / rows;
   const int64_t most = int64_t(sms) * 8;
   const int grid = int(want < most ? want : most);
   if (picks) {
     if (p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.dlogits) % 16 == 0)
-      route_bwd_picks_kernel<Elem, true><<<grid, kRouteThreads, 0, stream>>>(p, per);
+      route_bwd_picks_kernel<Elem, true><<<grid, kRouteThreads, 0, stream>>>(p);
     else
-      route_bwd_picks_kernel<Elem, false><<<grid, kRouteThreads, 0, stream>>>(p, per);
+      route_bwd_picks_kernel<Elem, false><<<grid, kRouteThreads, 0, stream>>>(p);
   } else if (p.E <= 4 * kWarp) {
     route_bwd_softmax_kernel<Elem, 4><<<grid, kRouteThreads, 0, stream>>>(p);
   } else if (p.E <= 8 * kWarp) {

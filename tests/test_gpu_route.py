@@ -155,6 +155,31 @@ def test_choice_values_that_fp32_cannot_tell_apart(mr, score, grouped):
     check(mr, zt, 8, score, None, 4, 2, "top2")
 
 
+@pytest.mark.parametrize("shape", [(512, 8, 4), (1024, 8, 4), (96, 32, 5), (510, 17, 9)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("biased", [False, True])
+def test_groups_that_fp32_cannot_tell_apart(mr, shape, biased):
+    """Groups whose two largest are another group's, or next to them, among many experts;
+    in some rows groups of one expert or of none, and groups of experts all alike."""
+    E, G, keep = shape
+    T, gs = 700, E // G
+    rng = np.random.default_rng(E + G)
+    z = (rng.standard_normal((T, G, gs)) * 1.5).astype(np.float32)
+    bias = np.repeat(bias_of(gs, 5)[None], G, 0).ravel() if biased else None
+    for t in range(T):
+        for g in range(1, G, 2):                                  # the group before it, in another order, half of them moved
+            z[t, g] = z[t, g - 1] if biased else rng.permutation(z[t, g - 1])
+            if rng.random() < 0.5:
+                i = int(np.argmax(z[t, g]))
+                z[t, g, i] = np.nextafter(z[t, g, i], np.float32(9 if rng.random() < 0.5 else -9))
+    z[600:620, :, 1:] = -np.inf
+    z[620:640, : G // 2] = -np.inf
+    z[640:660] = z[640:660, :, :1]
+    z = torch.from_numpy(z.reshape(T, E))
+    for group_score in ("top2", "max"):
+        check(mr, z, 4, "sigmoid", bias, G, keep, group_score)
+        check(mr, z.to(torch.bfloat16), 4, "sigmoid", bias, G, keep, group_score)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_masked_logits(mr, score, dtype):
