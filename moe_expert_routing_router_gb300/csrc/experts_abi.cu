@@ -169,7 +169,9 @@ moe_status moe_quantize_cols(const void* x, moe_dtype dt, int64_t rows, int64_t 
   if (!aligned(offsets, 4) || !aligned(kept, 4)) return fail(MOE_ERR_INVALID, "offsets or kept is not 4-byte aligned");
   moe::QuantColsParams p = {x, rows, M, K, k, E, offsets, kept, perm, moe_quantize_cols_width(M, E), static_cast<uint8_t*>(q), scale};
   if (p.width >= kInt32Limit) return fail(MOE_ERR_INVALID, "M = %lld over E = %d experts is too wide", (long long)M, E);
-  return launched(moe::launch_quantize_cols(p, dt == MOE_DTYPE_BF16, stream), "moe_quantize_cols launch");
+  int sms = 0;
+  if ((s = moe::abi_sms(&sms)) != MOE_OK) return s;
+  return launched(moe::launch_quantize_cols(p, dt == MOE_DTYPE_BF16, sms, stream), "moe_quantize_cols launch");
 }
 
 moe_status moe_quantize_weights(const void* w, moe_dtype dt, int32_t E, int32_t N, int32_t K,

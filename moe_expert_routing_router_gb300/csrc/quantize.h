@@ -28,8 +28,9 @@ struct QuantColsParams {
   int64_t width;          // columns of q
   uint8_t* q;             // [K, width] e4m3
   float* scale;           // [width/128, K]
+  int64_t share;          // tiles of a CTA, set by the launcher
 };
-cudaError_t launch_quantize_cols(const QuantColsParams& p, bool bf16, cudaStream_t stream);
+cudaError_t launch_quantize_cols(QuantColsParams p, bool bf16, int sms, cudaStream_t stream);
 
 struct QuantWeightsParams {
   const void* w;          // [E, N, K]
