@@ -124,7 +124,8 @@ MOE_API moe_status moe_quantize_rows(const void* x, moe_dtype dt, int64_t rows, 
  * last expert's are left as they are.  width = moe_quantize_cols_width(M, E) =
  * 128 * floor((M + 127 E) / 128), which holds any split of M rows.  Rows are
  * gathered by perm as in moe_quantize_rows; offsets and kept as in
- * moe_expert_matmul (kept may be NULL: every row). */
+ * moe_expert_matmul (kept may be NULL: every row).  x, q and scale are 16-byte
+ * aligned. */
 MOE_API int64_t moe_quantize_cols_width(int64_t M, int32_t E);
 MOE_API moe_status moe_quantize_cols(const void* x, moe_dtype dt, int64_t rows, int64_t M, int32_t K, int32_t E,
                                      const int32_t* offsets, const int32_t* kept, const int32_t* perm, int32_t k,
@@ -149,8 +150,9 @@ MOE_API moe_status moe_quantize_weights(const void* w, moe_dtype dt, int32_t E, 
  *   wq [E,N,K] e4m3, wscale [E, ceil(N/128), ceil(K/128)] fp32: as moe_quantize_weights
  *   out [M,N] bf16 or fp32 (out_dt)
  * Scales may be any fp32 numbers.  A block's 128 products are summed by the
- * tensor core in fp32, the blocks in fp32 registers, in order; the one rounding
- * to bf16 is at the end.  A row's result does not depend on the other rows.
+ * tensor core in fp32 (where products below about 2^-25 of the block's largest
+ * may be lost), the blocks in fp32 registers, in order; the one rounding to bf16
+ * is at the end.  A row's result does not depend on the other rows.
  * The data gradient is the same call with dy's rows and the transposed weights.
  * K and N are multiples of 16 up to MOE_MAX_WIDTH, E * N < 2^31, M >= 1, M < 2^31;
  * q, wq and out are 16-byte aligned.
@@ -168,7 +170,7 @@ MOE_API moe_status moe_expert_matmul(const void* q, const float* scale, int64_t 
  *   moe_quantize_cols of the rows of dy and x with the same offsets and kept
  *   kept [E]: the rows of each expert
  * Sums as in moe_expert_matmul.  K and N as there; width is a multiple of 128
- * below 2^31. */
+ * below 2^31; all arrays but kept are 16-byte aligned. */
 MOE_API moe_status moe_expert_wgrad(const void* dyq, const float* dyscale, const void* xq, const float* xscale,
                                     int64_t width, int32_t N, int32_t K, int32_t E, const int32_t* kept, float* dw,
                                     moe_stream_t stream);

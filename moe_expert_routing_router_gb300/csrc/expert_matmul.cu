@@ -33,7 +33,7 @@ constexpr int kEpiWarps = 16, kFirstEpi = 4;
 constexpr int kMmThreads = (kFirstEpi + kEpiWarps) * kWarp;
 constexpr int kTmemCols = 512;
 constexpr int kMaxE = 1024;
-constexpr int kOutCols = 16;                  // columns of a tensor copy of results: 64 bytes of fp32
+constexpr int kOutCols = 32;                  // columns of a tensor copy of results: 128 bytes of fp32
 constexpr int kWarpOutBytes = 32 * kOutCols * 4;
 constexpr int kGroupM = 16;                   // row tiles of an expert that are taken before the next column tile
 constexpr unsigned kFull = 0xffffffffu;
@@ -76,10 +76,14 @@ __device__ __forceinline__ void tma_store_3d(const void* src, const CUtensorMap*
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
                :: "l"(map), "r"(smem_addr(src)), "r"(x), "r"(y), "r"(z) : "memory");
 }
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar)) : "memory");
+}
 // Ends a group of stores; a group may be empty.
 __device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// Until all but the thread's last group have read their shared memory / all have ended.
-__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+// Until the thread's groups have read their shared memory / have ended.
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -147,31 +151,37 @@ template <int BN, int RB, bool STORE>
 struct Tile {
   static constexpr int kBlockBytes = (kBM + BN) * kBK;
   static constexpr int kStageBytes = RB * kBlockBytes;
-  static constexpr int kOutBytes = STORE ? kEpiWarps * 2 * kWarpOutBytes : 0;
+  static constexpr int kOutBytes = STORE ? kEpiWarps * kWarpOutBytes : 0;
   static constexpr int kStages = 196608 / kStageBytes - (STORE ? 1 : 0);   // 192 KB, or 144 KB, of operands
   static constexpr int kBufs = kTmemCols / (BN * RB);          // stages' products in tensor memory
   static constexpr int kCols = BN / 4;                         // columns of one epilogue warp
 };
 
+// Blocks whose scales the weight gradient holds in shared memory: its producer copies them
+// beside the operands (32,836 rows of 32 experts, 2048 x 2048: 228 us, against 282 with loads
+// by the epilogue's lanes and narrower copies of the results).
+constexpr int kScaleSlots = 6;
+
+template <bool WGRAD>
 struct alignas(16) Shared {
   // full: a stage's operands have landed; done: its product has been formed (the
-  // producer may fill it again, the epilogue may read); tempty: the product has been read
-  uint64_t full[8], done[8], tempty[8], drain;
+  // producer may fill it again, the epilogue may read); tempty: the product has been read;
+  // scales: a block's scales have landed
+  uint64_t full[8], done[8], tempty[8], drain, scales[kScaleSlots];
   uint32_t tmem;
   int abort;
-  int first[kMaxE + 1];                                        // tiles before expert e
   int block[kMaxE + 1];                                        // weight gradient: column blocks before expert e; product: its first row
-  union {
-    int count[kMaxE];                                          // product: an expert's rows
-    float4 bscale[kEpiWarps][2][16];                           // weight gradient: a block's column scales, per warp
-  };
+  int first[WGRAD ? 1 : kMaxE + 1];                            // product: tiles before expert e
+  int count[WGRAD ? 1 : kMaxE];                                // product: its rows
+  alignas(16) float scale[WGRAD ? kScaleSlots : 1][kBM + 256]; // weight gradient: a block's scales of rows and columns
 };
 
 // Bounded wait that every role uses: false once it, or another role's, ran out.
 // Time is counted in SM cycles (at most about two a nanosecond), whose counter is
 // read in a few cycles, and only after some waits have failed.
 // With a second barrier, both are tested at once: a test takes some 100 cycles.
-__device__ __forceinline__ bool mm_wait(Shared& sh, const MatmulParams& p, uint64_t* bar, uint32_t parity,
+template <class S>
+__device__ __forceinline__ bool mm_wait(S& sh, const MatmulParams& p, uint64_t* bar, uint32_t parity,
                                         uint64_t* bar2 = nullptr, uint32_t parity2 = 0) {
   const auto test = [&]() {
     const bool a = mbar_test(bar, parity), b = bar2 == nullptr || mbar_test(bar2, parity2);
@@ -216,16 +226,22 @@ struct Walk {
   int block0 = 0, blocks = 0;     // blocks along the contraction
 
   template <int BN, bool WGRAD>
-  __device__ __forceinline__ void at(const MatmulParams& p, const Shared& sh, int tile) {
-    for (;;) {                                                   // the expert that has the tile: 32 at a time, by the whole warp
-      const int next = e + 1 + int(threadIdx.x % kWarp);
-      const unsigned past = __ballot_sync(kFull, next <= p.E && sh.first[next] <= tile);
-      e += __popc(past);
-      if (past != kFull) break;
-    }
-    const int i = tile - sh.first[e];
+  __device__ __forceinline__ void at(const MatmulParams& p, const Shared<WGRAD>& sh, int tile) {
     const int ct = (p.C + BN - 1) / BN;
-    const int rt = (sh.first[e + 1] - sh.first[e]) / ct;
+    int i = tile, rt = (p.R + kBM - 1) / kBM;                    // of the expert: the tile's place, tiles of rows
+    if constexpr (WGRAD) {
+      e = tile / (rt * ct);
+      i -= e * rt * ct;
+    } else {
+      for (;;) {                                                 // the expert that has the tile: 32 at a time, by the whole warp
+        const int next = e + 1 + int(threadIdx.x % kWarp);
+        const unsigned past = __ballot_sync(kFull, next <= p.E && sh.first[next] <= tile);
+        e += __popc(past);
+        if (past != kFull) break;
+      }
+      i -= sh.first[e];
+      rt = (sh.first[e + 1] - sh.first[e]) / ct;
+    }
     // kGroupM row tiles by all column tiles at a time, rows fastest: the CTAs at
     // work share both operands' tiles in L2.
     const int group = i / (kGroupM * ct), in = i - group * kGroupM * ct;
@@ -255,7 +271,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
                      const __grid_constant__ CUtensorMap map_out) {
   using TL = Tile<BN, RB, WGRAD>;
   extern __shared__ uint8_t s_dyn[];
-  __shared__ Shared sh;
+  __shared__ Shared<WGRAD> sh;
   uint8_t* ring = s_dyn + (1024 - smem_addr(s_dyn) % 1024) % 1024;
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
 
@@ -267,9 +283,9 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
         mbar_init(&sh.full[i], 1 + p.extra);
         mbar_init(&sh.done[i], 1);
       }
-      for (int i = 0; i < TL::kBufs; ++i) {
-        mbar_init(&sh.tempty[i], kEpiWarps);
-      }
+      for (int i = 0; i < TL::kBufs; ++i) mbar_init(&sh.tempty[i], kEpiWarps);
+      if constexpr (WGRAD)
+        for (int i = 0; i < kScaleSlots; ++i) mbar_init(&sh.scales[i], 1);
       mbar_init(&sh.drain, 1);
       mbar_fence_init();
       // an error that the host has not read yet: write nothing
@@ -285,7 +301,6 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       int t = 0, b = 0;
       if (e0 + lane < p.E) {
         if constexpr (WGRAD) {
-          t = (p.R + kBM - 1) / kBM * ct;
           b = int((max(int64_t(p.kept[e0 + lane]), int64_t(0)) + kBK - 1) / kBK);
         } else {
           int64_t start, n;
@@ -305,21 +320,25 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
         }
       }
       if (e0 + lane < p.E) {
-        sh.first[e0 + lane] = tiles + ti - t;
-        if constexpr (WGRAD) sh.block[e0 + lane] = int(min(int64_t(blocks) + bi - b, p.blocks));   // inside the operands
+        if constexpr (!WGRAD) sh.first[e0 + lane] = tiles + ti - t;
+        else sh.block[e0 + lane] = int(min(int64_t(blocks) + bi - b, p.blocks));   // inside the operands
       }
       tiles += __shfl_sync(kFull, ti, kWarp - 1);
       blocks = int(min(int64_t(blocks) + __shfl_sync(kFull, bi, kWarp - 1), p.blocks));
     }
     if (lane == 0) {
-      sh.first[p.E] = tiles;
-      if constexpr (WGRAD) sh.block[p.E] = blocks;
+      if constexpr (!WGRAD) sh.first[p.E] = tiles;
+      else sh.block[p.E] = blocks;
     }
   }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const int n_tiles = sh.abort != 0 ? 0 : sh.first[p.E];
+  int n_tiles = 0;
+  if (sh.abort == 0) {
+    if constexpr (WGRAD) n_tiles = p.E * ((p.R + kBM - 1) / kBM) * ((p.C + BN - 1) / BN);
+    else n_tiles = sh.first[p.E];
+  }
   __syncthreads();                                               // every thread has seen abort before a role sets it
 
   // The epilogue's sums want more registers than an even split gives: of the
@@ -332,7 +351,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
     // in a branch of its own a block took 430 ns however little it copied.)
     if (warp == 0) {
       // ---- producer: one stage per block ----
-      int s = 0, issued = 0;
+      int s = 0, issued = 0, q = 0;
       uint32_t phase = 0;
       bool ok = true;
       Walk w;
@@ -345,6 +364,16 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
           ok = __all_sync(kFull, mm_wait(sh, p, &sh.done[s], phase ^ 1u));
           if (!ok) break;
           if (elect_one()) {
+            // A block's scales go where those of the block six before were: the stage that is
+            // free held the block three before, whose product was formed when the one five
+            // before had been read.
+            if constexpr (WGRAD) {
+              static_assert(kScaleSlots > TL::kStages + TL::kBufs, "scales that are still read");
+              const int64_t blk = w.block0 + b;
+              mbar_arrive_expect_tx(&sh.scales[q], uint32_t(w.rows + w.cols) * 4u);
+              bulk_load(sh.scale[q], p.a_scale + blk * p.R + w.r0, uint32_t(w.rows) * 4u, &sh.scales[q]);
+              bulk_load(sh.scale[q] + kBM, p.b_scale + blk * p.C + w.col0, uint32_t(w.cols) * 4u, &sh.scales[q]);
+            }
             uint64_t* bar = &sh.full[s];
             mbar_arrive_expect_tx(bar, uint32_t((na + nb) * now * kBox * kBK));
             for (int j = 0; j < now; ++j) {
@@ -359,6 +388,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
           }
           __syncwarp();
           ++issued;
+          if (++q == kScaleSlots) q = 0;
           if (++s == TL::kStages) {
             s = 0;
             phase ^= 1u;
@@ -369,6 +399,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
         for (int i = 0; i < TL::kStages && i < issued; ++i) {
           const int back = issued - 1 - i;
           mbar_wait(&sh.full[back % TL::kStages], uint32_t(back / TL::kStages) & 1u, p.timeout_ns);
+          if constexpr (WGRAD) mbar_wait(&sh.scales[back % kScaleSlots], uint32_t(back / kScaleSlots) & 1u, p.timeout_ns);
         }
       }
     } else if (warp == 1) {
@@ -395,7 +426,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
               for (int k = 0; k < kBK / 32; ++k)                 // 32 bytes along the row: 2 units of 16
                 tc_mma_f8(tmem + (t * RB + j) * BN, da + k * 2, db + k * 2, idesc, k > 0);
             }
-            tc_commit(&sh.done[s]);                          // the stage is free, and the product there
+            tc_commit(&sh.done[s]);                              // the stage is free, and the product there
           }
           __syncwarp();
           if (++s == TL::kStages) {
@@ -419,31 +450,24 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
     // ---- epilogue: rows 32 * quad + lane, kCols columns ----
     constexpr int CW = TL::kCols;
     const int quad = warp % 4, cg = (warp - kFirstEpi) / 4, row = quad * 32 + lane;
-    float4(*s_bs)[16] = sh.bscale[warp - kFirstEpi];
     const int kblocks = (p.K + kBK - 1) / kBK, cblocks = (p.C + kBK - 1) / kBK;
-    int s = 0, t = 0;
-    uint32_t phase = 0;
+    int s = 0, t = 0, q = 0;
+    uint32_t phase = 0, qphase = 0;
     bool ok = true;
     Walk w;
     int c0 = 0;                                                  // the warp's first column of out
-    bool busy = false, live = false, col = false;                // whether the warp has anything to add, the lane a row,
-    const float *pa = nullptr, *pb = nullptr;                    // and (weight gradient) four column scales
-    const int64_t step_a = WGRAD ? int64_t(p.R) : p.M, step_b = WGRAD ? p.C : 1;
+    bool busy = false, live = false;                             // whether the warp has anything to add, the lane a row
+    const float *pa = nullptr, *pb = nullptr;
     float sa[RB] = {}, sb[RB] = {};
-    float4 sb4 = make_float4(0.f, 0.f, 0.f, 0.f);
-    const auto fetch = [&](int b) {                              // the scales of a stage's blocks
+    const auto fetch = [&](int b) {                              // product: the scales of a stage's blocks
 #pragma unroll
       for (int j = 0; j < RB; ++j) {
         if (busy && b + j < w.blocks) {
           sa[j] = live ? *pa : 0.f;
-          if constexpr (WGRAD) {
-            if (col) sb4 = *reinterpret_cast<const float4*>(pb);
-          } else {
-            sb[j] = *pb;
-          }
+          sb[j] = *pb;
         }
-        pa += step_a;
-        pb += step_b;
+        pa += p.M;
+        pb += 1;
       }
     };
     const auto begin = [&](int tile) {                           // a tile's place and its first scales
@@ -451,15 +475,11 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       c0 = w.col0 + cg * CW;
       busy = quad * 32 < w.rows && c0 < p.C;                     // warp-uniform
       live = row < w.rows;
-      if constexpr (WGRAD) {
-        col = lane * 4 < CW && c0 + lane * 4 < p.C;
-        pa = p.a_scale + int64_t(w.block0) * p.R + w.r0 + row;
-        pb = p.b_scale + int64_t(w.block0) * p.C + c0 + lane * 4;
-      } else {
+      if constexpr (!WGRAD) {
         pa = p.a_scale + w.row0 + row;
         pb = p.b_scale + (int64_t(w.e) * cblocks + c0 / kBK) * kblocks;
+        fetch(0);
       }
-      fetch(0);
     };
     if (!WGRAD && int(blockIdx.x) < n_tiles) begin(blockIdx.x);
     for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
@@ -469,21 +489,17 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       for (int i = 0; i < CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
       for (int b = 0; b < w.blocks; b += RB) {
         float scale[RB];
+        if constexpr (!WGRAD) {
 #pragma unroll
-        for (int j = 0; j < RB; ++j) scale[j] = WGRAD ? sa[j] : sa[j] * sb[j];
-        if constexpr (WGRAD) {
-          static_assert(!WGRAD || RB == 1, "two buffers of column scales serve single blocks");
-          if (lane * 4 < CW) s_bs[b & 1][lane] = sb4;
-          __syncwarp();
+          for (int j = 0; j < RB; ++j) scale[j] = sa[j] * sb[j];
+          // The next scales, in front of the wait (508 us against 535 at 65,536 rows).
+          fetch(b + RB);
         }
-        // The next scales: in front of the wait (508 us against 535 at 65,536 rows), but
-        // behind it for the weight gradient, whose loads of column scales hold it up (280
-        // us against 297).
-        if constexpr (!WGRAD) fetch(b + RB);
-        ok = __all_sync(kFull, mm_wait(sh, p, &sh.done[s], phase));   // one answer for the warp
+        ok = __all_sync(kFull, mm_wait(sh, p, &sh.done[s], phase, WGRAD ? &sh.scales[q] : nullptr, qphase));   // one answer for the warp
         if (!ok) break;
         tc_fence_after();
-        if constexpr (WGRAD) fetch(b + RB);
+        const float* block_scales = sh.scale[WGRAD ? q : 0];
+        if constexpr (WGRAD) scale[0] = block_scales[row];       // a row behind the last one is not stored
         // The buffer is free as soon as its last columns have been read.
         const auto release = [&]() {
           tc_fence_before();
@@ -507,9 +523,9 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
                 const float2 x = make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1]));
                 const float2 y = make_float2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3]));
                 if constexpr (WGRAD) {
-                  const float4 q = s_bs[b & 1][(c + i) / 4];
-                  acc[(c + i) / 2] = fma2(mul2(x, s2), make_float2(q.x, q.y), acc[(c + i) / 2]);
-                  acc[(c + i) / 2 + 1] = fma2(mul2(y, s2), make_float2(q.z, q.w), acc[(c + i) / 2 + 1]);
+                  const float4 f = *reinterpret_cast<const float4*>(&block_scales[kBM + cg * CW + c + i]);
+                  acc[(c + i) / 2] = fma2(mul2(x, s2), make_float2(f.x, f.y), acc[(c + i) / 2]);
+                  acc[(c + i) / 2 + 1] = fma2(mul2(y, s2), make_float2(f.z, f.w), acc[(c + i) / 2 + 1]);
                 } else {
                   acc[(c + i) / 2] = fma2(x, s2, acc[(c + i) / 2]);
                   acc[(c + i) / 2 + 1] = fma2(y, s2, acc[(c + i) / 2 + 1]);
@@ -526,32 +542,34 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
           phase ^= 1u;
         }
         if (++t == TL::kBufs) t = 0;
+        if (++q == kScaleSlots) {
+          q = 0;
+          qphase ^= 1u;
+        }
       }
       if (!ok) break;
-      // The next tile's first scales are on their way while this one is stored.  (The
-      // weight gradient has no registers left for that: 280 us without, 307 with.)
+      // The next tile's first scales are on their way while this one is stored.
       const bool store = busy;
       const int to_c0 = c0, to_rows = w.rows, to_row0 = WGRAD ? w.r0 : w.row0, to_e = w.e;
       if (!WGRAD && tile + int(gridDim.x) < n_tiles) begin(tile + gridDim.x);
       if (!store) continue;
       if constexpr (WGRAD) {
-        // 32 x 16 values at a time through the warp's part of shared memory, whose
-        // 64-byte rows hold their 16-byte pieces in the tensor copy's swizzled order.
-        uint8_t* stage = ring + TL::kStages * TL::kStageBytes + (warp - kFirstEpi) * 2 * kWarpOutBytes;
+        // 32 x 32 values at a time through the warp's part of shared memory, whose
+        // 128-byte rows hold their 16-byte pieces in the tensor copy's swizzled order.
+        uint8_t* stage = ring + TL::kStages * TL::kStageBytes + (warp - kFirstEpi) * kWarpOutBytes;
 #pragma unroll
         for (int h = 0; h < CW; h += kOutCols) {
-          uint8_t* half = stage + h / kOutCols % 2 * kWarpOutBytes;
-          tma_store_read();                                      // the copy before the last has read it (lane 0 issued it)
+          tma_store_read();                                      // the last copy has read it (lane 0 issued it)
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < kOutCols / 4; ++i) {
             const float2 x = acc[(h + 4 * i) / 2], y = acc[(h + 4 * i) / 2 + 1];
-            *reinterpret_cast<float4*>(half + lane * 64 + (i ^ (lane >> 1 & 3)) * 16) = make_float4(x.x, x.y, y.x, y.y);
+            *reinterpret_cast<float4*>(stage + lane * 128 + (i ^ (lane & 7)) * 16) = make_float4(x.x, x.y, y.x, y.y);
           }
           async_proxy_fence();
           __syncwarp();
-          if (lane == 0) {                                       // a group every time: the buffers are counted by groups
-            if (to_c0 + h < p.C) tma_store_3d(half, &map_out, to_c0 + h, to_row0 + quad * 32, to_e);
+          if (lane == 0) {
+            if (to_c0 + h < p.C) tma_store_3d(stage, &map_out, to_c0 + h, to_row0 + quad * 32, to_e);
             tma_store_commit();
           }
         }
@@ -624,13 +642,13 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, 
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// fp32 results [E, R, C] written in boxes of 32 rows by 16 columns.
+// fp32 results [E, R, C] written in boxes of 32 rows by 32 columns.
 bool make_out_map(CUtensorMap* map, void* base, uint64_t E, uint64_t R, uint64_t C) {
   const cuuint64_t dims[3] = {C, R, E}, strides[2] = {C * 4, R * C * 4};
   const cuuint32_t boxes[3] = {kOutCols, 32, 1}, ones[3] = {1, 1, 1};
   return encode_fn() != nullptr &&
          encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int BN, int RB, bool WGRAD, bool BF16>
@@ -646,7 +664,7 @@ cudaError_t launch(const MatmulParams& p, int sms, const char** error, cudaStrea
     return cudaErrorUnknown;
   }
   constexpr size_t smem = size_t(TL::kStages) * TL::kStageBytes + TL::kOutBytes + 1024;
-  static_assert(TL::kStages <= 8 && TL::kBufs <= 8 && TL::kBufs >= 2 && sizeof(Shared) + smem <= 232448, "shared memory of one CTA");
+  static_assert(TL::kStages <= 8 && TL::kBufs <= 8 && TL::kBufs >= 2 && sizeof(Shared<WGRAD>) + smem <= 232448, "shared memory of one CTA");
   static_assert(BN % kBox == 0 && TL::kStageBytes % 1024 == 0, "whole boxes, swizzle atoms aligned");
   const auto kernel = expert_matmul_kernel<BN, RB, WGRAD, BF16>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));

@@ -238,8 +238,8 @@ moe_status moe_expert_wgrad(const void* dyq, const float* dyscale, const void* x
     return fail(MOE_ERR_INVALID, "width = %lld must be a multiple of 128 in [128, 2^31)", (long long)width);
   if (!dyq || !dyscale || !xq || !xscale || !kept || !dw) return fail(MOE_ERR_INVALID, "an argument is NULL");
   if (!aligned(dyq, 16) || !aligned(xq, 16) || !aligned(dw, 16)) return fail(MOE_ERR_INVALID, "dyq, xq or dw is not 16-byte aligned");
-  if (!aligned(xscale, 16) || !aligned(dyscale, 4) || !aligned(kept, 4))
-    return fail(MOE_ERR_INVALID, "xscale (16 bytes), dyscale or kept (4 bytes) is misaligned");
+  if (!aligned(xscale, 16) || !aligned(dyscale, 16) || !aligned(kept, 4))
+    return fail(MOE_ERR_INVALID, "xscale, dyscale (16 bytes) or kept (4 bytes) is misaligned");
   if (int64_t(E) * ((N + 127) / 128) * ((K + 127) / 128) >= kInt32Limit) return fail(MOE_ERR_INVALID, "E x N x K is too large");
   int sms = 0;
   if ((s = moe::abi_sms(&sms)) != MOE_OK) return s;

@@ -66,7 +66,7 @@ BAD += [("moe_expert_matmul", p, v, w) for p, v, w in [
     (6, 1025, 1), (7, 40, 1), (8, None, 1), (8, FAKE + 2, 1), (9, FAKE + 2, 1), (10, 2, 2), (11, None, 1), (11, FAKE + 8, 1)]]
 BAD += [("moe_expert_wgrad", p, v, w) for p, v, w in [
     (0, None, 1), (1, None, 1), (2, None, 1), (3, None, 1), (2, FAKE + 8, 1), (4, 0, 1), (4, 1000, 1), (4, BIG, 1), (5, 24, 1), (6, 0, 1), (7, 0, 1), (8, None, 1),
-    (8, FAKE + 2, 1), (9, None, 1), (9, FAKE + 4, 1)]]
+    (8, FAKE + 2, 1), (9, None, 1), (9, FAKE + 4, 1), (1, FAKE + 4, 1), (3, FAKE + 8, 1)]]
 BAD += [("moe_expert_combine", p, v, w) for p, v, w in [
     (0, None, 1), (0, FAKE + 1, 1), (1, 4, 2), (2, 0, 1), (3, 0, 1), (3, 1 << 21, 1), (4, 0, 1), (5, 9, 1), (6, 0, 1), (7, None, 1), (8, None, 1), (9, None, 1),
     (10, FAKE + 2, 1), (11, None, 1)]]
