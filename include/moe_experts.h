@@ -145,7 +145,8 @@ MOE_API moe_status moe_quantize_weights(const void* w, moe_dtype dt, int32_t E, 
 /* out[r,n] = sum_k a[r,k] w[e,n,k] for the rows r = offsets[e] ..
  * offsets[e] + n_e - 1 of every expert e, n_e = kept[e] (or all rows up to
  * offsets[e+1] with kept NULL).  Other rows of out are left as they are.
- * offsets NULL: one expert (E == 1) with all M rows, a plain product.
+ * offsets NULL: one expert (E == 1) with all M rows, a plain product.  The
+ * experts' ranges are disjoint; a row that two share holds results of either.
  *   q [M,K] e4m3, scale [ceil(K/128), M] fp32: as moe_quantize_rows
  *   wq [E,N,K] e4m3, wscale [E, ceil(N/128), ceil(K/128)] fp32: as moe_quantize_weights
  *   out [M,N] bf16 or fp32 (out_dt)
@@ -198,7 +199,9 @@ MOE_API moe_status moe_expert_combine(const void* y, moe_dtype dt, int64_t M, in
 
 /* Its gradients: dy[row,:] = gate[t,j] * dout[t,:] for the rows of kept
  * assignments (others are left as they are), dgate[t,j] = sum_h dout[t,h] y[row,h]
- * (0 for a dropped assignment).  dy has y's type, dgate is fp32. */
+ * (0 for a dropped assignment).  dy has y's type, dgate is fp32.  The rows of
+ * kept assignments are distinct, as moe_dispatch makes them; one that two share
+ * holds values of either. */
 MOE_API moe_status moe_expert_combine_bwd(const void* dout, const void* y, moe_dtype dt, int64_t M, int32_t H, int64_t T,
                                           int32_t k, int32_t E, const int32_t* idx, const int32_t* slot,
                                           const int32_t* offsets, const float* gate, void* dy, float* dgate,

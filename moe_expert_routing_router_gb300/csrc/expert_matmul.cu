@@ -297,6 +297,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
   } else if (warp == 2) {                                        // tiles and blocks before each expert
     const int ct = (p.C + BN - 1) / BN;
     int tiles = 0, blocks = 0;
+    float sum = 0.f;                                             // of the tiles, where ranges that overlap pass an int
     for (int e0 = 0; e0 < p.E; e0 += kWarp) {
       int t = 0, b = 0;
       if (e0 + lane < p.E) {
@@ -308,6 +309,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
           sh.block[e0 + lane] = int(start);
           sh.count[e0 + lane] = int(n);
           t = int((n + kBM - 1) / kBM) * ct;
+          sum += float(t);
         }
       }
       int ti = t, bi = b;
@@ -326,6 +328,7 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       tiles += __shfl_sync(kFull, ti, kWarp - 1);
       blocks = int(min(int64_t(blocks) + __shfl_sync(kFull, bi, kWarp - 1), p.blocks));
     }
+    if (warp_sum_f(sum) > 2e9f) tiles = 0;                       // such offsets give nothing
     if (lane == 0) {
       if constexpr (!WGRAD) sh.first[p.E] = tiles;
       else sh.block[p.E] = blocks;

@@ -274,7 +274,8 @@ def moe_expert_device_status(stream: torch.cuda.Stream | None = None) -> int:
 
 def _assignments(idx, slot, offsets, gate, at: int) -> tuple[int, int, int]:
     T, k = _need_dims("idx", idx, 2, _I32, at)
-    if slot.numel() != T * k:
+    if not isinstance(slot, torch.Tensor) or slot.numel() != T * k:
+        _need_cuda("slot", slot)
         raise ValueError("slot must have T*k elements")
     _need("slot", slot, at, torch.int32, slot.shape)
     E = _need_dims("offsets", offsets, 1, _I32, at)[0] - 1

@@ -95,3 +95,10 @@ def test_positions_outside_the_arrays_stay_inside(mr):
         out = mr.moe_expert_combine(y.cuda(), i32(i), i32(s), i32(o), gate=gate.cuda())
         g = mr.moe_expert_combine_bwd(dout.cuda(), y.cuda(), i32(i), i32(s), i32(o), gate.cuda())
         assert not out.any() and not g["dgate"].any()
+
+
+def test_a_slot_that_is_no_tensor_is_refused(mr):
+    idx, slot, offsets, y, gate, dout = make(20, 2, 4, 64, 99, torch.float32)
+    for bad in (None, 5, i32(slot).cpu(), i32(slot)[:-1]):
+        with pytest.raises(ValueError, match="slot"):
+            mr.moe_expert_combine(y.cuda(), i32(idx), bad, i32(offsets), gate=gate.cuda())

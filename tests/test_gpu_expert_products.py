@@ -343,3 +343,75 @@ def test_an_expired_wait_is_reported(mr, native_lib):
     assert mr.moe_expert_device_status() == 2
     assert mr.moe_expert_device_status() == 0
     assert torch.equal(mr.moe_expert_matmul(q, scale, wq, wscale, out=out), want)
+
+
+def test_an_expired_wait_of_the_weight_gradient(mr, native_lib):
+    """As above for the kernel that copies scales beside the operands."""
+    counts = [900, 0, 300]
+    offsets, kept, _ = split(counts, counts)
+    gen = torch.Generator().manual_seed(8)
+    x = torch.randn(1200, 512, generator=gen).to(torch.bfloat16).cuda()
+    dy = torch.randn(1200, 256, generator=gen).to(torch.bfloat16).cuda()
+    a, b = mr.moe_quantize_cols(dy, offsets, kept), mr.moe_quantize_cols(x, offsets, kept)
+    args = (a["q"], a["scale"], b["q"], b["scale"], kept)
+    want = mr.moe_expert_wgrad(*args)
+    torch.cuda.synchronize()
+    native_lib.moe_set_wait_timeout_ns(1_000_000)
+    native_lib.moe_set_unreachable_barriers(1)
+    try:
+        mr.moe_expert_wgrad(*args)
+        torch.cuda.synchronize()
+    finally:
+        native_lib.moe_set_unreachable_barriers(0)
+        native_lib.moe_set_wait_timeout_ns(0)
+    assert mr.moe_expert_device_status() == 2
+    assert torch.equal(mr.moe_expert_wgrad(*args), want)
+    assert mr.moe_expert_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [2048, 1040])
+def test_cols_of_many_tiles(mr, K, dtype):
+    """More tiles than CTAs at once.  Columns in blocks of 128 rows are the rows, in blocks of 128, of
+    the transposed matrix that has each expert's rows filled up with zeros."""
+    counts, kept_counts, k = [9000, 0, 127, 4000, 1, 7000], [9000, 0, 100, 3900, 1, 0], 2
+    offsets, kept, _ = split(counts, kept_counts)
+    M = sum(counts)
+    gen = torch.Generator().manual_seed(K)
+    x = (torch.randn(M // k + 1, K, generator=gen) * 3).to(dtype).cuda()
+    perm = torch.randint(0, x.shape[0] * k, (M,), generator=gen).int().cuda()
+    out = {"q": torch.full((K, mr.moe_quantize_cols_width(M, len(counts))), 77, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn),
+           "scale": torch.full((mr.moe_quantize_cols_width(M, len(counts)) // 128, K), 7.0, device="cuda")}
+    mr.moe_quantize_cols(x, offsets, kept, perm=perm, k=k, out=out)
+    parts, at = [], 0
+    for c, n in zip(counts, kept_counts):
+        rows = x[(perm[at:at + n].long() // k)]
+        parts += [rows, rows.new_zeros(-n % 128, K)]
+        at += c
+    filled = torch.cat(parts)
+    W = filled.shape[0]
+    want = mr.moe_quantize_rows(filled.T.contiguous())
+    assert torch.equal(out["q"][:, :W].view(torch.uint8), want["q"].view(torch.uint8))
+    assert torch.equal(out["scale"][: W // 128], want["scale"])
+    assert (out["q"][:, W:].view(torch.uint8) == 77).all() and (out["scale"][W // 128:] == 7).all()
+
+
+def test_wgrad_of_many_tiles_is_exact_for_whole_numbers(mr):
+    """More tiles than CTAs and more blocks than the pipeline holds, scales that differ from block to
+    block: every sum is a multiple of 1/4 below 2^22, so fp32 holds it exactly in any order."""
+    counts = [1000, 130, 0, 1664]
+    offsets, kept, _ = split(counts, counts)
+    M, N, K = sum(counts), 2064, 1808
+    gen = torch.Generator().manual_seed(3)
+
+    def whole(C):
+        v = torch.randint(-4, 5, (M, C), generator=gen).double()
+        return (v * 2.0 ** torch.randint(-1, 2, ((M + 99) // 100, C), generator=gen).repeat_interleave(100, 0)[:M]).cuda()
+
+    dy, x = whole(N), whole(K)
+    a, b = (mr.moe_quantize_cols(t.to(torch.bfloat16), offsets, kept) for t in (dy, x))
+    got = mr.moe_expert_wgrad(a["q"], a["scale"], b["q"], b["scale"], kept)
+    at = 0
+    for e, n in enumerate(counts):
+        assert torch.equal(got[e].double(), dy[at:at + n].T @ x[at:at + n]), e
+        at += n
