@@ -284,7 +284,7 @@ __device__ __noinline__ int route_settle(const RouteParams& p, int64_t row, int 
 // them are computed, a pick a lane.
 // Instructions bound it.  For a row of 256 in 8 groups: 1145 with a warp a row whose
 // lanes sort their experts, 728 with a warp a row and this selection, 436 with 8 lanes
-// a row: 131,072 rows of bf16 in 90 us (0.8 TB/s), where the bytes alone would take 11.
+// a row: 131,072 rows of bf16 in 79 us (0.9 TB/s), where the bytes alone would take 11.
 // ---------------------------------------------------------------------------
 constexpr int kMaxRounds = 10;                                   // 8 picks and two more
 constexpr int kMaxPer = kWarp / kPickLanes;                      // rows a warp finishes at once
@@ -303,13 +303,19 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
+// CTAs of an SM, which hide the loads: as many as the registers of a lane's experts leave
+// room for.  (The next pass's loads issued beside this one's work cost more in registers
+// than they hid: 131,072 x 256 bf16 89 us, with 2 CTAs; 79 with 3 and no such loads, 82
+// with 4; fp32 93 with 2, slower with 3; 131,072 x 128 fp32 94 with 3, 87 with 4.)
+template <int NV, int SIZE>
+constexpr int kRouteCtas = NV <= 16 ? 4 : NV > 32 ? 1 : SIZE == 2 ? 3 : 2;
+
 template <class Elem, int LPR, int NV, int VB, bool FULL, int MODE>
-__global__ void __launch_bounds__(kRouteThreads, NV <= 8 ? 4 : NV <= 16 ? 3 : NV <= 32 ? 2 : 1)
+__global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NV, sizeof(typename Elem::Raw)>)
 route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
   using Raw = typename Elem::Raw;
   constexpr int R = kWarp / LPR;                                 // rows of a pass
   constexpr int kPer = VB / int(sizeof(Raw));                    // elements per load
-  constexpr bool kAhead = NV * int(sizeof(Raw)) <= 64;           // whether the next pass fits beside this one
   constexpr int kMaxima = (NV + 7) / 8;
   constexpr bool kSpread = NV <= 32;                             // values go through shared memory to be picked by place
   using Mask = typename std::conditional<NV <= 32, uint32_t, unsigned long long>::type;
@@ -360,13 +366,12 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
 
   const int64_t stride = int64_t(gridDim.x) * kRouteWarps * per;
   const int64_t first0 = (int64_t(blockIdx.x) * kRouteWarps + warp) * per;
-  if (kAhead && first0 < p.T) fetch(first0 + rr);
   for (int64_t first = first0; first < p.T; first += stride) {
     float my_max = 0.f, my_sum = 1.f, my_tol = 0.f;              // of row first + lane / 8
     unsigned close_rows = 0u, unsure_rows = 0u;
     const int rows = int(min(int64_t(per), p.T - first));
     for (int r0 = 0; r0 < rows; r0 += R) {
-      if constexpr (!kAhead) fetch(first + r0 + rr);
+      fetch(first + r0 + rr);
 
       // Choice values in fp32.  Their error is within tol / 2.
       float c[NV], tol = 0.f;
@@ -440,10 +445,6 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
       if constexpr (!FULL) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) c[i] = i < n ? c[i] : none();
-      }
-      if constexpr (kAhead) {
-        const int64_t then = r0 + R < rows ? first + r0 + R : first + stride;
-        fetch(then + rr);
       }
 
       float best[kMaxima];                                       // the maxima of eight
@@ -600,8 +601,6 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
         if (lane < p.k) s_ranked[warp][r][lane].y = __int_as_float(e);
         __syncwarp();
       }
-      // Read again, so that nothing of a row's size is kept across the calls.
-      if (kAhead) fetch(first + stride + rr);
     }
 
     const int64_t row = first + lane / kPickLanes;
