@@ -89,30 +89,53 @@ __device__ __forceinline__ double from_ordered(long long k) {
   return __longlong_as_double(k ^ (k >> 63 & 0x7fffffffffffffffll));
 }
 
+// A score in double: of one logit, given a softmax row's largest and its sum.
+struct DoubleScore {
+  int softmax;
+  float m;
+  double sum;
+  __device__ __forceinline__ double operator()(float z) const {
+    return softmax ? exp(double(z) - double(m)) / sum : 1.0 / (1.0 + exp(-double(z)));
+  }
+};
+template <class Elem>
+__device__ __noinline__ DoubleScore route_double_score(const RouteParams& p, int64_t row, int lane) {
+  DoubleScore s = {p.softmax, neg_inf(), 0.0};
+  if (!p.softmax) return s;
+  constexpr int kAtOnce = 4;                                     // loads in flight
+  float z[kAtOnce];
+  const auto load = [&](int e0) {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      z[i] = e0 + i * kWarp + lane < p.E ? load_logit<Elem>(p.logits, row * p.E + e0 + i * kWarp + lane) : neg_inf();
+  };
+  for (int e0 = 0; e0 < p.E; e0 += kAtOnce * kWarp) {
+    load(e0);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) s.m = fmaxf(s.m, z[i]);
+  }
+  s.m = warp_max_f(s.m);
+  for (int e0 = 0; e0 < p.E; e0 += kAtOnce * kWarp) {
+    load(e0);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (z[i] > neg_inf()) s.sum += exp(double(z[i]) - double(s.m));
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s.sum += __shfl_xor_sync(kFull, s.sum, off);
+  return s;
+}
+
 // ---------------------------------------------------------------------------
 // The row ranked in double: the definition, by all lanes of the warp.  Lane j
 // gets pick j.  `bias` and the row are read again (they are in the caches).
 // ---------------------------------------------------------------------------
 template <class Elem>
-__device__ __noinline__ int route_row_double(const RouteParams& p, int64_t row, int lane) {
+__device__ __noinline__ int route_row_double(const RouteParams& p, int64_t row, int lane, DoubleScore score_of) {
   long long c[64];                                               // choice values of the lane's experts
   const int g = lane / p.L, base = g * p.gs + (lane % p.L) * p.chunk;
   const int n = g < p.G ? max(0, min(p.chunk, p.gs - (lane % p.L) * p.chunk)) : 0;
   const long long masked = ordered(double(neg_inf()));
-  float m = neg_inf();
-  double sum = 1.0;
-  if (p.softmax) {
-    for (int i = 0; i < n; ++i) m = fmaxf(m, load_logit<Elem>(p.logits, row * p.E + base + i));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-    sum = 0.0;
-    for (int i = 0; i < n; ++i) {
-      const float z = load_logit<Elem>(p.logits, row * p.E + base + i);
-      if (z > neg_inf()) sum += exp(double(z) - double(m));
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-  }
   long long a = masked, b = masked;                              // the two largest of the lane, then of the group
   unsigned long long gone = 0;
   for (int i = 0; i < n; ++i) {
@@ -121,7 +144,7 @@ __device__ __noinline__ int route_row_double(const RouteParams& p, int64_t row, 
     if (z > neg_inf()) {
       double s = 0.0;
       if (p.bias != nullptr || p.top2) {
-        s = p.softmax ? exp(double(z) - double(m)) / sum : 1.0 / (1.0 + exp(-double(z)));
+        s = score_of(z);
         if (p.bias != nullptr) s += double(p.bias[base + i]);
       }
       v = ordered(s);
@@ -171,17 +194,19 @@ __device__ __noinline__ int route_row_double(const RouteParams& p, int64_t row, 
 
 // ---------------------------------------------------------------------------
 // Whether the row's best groups in double are those that fp32 has taken
-// (`kept`: bit g << tshift for group g), for sigmoid scores.  Only the experts
-// that can be among a group's two largest are evaluated, one a lane; false where
-// there are more than 32 of them.  `list`: 32 ints of shared memory.
+// (`kept`: bit g << tshift for group g).  Only the experts that can be among a
+// group's two largest are evaluated, one a lane; false where there are more than
+// 32 of them.  `list`: 32 ints of shared memory.
 // ---------------------------------------------------------------------------
 template <class Elem>
-__device__ __noinline__ bool route_groups_hold(const RouteParams& p, int64_t row, int lane, float tol, unsigned kept, int* list) {
+__device__ __noinline__ bool route_groups_hold(const RouteParams& p, int64_t row, int lane, float tol, unsigned kept, int* list, DoubleScore score_of) {
+  const float inv = float(1.0 / score_of.sum);                   // softmax
   const int g = lane / p.L, base = g * p.gs + (lane % p.L) * p.chunk;
   const int n = g < p.G ? max(0, min(p.chunk, p.gs - (lane % p.L) * p.chunk)) : 0;
   const auto value = [&](int i) {
     const float z = load_logit<Elem>(p.logits, row * p.E + base + i);
-    return z > neg_inf() ? rcp_approx(1.f + ex2_approx(z * -kLog2e)) + (p.bias != nullptr ? p.bias[base + i] : 0.f) : neg_inf();
+    const float s = p.softmax ? ex2_approx((z - score_of.m) * kLog2e) * inv : rcp_approx(1.f + ex2_approx(z * -kLog2e));
+    return z > neg_inf() ? s + (p.bias != nullptr ? p.bias[base + i] : 0.f) : neg_inf();
   };
   float a = neg_inf(), b = neg_inf();
   for (int i = 0; i < n; ++i) {
@@ -210,7 +235,7 @@ __device__ __noinline__ bool route_groups_hold(const RouteParams& p, int64_t row
   const int e = lane < total ? list[lane] : 0, of = lane < total ? e / p.gs : -1;
   long long v = masked;
   if (lane < total)
-    v = ordered(1.0 / (1.0 + exp(-double(load_logit<Elem>(p.logits, row * p.E + e)))) + (p.bias != nullptr ? double(p.bias[e]) : 0.0));
+    v = ordered(score_of(load_logit<Elem>(p.logits, row * p.E + e)) + (p.bias != nullptr ? double(p.bias[e]) : 0.0));
   long long a2 = masked, b2 = masked;                            // of group `lane`
   for (int o = 0; o < total; ++o) {
     const long long w = __shfl_sync(kFull, v, o);
@@ -231,12 +256,15 @@ __device__ __noinline__ bool route_groups_hold(const RouteParams& p, int64_t row
 // ---------------------------------------------------------------------------
 // The picks of a row where values that decide them are next to one another
 // (`close`), or where its groups' scores are (`unsure`).  Lane j holds the j-th
-// largest choice value and its expert, the k picks and two more.
+// largest choice value and its expert, the k picks and two more.  (A whole row in
+// double takes some 40 us, its candidates a few: 2048 x 384 softmax with a bias 57 us
+// with the whole rows, 22 with the candidates.)
 // ---------------------------------------------------------------------------
 template <class Elem>
 __device__ __noinline__ int route_settle(const RouteParams& p, int64_t row, int lane, float c, int ce, int rounds, float tol,
                                          bool close, bool unsure, unsigned kept, int* list) {
-  if (unsure && (p.softmax || !route_groups_hold<Elem>(p, row, lane, tol, kept, list))) return route_row_double<Elem>(p, row, lane);
+  const DoubleScore score_of = route_double_score<Elem>(p, row, lane);
+  if (unsure && !route_groups_hold<Elem>(p, row, lane, tol, kept, list, score_of)) return route_row_double<Elem>(p, row, lane, score_of);
   if (!close) return ce;
   const bool there = lane < rounds && c == c;
   const float zc = there ? load_logit<Elem>(p.logits, row * p.E + ce) : neg_inf();
@@ -248,11 +276,11 @@ __device__ __noinline__ int route_settle(const RouteParams& p, int64_t row, int 
   const float last = __shfl_sync(kFull, c, p.k - 1);
   const bool beyond = lane == p.k + 1 && there && last - c <= tol + 2.4e-7f * fabsf(last);
   const bool any_open = __any_sync(kFull, open), any_beyond = __any_sync(kFull, beyond);
-  if (any_open && (any_beyond || p.softmax)) return route_row_double<Elem>(p, row, lane);
+  if (any_open && any_beyond) return route_row_double<Elem>(p, row, lane, score_of);
   if (!any_open) return ce;
-  // The k + 1 largest are known as a set: one double-precision sigmoid a lane orders them.
+  // The k + 1 largest are known as a set: one double-precision score a lane orders them.
   const bool in = there && lane <= p.k;
-  const long long d = ordered(in && zc > neg_inf() ? 1.0 / (1.0 + exp(-double(zc))) + double(bc) : double(neg_inf()));
+  const long long d = ordered(in && zc > neg_inf() ? score_of(zc) + double(bc) : double(neg_inf()));
   int rank = 0;
   for (int o = 0; o <= p.k; ++o) {
     const long long od = __shfl_sync(kFull, d, o);

@@ -157,7 +157,8 @@ def test_choice_values_that_fp32_cannot_tell_apart(mr, score, grouped):
 
 @pytest.mark.parametrize("shape", [(512, 8, 4), (1024, 8, 4), (96, 32, 5), (510, 17, 9)], ids=lambda s: "x".join(map(str, s)))
 @pytest.mark.parametrize("biased", [False, True])
-def test_groups_that_fp32_cannot_tell_apart(mr, shape, biased):
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_groups_that_fp32_cannot_tell_apart(mr, shape, score, biased):
     """Groups whose two largest are another group's, or next to them, among many experts;
     in some rows groups of one expert or of none, and groups of experts all alike."""
     E, G, keep = shape
@@ -176,8 +177,8 @@ def test_groups_that_fp32_cannot_tell_apart(mr, shape, biased):
     z[640:660] = z[640:660, :, :1]
     z = torch.from_numpy(z.reshape(T, E))
     for group_score in ("top2", "max"):
-        check(mr, z, 4, "sigmoid", bias, G, keep, group_score)
-        check(mr, z.to(torch.bfloat16), 4, "sigmoid", bias, G, keep, group_score)
+        check(mr, z, 4, score, bias, G, keep, group_score)
+        check(mr, z.to(torch.bfloat16), 4, score, bias, G, keep, group_score)
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
