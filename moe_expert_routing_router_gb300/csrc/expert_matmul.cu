@@ -696,12 +696,16 @@ cudaError_t expert_matmul_errors(int* bits, cudaStream_t stream) {
 
 cudaError_t launch_expert_matmul(const MatmulParams& p, int sms, const char** error, cudaStream_t stream) {
   if (p.wgrad) return launch<256, 1, true, false>(p, sms, error, stream);
-  // Tiles of 128 columns, two blocks a stage, up to 200 rows an expert; beyond, 256
-  // columns.  The narrow ones spread few rows' weights over more SMs (rows x experts,
-  // 4096 -> 2048: 87 x 64 109 us against 138, 175 x 64 150 against 158, 300 x 16 60
-  // against 64); the wide ones halve the reads of the rows (600 x 16 96 us against
-  // 98, 1024 x 64 490 against 559).
-  const bool narrow = p.M <= int64_t(p.E) * 200;
+  // Tiles of 128 columns, two blocks a stage, up to 200 rows an expert: they spread few rows'
+  // weights over more SMs (rows x experts, 4096 -> 2048: 87 x 64 109 us against 138, 175 x 64
+  // 150 against 158).  Beyond, 256 columns, which halve the reads of the rows (1024 x 64 490
+  // against 559), unless the narrow tiles leave the SMs less idle behind the last one: a
+  // narrow one takes some 3/5 of a wide one's time, and an expert's last row tile counts
+  // half (500 x 4, 1024 -> 1024: 8.5 us against 11.2; 300 x 1, 4096 -> 4096: 14 against 21;
+  // but 750 x 8, 1424 -> 1040: 28 against 24, and 600 x 16, 4096 -> 2048: 96 against 93).
+  const int64_t row_tiles = (p.M + (p.E > 1 ? 64 * int64_t(p.E) : 0) + kBM - 1) / kBM;
+  const auto rounds = [&](int columns) { return (row_tiles * ((p.C + columns - 1) / columns) + sms - 1) / sms; };
+  const bool narrow = p.M <= int64_t(p.E) * 200 || rounds(128) * 3 < rounds(256) * 5;
   if (p.out_bf16)
     return narrow ? launch<128, 2, false, true>(p, sms, error, stream) : launch<256, 1, false, true>(p, sms, error, stream);
   return narrow ? launch<128, 2, false, false>(p, sms, error, stream) : launch<256, 1, false, false>(p, sms, error, stream);
