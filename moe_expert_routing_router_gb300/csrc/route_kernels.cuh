@@ -47,6 +47,29 @@ __device__ __forceinline__ float warp_max_f(float x) {
   return x;
 }
 
+// The CTAs of a cluster: how many, which one this is, a barrier of all, and the word in
+// CTA r's shared memory at the place of this one's `p`.
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t n;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t n;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int cluster_load(const int* p, uint32_t r) {
+  uint32_t at;
+  int v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(r));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
 // The sigmoid, relative to its own size (no cancellation on either side).
 __device__ __forceinline__ float sigmoid_exact(float z) {
   const float t = expf(-fabsf(z));
@@ -652,13 +675,17 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
     }
   }
   __syncthreads();
-  if (gridDim.x > 1) {
+  const uint32_t ctas = cluster_ctas();
+  if (gridDim.x > ctas) {
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads)
       if (s_hist[e] != 0) atomicAdd(&p.counts[e], s_hist[e]);   // integers: any order gives the same sum
     return;
   }
-  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
-    const int cnt = s_hist[e];
+  // One cluster has all rows: its CTAs finish the experts between them.
+  if (ctas > 1) cluster_barrier();
+  for (int e = cluster_rank() * kRouteThreads + threadIdx.x; e < p.E; e += ctas * kRouteThreads) {
+    int cnt = 0;
+    for (uint32_t r = 0; r < ctas; ++r) cnt += cluster_load(&s_hist[e], r);
     p.counts[e] = cnt;
     if (p.bias_out != nullptr) {
       const int64_t over = p.T * p.k - int64_t(cnt) * p.E;
@@ -666,6 +693,7 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
       p.bias_out[e] = over > 0 ? b + p.bias_gamma : over < 0 ? b - p.bias_gamma : b;
     }
   }
+  if (ctas > 1) cluster_barrier();                               // its counts have been read
 }
 
 // bias + gamma * sign(T*k/E - count), after all counts are in.
@@ -681,18 +709,33 @@ __global__ void __launch_bounds__(256) route_bias_kernel(const RouteParams p) {
 // an SM on (1024 experts, a row a pass: 2048 rows 24.7 us with one row a warp and 32.8 with
 // four, 8192 rows 39.7 and 38.8, 32,768 rows 112 and 99).
 int rows_per_warp(int64_t T, int sms) { return T >= int64_t(sms) * 64 ? 4 : 1; }
-// Passes of one CTA alone, which writes counts and bias without a second and third
-// launch (256 experts, 32 rows a pass, with a bias: 33 rows 14.0 us against 15.2 with
-// more CTAs, 64 rows 10.6 against 11.2, 96 rows 14.4 against 12.3).
-constexpr int kOneCtaPasses = 2;
+// CTAs of a cluster.  One CTA alone, and one cluster, write counts and bias without a second
+// and third launch; each takes what it has in one pass (256 experts, 32 rows a CTA, with a
+// bias; CTA, cluster, more CTAs: 32 rows 6.6, 7.7 and 11.5 us; 64 rows 10.7, 7.6 and 11.2;
+// 256 rows -, 8.9 and 13.0; 512 rows, two passes, 12.8 and 12.9; 768 rows 16.3 and 12.3).
+constexpr int kCluster = 8;
 
 template <class Elem, int LPR, int NV, int VB, bool FULL, int MODE>
 cudaError_t fwd_launch(const RouteParams& p, int sms, cudaStream_t stream) {
   const size_t counts = size_t(p.E) * sizeof(int), smem = counts + size_t(LPR) * ((NV + 3) / 4 * 4) * sizeof(float);
   constexpr int R = kWarp / LPR;
-  if (p.T <= kOneCtaPasses * kRouteWarps * R) {
+  if (p.T <= kRouteWarps * R) {
     route_fwd_kernel<Elem, LPR, NV, VB, FULL, MODE><<<1, kRouteThreads, smem, stream>>>(p, R);
     return cudaGetLastError();
+  }
+  if (p.T <= kCluster * kRouteWarps * R) {
+    cudaLaunchAttribute cluster = {};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = kCluster;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(kRouteThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, route_fwd_kernel<Elem, LPR, NV, VB, FULL, MODE>, p, R);
   }
   cudaError_t e = cudaMemsetAsync(p.counts, 0, counts, stream);
   if (e != cudaSuccess) return e;

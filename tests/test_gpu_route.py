@@ -310,3 +310,22 @@ def test_a_large_batch_and_64_bit_offsets(mr):
     dg[-300:] = torch.randn(300, k, device="cuda")
     d = mr.moe_route_bwd(z, got["idx"], dg)
     assert torch.equal(d[-300:], mr.moe_route_bwd(part.cuda(), want["idx"], dg[-300:].contiguous()))
+
+
+@pytest.mark.parametrize("E,G", [(256, 8), (64, 1), (1024, 32), (40, 5)])
+def test_counts_and_bias_of_every_way_to_launch(mr, E, G):
+    """One CTA, one cluster, many CTAs, and both sides of where they change over."""
+    for T in (1, 8, 16, 17, 32, 33, 64, 65, 128, 129, 256, 257, 512, 513, 700):
+        z = logits_of(T, E, torch.bfloat16, seed=T)
+        check(mr, z, 4, "sigmoid", bias_of(E, 5), G, max(1, G // 2))
+
+
+def test_bias_in_place_of_one_cluster(mr):
+    """The bias that the rows read is overwritten only behind the last row."""
+    T, E = 300, 256
+    z, bias = logits_of(T, E, torch.float32, 4), bias_of(E, 6)
+    want = mr.moe_route_fwd(z.cuda(), 8, bias=torch.from_numpy(bias).cuda(), n_groups=8, topk_groups=4, bias_gamma=0.5, bias_out=True)
+    for _ in range(20):
+        b = torch.from_numpy(bias).cuda()
+        got = mr.moe_route_fwd(z.cuda(), 8, bias=b, n_groups=8, topk_groups=4, bias_gamma=0.5, bias_out=b)
+        assert torch.equal(b, want["bias_out"]) and torch.equal(got["idx"], want["idx"]) and torch.equal(got["counts"], want["counts"])
