@@ -111,6 +111,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr) : "memory");
 }
+// 16 rows by 32 columns, spread like a matrix product's fragments: for the n-th 8 columns,
+// lane l gets columns 2 (l % 4) and the next one of row l / 4 in r[4 n], r[4 n + 1], and of
+// row l / 4 + 8 in r[4 n + 2], r[4 n + 3].
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+      "}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr) : "memory");
+}
 // Waits for the thread's loads.  The values pass through the statement, so that
 // no use of them can be moved before it.
 __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
@@ -158,8 +170,8 @@ struct Tile {
 };
 
 // Blocks whose scales the weight gradient holds in shared memory: its producer copies them
-// beside the operands (32,836 rows of 32 experts, 2048 x 2048: 228 us, against 282 with loads
-// by the epilogue's lanes and narrower copies of the results).
+// beside the operands (32,836 rows of 32 experts, 2048 x 2048: 282 -> 228 us, with wider
+// copies of the results, against loads by the epilogue's lanes).
 constexpr int kScaleSlots = 6;
 
 template <bool WGRAD>
@@ -501,15 +513,40 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
         ok = __all_sync(kFull, mm_wait(sh, p, &sh.done[s], phase, WGRAD ? &sh.scales[q] : nullptr, qphase));   // one answer for the warp
         if (!ok) break;
         tc_fence_after();
-        const float* block_scales = sh.scale[WGRAD ? q : 0];
-        if constexpr (WGRAD) scale[0] = block_scales[row];       // a row behind the last one is not stored
         // The buffer is free as soon as its last columns have been read.
         const auto release = [&]() {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.tempty[t]);
         };
-        if (busy) {
+        if (WGRAD && busy) {
+          // Fragments: a lane needs 16 scales of columns and 4 of rows, instead of the 64 of
+          // columns that a row a lane takes (219 us against 225 at 32,836 rows).
+          const float* f_row = &sh.scale[WGRAD ? q : 0][quad * 32 + lane / 4];
+          const float* f_col = &sh.scale[WGRAD ? q : 0][kBM + cg * CW + lane % 4 * 2];
+          const uint32_t addr = tmem + t * BN + cg * CW + (uint32_t(quad * 32) << 16);
+          const float row_scale[4] = {f_row[0], f_row[8], f_row[16], f_row[24]};   // one behind the last row is not stored
+#pragma unroll
+          for (int c = 0; c < CW; c += 32) {
+            float2 f[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) f[n] = *reinterpret_cast<const float2*>(&f_col[c + 8 * n]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {                        // rows 16 h and following
+              uint32_t u[16];
+              tmem_ld_16x32(addr + c + (uint32_t(16 * h) << 16), u);
+              tmem_ld_wait(u);
+              if (c + 32 == CW && h == 1) release();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {                      // acc: (columns / 32, rows / 16, columns / 8, rows / 8)
+                const float r = row_scale[2 * h + i % 2];
+                const float2 x = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+                float2& a = acc[c / 2 + 8 * h + i];
+                a = fma2(mul2(x, make_float2(r, r)), f[i / 2], a);
+              }
+            }
+          }
+        } else if (busy) {
 #pragma unroll
           for (int j = 0; j < RB; ++j) {
             const bool last = j + 1 == RB || b + j + 1 >= w.blocks;
@@ -525,14 +562,8 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
               for (int i = 0; i < 16; i += 4) {
                 const float2 x = make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1]));
                 const float2 y = make_float2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3]));
-                if constexpr (WGRAD) {
-                  const float4 f = *reinterpret_cast<const float4*>(&block_scales[kBM + cg * CW + c + i]);
-                  acc[(c + i) / 2] = fma2(mul2(x, s2), make_float2(f.x, f.y), acc[(c + i) / 2]);
-                  acc[(c + i) / 2 + 1] = fma2(mul2(y, s2), make_float2(f.z, f.w), acc[(c + i) / 2 + 1]);
-                } else {
-                  acc[(c + i) / 2] = fma2(x, s2, acc[(c + i) / 2]);
-                  acc[(c + i) / 2 + 1] = fma2(y, s2, acc[(c + i) / 2 + 1]);
-                }
+                acc[(c + i) / 2] = fma2(x, s2, acc[(c + i) / 2]);
+                acc[(c + i) / 2 + 1] = fma2(y, s2, acc[(c + i) / 2 + 1]);
               }
             }
             if (last) break;
@@ -559,20 +590,22 @@ expert_matmul_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap m
       if constexpr (WGRAD) {
         // 32 x 32 values at a time through the warp's part of shared memory, whose
         // 128-byte rows hold their 16-byte pieces in the tensor copy's swizzled order.
+        // (Two pieces of 16 rows, so that one is written while the other leaves: 226 us
+        // against 219.)
         uint8_t* stage = ring + TL::kStages * TL::kStageBytes + (warp - kFirstEpi) * kWarpOutBytes;
 #pragma unroll
-        for (int h = 0; h < CW; h += kOutCols) {
+        for (int c = 0; c < CW; c += kOutCols) {
           tma_store_read();                                      // the last copy has read it (lane 0 issued it)
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < kOutCols / 4; ++i) {
-            const float2 x = acc[(h + 4 * i) / 2], y = acc[(h + 4 * i) / 2 + 1];
-            *reinterpret_cast<float4*>(stage + lane * 128 + (i ^ (lane & 7)) * 16) = make_float4(x.x, x.y, y.x, y.y);
+          for (int i = 0; i < kOutCols / 2; ++i) {               // as acc: rows 16 (i / 8) + 8 (i % 2) + lane / 4
+            const int to_row = i / 8 * 16 + i % 2 * 8 + lane / 4, piece = i / 2 % 4 * 2 + lane % 4 / 2;
+            *reinterpret_cast<float2*>(stage + to_row * 128 + (piece ^ lane / 4) * 16 + lane % 2 * 8) = acc[c / 2 + i];
           }
           async_proxy_fence();
           __syncwarp();
           if (lane == 0) {
-            if (to_c0 + h < p.C) tma_store_3d(stage, &map_out, to_c0 + h, to_row0 + quad * 32, to_e);
+            if (to_c0 + c < p.C) tma_store_3d(stage, &map_out, to_c0 + c, to_row0 + quad * 32, to_e);
             tma_store_commit();
           }
         }
