@@ -215,6 +215,34 @@ __device__ __noinline__ int route_row_double(const RouteParams& p, int64_t row, 
   return mine;
 }
 
+// The choice value of expert e in fp32 (its error within tol / 2), -infinity if masked.
+template <class Elem>
+__device__ __forceinline__ float route_fast_choice(const RouteParams& p, int64_t row, int e, const DoubleScore& score_of, float inv) {
+  const float z = load_logit<Elem>(p.logits, row * p.E + e);
+  const float s = score_of.softmax ? ex2_approx((z - score_of.m) * kLog2e) * inv : rcp_approx(1.f + ex2_approx(z * -kLog2e));
+  return z > neg_inf() ? s + (p.bias != nullptr ? p.bias[e] : 0.f) : neg_inf();
+}
+
+// The experts of the lanes' groups whose choice values reach the lane's bound: how many,
+// and in `list` (32 ints of shared memory) up to 32 of them.
+template <class Elem>
+__device__ __forceinline__ int route_candidates(const RouteParams& p, int64_t row, int lane, float reach, bool taken, int* list,
+                                                const DoubleScore& score_of, float inv) {
+  const int g = lane / p.L, base = g * p.gs + (lane % p.L) * p.chunk;
+  const int n = g < p.G && taken ? max(0, min(p.chunk, p.gs - (lane % p.L) * p.chunk)) : 0;
+  int total = 0;
+  for (int i = 0; i < p.chunk; ++i) {
+    const float v = i < n ? route_fast_choice<Elem>(p, row, base + i, score_of, inv) : neg_inf();
+    const bool in = v > neg_inf() && !(v < reach);               // a bound of -infinity: every expert that is not masked
+    const unsigned m = __ballot_sync(kFull, in);
+    const int at = total + __popc(m & ((1u << lane) - 1u));
+    if (in && at < kWarp) list[at] = base + i;
+    total += __popc(m);
+  }
+  __syncwarp();
+  return total;
+}
+
 // ---------------------------------------------------------------------------
 // Whether the row's best groups in double are those that fp32 has taken
 // (`kept`: bit g << tshift for group g).  Only the experts that can be among a
@@ -226,14 +254,9 @@ __device__ __noinline__ bool route_groups_hold(const RouteParams& p, int64_t row
   const float inv = float(1.0 / score_of.sum);                   // softmax
   const int g = lane / p.L, base = g * p.gs + (lane % p.L) * p.chunk;
   const int n = g < p.G ? max(0, min(p.chunk, p.gs - (lane % p.L) * p.chunk)) : 0;
-  const auto value = [&](int i) {
-    const float z = load_logit<Elem>(p.logits, row * p.E + base + i);
-    const float s = p.softmax ? ex2_approx((z - score_of.m) * kLog2e) * inv : rcp_approx(1.f + ex2_approx(z * -kLog2e));
-    return z > neg_inf() ? s + (p.bias != nullptr ? p.bias[base + i] : 0.f) : neg_inf();
-  };
   float a = neg_inf(), b = neg_inf();
   for (int i = 0; i < n; ++i) {
-    const float v = value(i);
+    const float v = route_fast_choice<Elem>(p, row, base + i, score_of, inv);
     b = fmaxf(b, fminf(a, v));
     a = fmaxf(a, v);
   }
@@ -243,16 +266,7 @@ __device__ __noinline__ bool route_groups_hold(const RouteParams& p, int64_t row
     a = fmaxf(a, a2);
   }
   const float last = p.top2 ? b : a, reach = last - (tol + 2.4e-7f * fabsf(last));
-  int total = 0;
-  for (int i = 0; i < p.chunk; ++i) {
-    const float v = i < n ? value(i) : neg_inf();
-    const bool in = v > neg_inf() && !(v < reach);               // a group without a second: every expert that is not masked
-    const unsigned m = __ballot_sync(kFull, in);
-    const int at = total + __popc(m & ((1u << lane) - 1u));
-    if (in && at < kWarp) list[at] = base + i;
-    total += __popc(m);
-  }
-  __syncwarp();
+  const int total = route_candidates<Elem>(p, row, lane, reach, true, list, score_of, inv);
   if (total > kWarp) return false;
   const long long masked = ordered(double(neg_inf()));
   const int e = lane < total ? list[lane] : 0, of = lane < total ? e / p.gs : -1;
@@ -293,13 +307,33 @@ __device__ __noinline__ int route_settle(const RouteParams& p, int64_t row, int 
   const float zc = there ? load_logit<Elem>(p.logits, row * p.E + ce) : neg_inf();
   const float bc = there && p.bias != nullptr ? p.bias[ce] : 0.f;
   const float c_up = __shfl_up_sync(kFull, c, 1), z_up = __shfl_up_sync(kFull, zc, 1), b_up = __shfl_up_sync(kFull, bc, 1);
-  // sure all the same where the inputs are equal
+  // sure all the same where the inputs are equal; but behind the last one that is held there
+  // can be more
   const bool open = lane >= 1 && lane <= p.k && there && c_up - c <= tol + 2.4e-7f * fabsf(c_up) &&
                     !(zc == z_up && bc == b_up);
   const float last = __shfl_sync(kFull, c, p.k - 1);
   const bool beyond = lane == p.k + 1 && there && last - c <= tol + 2.4e-7f * fabsf(last);
   const bool any_open = __any_sync(kFull, open), any_beyond = __any_sync(kFull, beyond);
-  if (any_open && any_beyond) return route_row_double<Elem>(p, row, lane, score_of);
+  if (any_beyond) {
+    const bool taken = p.keep >= p.G || (kept >> ((lane / p.L << p.tshift) & 31) & 1u) != 0u;
+    const int total = route_candidates<Elem>(p, row, lane, last - (tol + 2.4e-7f * fabsf(last)), taken, list, score_of,
+                                             float(1.0 / score_of.sum));
+    if (total > kWarp) return route_row_double<Elem>(p, row, lane, score_of);
+    const int e = lane < total ? list[lane] : 0x7fffffff;
+    const long long d = lane < total ? ordered(score_of(load_logit<Elem>(p.logits, row * p.E + e)) + double(p.bias[e])) : 0;
+    int rank = 0;
+    for (int o = 0; o < total; ++o) {
+      const long long od = __shfl_sync(kFull, d, o);
+      const int oe = __shfl_sync(kFull, e, o);
+      rank += od > d || (od == d && oe < e);
+    }
+    int to = ce;
+    for (int o = 0; o < total; ++o) {
+      const int orank = __shfl_sync(kFull, rank, o), oe = __shfl_sync(kFull, e, o);
+      if (orank == lane) to = oe;
+    }
+    return to;
+  }
   if (!any_open) return ce;
   // The k + 1 largest are known as a set: one double-precision score a lane orders them.
   const bool in = there && lane <= p.k;

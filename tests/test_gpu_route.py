@@ -329,3 +329,21 @@ def test_bias_in_place_of_one_cluster(mr):
         b = torch.from_numpy(bias).cuda()
         got = mr.moe_route_fwd(z.cuda(), 8, bias=b, n_groups=8, topk_groups=4, bias_gamma=0.5, bias_out=b)
         assert torch.equal(b, want["bias_out"]) and torch.equal(got["idx"], want["idx"]) and torch.equal(got["counts"], want["counts"])
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("copies", [1, 2, 3, 7, 40])
+def test_a_larger_value_behind_equal_ones(mr, copies, grouped):
+    """Experts with the same logit and bias, and behind them one whose choice value is larger only in
+    double precision."""
+    T, E = 70, 96
+    z = np.full((T, E), -2.0, np.float32)
+    bias = np.full(E, 0.1, np.float32)
+    bias[7] = 0.2
+    z[:, 7] = 3.5625
+    at = np.r_[10:10 + copies]
+    z[:, at] = 17.125
+    z[::2, 60], z[1::2, 61] = 19.125, 18.0
+    for k in (1, 2, 3, 8):
+        check(mr, torch.from_numpy(z), k, "sigmoid", bias, 4 if grouped else 1, 3 if grouped else 1, "max")
+        check(mr, torch.from_numpy(z).to(torch.bfloat16), k, "sigmoid", bias, 4 if grouped else 1, 3 if grouped else 1, "top2")
