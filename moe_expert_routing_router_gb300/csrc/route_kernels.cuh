@@ -508,7 +508,7 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
       }
 
       bool open = g < p.G;                                       // whether the lane's group is a choice
-      float score = neg_inf();
+      float score = neg_inf(), size = 0.f;                       // of the group; the sizes of the values it is made of
       if (grouped && MODE != 0 && p.top2) {
         float a = neg_inf(), b = neg_inf();
 #pragma unroll
@@ -522,6 +522,7 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
           a = fmaxf(a, a2);
         }
         score = b > neg_inf() ? a + b : a;
+        size = fabsf(a) + (b > neg_inf() ? fabsf(b) : 0.f);
       }
       if (MODE == 0 || !has_bias) {                              // without a bias the logits' order is the scores'
 #pragma unroll
@@ -556,9 +557,16 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
         }
         const bool kept = open && rank < p.keep;
         if (MODE != 0 && (has_bias || p.top2)) {
-          const float lo = -row_max<LPR>(kept ? -score : none()), hi = row_max<LPR>(kept ? none() : score);
-          // 2.4e-7: four roundings of 2^-24 in the two sums with the bias and of two values
-          hangs = lo - hi <= (p.top2 ? 2.f * tol : tol) + 2.4e-7f * fabsf(lo);
+          // A score is the true one within tol / 2 for each of its values and three roundings
+          // of 2^-24 of their sizes: where the bias was added, where the two were (which can
+          // be far larger than their sum) and in the two lines below.  A masked group's is
+          // exact; where the sizes pass fp32 nothing is known.
+          if (!p.top2) size = fabsf(score);
+          const float e = score > neg_inf() ? 1.8e-7f * size : 0.f;
+          const bool known = e < __uint_as_float(0x7f800000u);
+          const float least = known ? score - e : neg_inf(), most = known ? score + e : -neg_inf();
+          const float lo = -row_max<LPR>(kept ? -least : none()), hi = row_max<LPR>(kept ? none() : most);
+          hangs = lo - hi <= (p.top2 ? 2.f * tol : tol);
         }
         open = kept;
         const unsigned lanes = __ballot_sync(kFull, kept);

@@ -347,3 +347,37 @@ def test_a_larger_value_behind_equal_ones(mr, copies, grouped):
     for k in (1, 2, 3, 8):
         check(mr, torch.from_numpy(z), k, "sigmoid", bias, 4 if grouped else 1, 3 if grouped else 1, "max")
         check(mr, torch.from_numpy(z).to(torch.bfloat16), k, "sigmoid", bias, 4 if grouped else 1, 3 if grouped else 1, "top2")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size", [10.0, 64.0, 1000.0, 4096.0, 1e6])
+def test_groups_of_large_biases_that_cancel(mr, score, size):
+    """A group's two largest of opposite sign and far larger than their sum: fp32 rounds each in
+    proportion to its own size, and the groups taken are those of double precision."""
+    rng = np.random.default_rng(int(size))
+    for T, G, gs, keep in ((1500, 2, 2, 1), (700, 8, 2, 3), (300, 4, 5, 2)):
+        z = np.tile(rng.standard_normal((T, 1, gs)), (1, G, 1))
+        z = z + rng.uniform(-4, 4, (T, G, gs)) * size * 2.0 ** -24        # apart by what fp32 rounds the choice values by
+        bias = np.full((G, gs), -2 * size, np.float32)
+        bias[:, 0], bias[:, 1] = size, -size
+        zt = torch.from_numpy(z.reshape(T, G * gs).astype(np.float32))
+        for group_score in ("top2", "max"):
+            check(mr, zt, 1, score, bias.ravel(), G, keep, group_score)
+            check(mr, zt.to(torch.bfloat16), 2, score, bias.ravel(), G, keep, group_score)
+        spread = rng.uniform(-size, size, G * gs).astype(np.float32)
+        check(mr, zt, 2, score, spread, G, keep, "top2")
+    z = torch.tensor([[0.0008, 0, 0, 0.00076]])
+    bias = np.array([4096, -4096, 4096, -4096], np.float32)
+    check(mr, z, 1, score, bias, 2, 1, "top2")
+    check(mr, torch.tensor([[-0.377855, 1.951048, 0.551829, 0.608678]]), 1, score, np.array([1000.1, -1000, 900.1, -900], np.float32), 2, 1, "top2")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_groups_whose_sums_pass_fp32(mr, score):
+    """Choice values near the largest fp32 number: their sums order groups as double precision has them."""
+    z = logits_of(60, 12, torch.float32, seed=3)
+    big = np.array([3.0e38, 2.9e38, -3e38, 3.1e38, 3.05e38, 0, 3.2e38, 3.3e38, 1, 3e38, -2e38, -3e38], np.float32)
+    for bias in (big, np.roll(big, 3), -big):
+        for keep in (1, 2, 3):
+            check(mr, z, 2, score, bias, 4, keep, "top2")
+            check(mr, z, 2, score, bias, 4, keep, "max")
