@@ -118,7 +118,9 @@ struct DoubleScore {
   float m;
   double sum;
   __device__ __forceinline__ double operator()(float z) const {
-    return softmax ? exp(double(z) - double(m)) / sum : 1.0 / (1.0 + exp(-double(z)));
+    if (softmax) return exp(double(z) - double(m)) / sum;
+    const double t = exp(-fabs(double(z)));                      // never above 1: small scores stay what they are
+    return (z >= 0.f ? 1.0 : t) / (1.0 + t);
   }
 };
 template <class Elem>

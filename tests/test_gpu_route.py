@@ -381,3 +381,13 @@ def test_groups_whose_sums_pass_fp32(mr, score):
         for keep in (1, 2, 3):
             check(mr, z, 2, score, bias, 4, keep, "top2")
             check(mr, z, 2, score, bias, 4, keep, "max")
+
+
+@pytest.mark.parametrize("E,G", [(32, 8), (256, 8)])
+def test_sigmoid_scores_at_the_end_of_double_precision(mr, E, G):
+    """Scores between 1e-313 and 1e-305, which fp32 holds as 0: in their order all the same."""
+    rng = np.random.default_rng(E)
+    z = torch.from_numpy(rng.uniform(-720, -704, (200, E)).astype(np.float32))
+    for bias in (None, np.zeros(E, np.float32)):
+        check(mr, z, 4, "sigmoid", bias, G, 3, "top2")
+        check(mr, z, 4, "sigmoid", bias, G, 3, "max")
