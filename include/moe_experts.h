@@ -150,7 +150,8 @@ MOE_API moe_status moe_quantize_weights(const void* w, moe_dtype dt, int32_t E, 
  *   q [M,K] e4m3, scale [ceil(K/128), M] fp32: as moe_quantize_rows
  *   wq [E,N,K] e4m3, wscale [E, ceil(N/128), ceil(K/128)] fp32: as moe_quantize_weights
  *   out [M,N] bf16 or fp32 (out_dt)
- * Scales may be any fp32 numbers.  A block's 128 products are summed by the
+ * Scales may be any fp32 numbers; rows for which two scales' product is past fp32's
+ * normal numbers are computed once more from the operands, which takes longer.  A block's 128 products are summed by the
  * tensor core in fp32 (where products below about 2^-25 of the block's largest
  * may be lost), the blocks in fp32 registers, in order; the one rounding to bf16
  * is at the end.  A row's result does not depend on the other rows.

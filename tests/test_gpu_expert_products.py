@@ -415,3 +415,68 @@ def test_wgrad_of_many_tiles_is_exact_for_whole_numbers(mr):
     for e, n in enumerate(counts):
         assert torch.equal(got[e].double(), dy[at:at + n].T @ x[at:at + n]), e
         at += n
+
+
+TINY = 2.0 ** -149                                               # fp32's smallest step: half of it is a rounding there
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K,E,N", [(150, 640, 2, 304), (900, 400, 2, 288), (5, 128, 1, 16)])
+def test_scales_whose_product_leaves_fp32(mr, M, K, E, N, dtype):
+    """Row scales by which the product of two scales is past 2^128 or far below 2^-126, or a scale is 0,
+    while the results are ordinary numbers; rows of codes 0 give 0, not 0 times infinity.  Rows of
+    ordinary scales keep their bits beside them."""
+    g = torch.Generator().manual_seed(M)
+    blocks = -(-K // 128)
+    wq = (torch.randn(E, N, K, generator=g) * 0.03).clamp(-2.0 ** -4, 2.0 ** -4).to(F8).cuda()
+    wscale = ((1 + torch.rand(E, -(-N // 128), blocks, generator=g)) * 2.0 ** torch.tensor([20.0, -40.0, 20.0, -45.0, -38.0])[:blocks]).cuda()
+    up, down, no = 2.0 ** 112, 1.3 * 2.0 ** -106, 1.0             # beside 2^20: 2^132; beside 2^-40: 2^-146
+    kind = torch.arange(M) % 4
+    codes = torch.randn(M, K, generator=g)
+    q, scale = torch.zeros(M, K), torch.ones(blocks, M)
+    for b in range(blocks):
+        at = slice(128 * b, 128 * (b + 1))
+        big = b in (0, 2)                                         # the blocks of large weight scales
+        q[:, at] = torch.where(kind[:, None] == 0, (codes[:, at] * 2.0 ** -9).clamp(-2.0 ** -8, 2.0 ** -8) if big else torch.zeros(()),
+                               torch.where(kind[:, None] == 1, (codes[:, at] * 200).clamp(-448, 448) if not big else torch.zeros(()),
+                                           codes[:, at] * 60)).clamp(-448, 448)
+        scale[b] = torch.where(kind == 0, up, torch.where(kind == 1, down, torch.where(kind == 2, no, 0.0))) * (1 + torch.rand(M, generator=g) / 8)
+    q, scale = q.to(F8).cuda(), scale.cuda()
+    q.view(torch.uint8)[8::16] = 0
+    offsets, _, rows = split([M // E] * (E - 1) + [M - M // E * (E - 1)])
+    got = mr.moe_expert_matmul(q, scale, wq, wscale, offsets, out_dtype=dtype)
+    want, size = ref.matmul(wide(q), wide(scale), wide(wq), wide(wscale), rows)
+    bound = (256 + 3 * blocks) * ref.U32 * size + blocks * TINY
+    if dtype == torch.bfloat16:
+        bound = bound * (1 + ref.U16) + ref.U16 * np.abs(want) + 2.0 ** -134
+    assert np.abs(want).max() > 2.0 ** 110 and np.isfinite(wide(got)).all() and not wide(got)[3::4].any()
+    ref.assert_near("out", wide(got), want, bound)
+    alone = scale.clone()
+    alone[:, kind.cuda() != 2] = 1
+    assert torch.equal(mr.moe_expert_matmul(q, alone, wq, wscale, offsets, out_dtype=dtype)[2::4], got[2::4])
+
+
+def test_wgrad_scales_whose_product_leaves_fp32(mr):
+    """The same for both sides' scales of a weight gradient, which meet in every element."""
+    g = torch.Generator().manual_seed(5)
+    N, K, counts = 272, 304, [300, 0, 128, 17]
+    rows = ref.expert_rows(np.concatenate([[0], np.cumsum(counts)]), None, sum(counts))
+    width = mr.moe_quantize_cols_width(sum(counts), len(counts))
+    dq, xq = ((torch.randn(n, width, generator=g) * 100).clamp(-448, 448).to(F8).cuda() for n in (N, K))
+    ds, xs = ((1 + torch.rand(width // 128, n, generator=g)).cuda() for n in (N, K))
+    ds[:, 1::8] *= 2.0 ** 110
+    ds[:, 2::8] *= 2.0 ** -145                                    # small sums times these hold few digits in fp32
+    ds[:, 3::8] *= 2.0 ** -120
+    ds[:, 5::8] = 0
+    xs[:, 0::4] *= 2.0 ** -100
+    xs[:, 1::4] *= 2.0 ** 75
+    xs[:, 2::4] *= 2.0 ** -60
+    xs[:, 3::4] *= 2.0 ** -70
+    dq[2::8] = (torch.randn(dq[2::8].shape, generator=g) * 2.0 ** -8).to(F8).cuda()
+    dq.view(torch.uint8)[9] = 0
+    got = mr.moe_expert_wgrad(dq, ds, xq, xs, i32(counts))
+    want, size = ref.wgrad(wide(dq), wide(ds), wide(xq), wide(xs), rows)
+    over = size > 2.0 ** 127                                      # 2^110 times 2^75: infinite, or 0
+    assert (~np.isfinite(wide(got))[over]).all() and np.isfinite(wide(got))[~over].all()
+    bound = (256 + 3 * 3) * ref.U32 * size + 3 * TINY
+    ref.assert_near("dw", np.where(over, 0, wide(got)), np.where(over, 0, want), np.where(over, 0, bound))
