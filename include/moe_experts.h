@@ -181,7 +181,8 @@ MOE_API moe_status moe_expert_wgrad(const void* dyq, const float* dyscale, const
  * calls have left on the current device (synchronises `stream`, on which they
  * were queued).  *flags = 0 when every wait completed; otherwise returns
  * MOE_ERR_TIMEOUT with bit 2 set: a wait of a kernel's pipeline expired and its
- * output is incomplete. */
+ * output is incomplete.  Bits are read and cleared in one step: each is given to one
+ * reader, whichever stream its call ran on. */
 MOE_API moe_status moe_expert_device_status(moe_stream_t stream, int32_t* flags);
 
 /* ------------------------------------------------------------------------ */

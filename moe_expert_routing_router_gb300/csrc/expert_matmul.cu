@@ -23,6 +23,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 namespace moe {
 namespace {
 
@@ -42,6 +44,12 @@ constexpr unsigned kFull = 0xffffffffu;
 // Error bits of the device's calls: they carry no other state from call to call,
 // so calls on any streams, and captured ones, share the word.
 __device__ int g_mm_errors;
+
+// Read and cleared in one step, so that a call that finds bits set is always followed by the
+// read that tells of them.  As many reads as this may wait at once, each in a place of its own.
+constexpr unsigned kReads = 256;
+__device__ int g_mm_read[kReads];
+__global__ void take_errors_kernel(unsigned place) { g_mm_read[place] = atomicExch(&g_mm_errors, 0); }
 
 // ---- tcgen05 / TMA primitives ------------------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
@@ -824,15 +832,15 @@ cudaError_t launch(const MatmulParams& p, int sms, const char** error, cudaStrea
 }  // namespace
 
 cudaError_t expert_matmul_errors(int* bits, cudaStream_t stream) {
+  static std::atomic<unsigned> calls{0};
+  const unsigned place = calls.fetch_add(1, std::memory_order_relaxed) % kReads;
+  take_errors_kernel<<<1, 1, 0, stream>>>(place);
+  cudaError_t e = cudaGetLastError();
   void* word = nullptr;
-  cudaError_t e = cudaGetSymbolAddress(&word, g_mm_errors);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(bits, word, sizeof(int), cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  if (e == cudaSuccess && *bits != 0) {
-    e = cudaMemsetAsync(word, 0, sizeof(int), stream);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  }
-  return e;
+  if (e == cudaSuccess) e = cudaGetSymbolAddress(&word, g_mm_read);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(bits, static_cast<int*>(word) + place, sizeof(int), cudaMemcpyDeviceToHost, stream);
+  const cudaError_t done = cudaStreamSynchronize(stream);
+  return e == cudaSuccess ? done : e;
 }
 
 cudaError_t launch_expert_matmul(const MatmulParams& p, int sms, const char** error, cudaStream_t stream) {

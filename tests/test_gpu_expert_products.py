@@ -480,3 +480,35 @@ def test_wgrad_scales_whose_product_leaves_fp32(mr):
     assert (~np.isfinite(wide(got))[over]).all() and np.isfinite(wide(got))[~over].all()
     bound = (256 + 3 * 3) * ref.U32 * size + 3 * TINY
     ref.assert_near("dw", np.where(over, 0, wide(got)), np.where(over, 0, want), np.where(over, 0, bound))
+
+
+def test_a_call_beside_the_status_is_reported_or_right(mr, native_lib):
+    """An error is read while another call is queued behind the read: that call either is covered by
+    what was read or does its work."""
+    import threading
+    import time
+
+    q, scale, wq, wscale = operands(200, 1024, 1, 256, 4)
+    want = mr.moe_expert_matmul(q, scale, wq, wscale)
+    out = torch.full_like(want, 5.0)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    native_lib.moe_set_wait_timeout_ns(1_000_000)
+    native_lib.moe_set_unreachable_barriers(1)
+    try:
+        mr.moe_expert_matmul(q, scale, wq, wscale)
+        torch.cuda.synchronize()
+    finally:
+        native_lib.moe_set_unreachable_barriers(0)
+        native_lib.moe_set_wait_timeout_ns(0)
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)                           # some 0.1 s, in which both are queued
+    read = []
+    reader = threading.Thread(target=lambda: read.append(mr.moe_expert_device_status(stream=s)))
+    reader.start()
+    time.sleep(0.02)
+    mr.moe_expert_matmul(q, scale, wq, wscale, out=out, stream=s)
+    reader.join()
+    s.synchronize()
+    assert read == [2] and torch.equal(out, want)
+    assert mr.moe_expert_device_status() == 0
