@@ -890,8 +890,13 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_picks_kernel(const Ro
   }
 }
 
+// CTAs of an SM: the loads' latency is hidden by other rows.
+template <int NV>
+constexpr int kBwdCtas = NV <= 4 ? 8 : NV <= 8 ? 6 : NV <= 12 ? 5 : 4;
+
 template <class Elem, int NV>
-__global__ void __launch_bounds__(kRouteThreads) route_bwd_softmax_kernel(const RouteBwdParams p) {
+__global__ void __launch_bounds__(kRouteThreads, kBwdCtas<NV>) route_bwd_softmax_kernel(const RouteBwdParams p) {
+  __shared__ float4 s_pick[kRouteWarps][kPickLanes];     // a row's picks: expert (as bits), dgate, score times dgate
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   const int64_t stride = int64_t(gridDim.x) * kRouteWarps;
   for (int64_t row = int64_t(blockIdx.x) * kRouteWarps + warp; row < p.T; row += stride) {
@@ -915,11 +920,34 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_softmax_kernel(const 
       sum += z[i];
     }
     sum = warp_sum_f(sum);
+    const float own = zp > neg_inf() ? ex2_approx((zp - shift) * kLog2e) : 0.f;
+    // dg_i - sum_j p_j dg_j at a pick, as dg_i times the share of all other experts less the
+    // other picks' p_j dg_j: next to an expert that has nearly all of the row the rest is
+    // small, and its digits count.  So it is summed apart there.
+    float outside = sum - own;
+    const unsigned most = __ballot_sync(kFull, own > 0.5f * sum);
+    if (most != 0u) {
+      const int o = __shfl_sync(kFull, e, __ffs(most) - 1), at = o % kWarp == lane ? o / kWarp : -1;
+      float rest = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (i != at) rest += z[i];
+      rest = warp_sum_f(rest);
+      if (e == o) outside = rest;
+    }
+    if (lane < kPickLanes) s_pick[warp][lane] = make_float4(__int_as_float(e), dg, own * dg, 0.f);
+    __syncwarp();
+    float dge = 0.f, S = 0.f, others = 0.f;              // the lanes from 8 on have no pick
+    for (int j = 0; j < p.k; ++j) {
+      const float4 o = s_pick[warp][j];
+      const bool same = __float_as_int(o.x) == e;
+      S += o.z;
+      if (same) dge += o.y;
+      if (!same) others += o.z;
+    }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const float pp = zp > neg_inf() ? ex2_approx((zp - shift) * kLog2e) * inv : 0.f;
-    float S = 0.f;                                       // sum_j p_j dg_j over the picks
-    for (int j = 0; j < p.k; ++j) S += __shfl_sync(kFull, pp, j) * __shfl_sync(kFull, dg, j);
-    const float v = pp * (sum_same(dg, e, p.k) - S);     // the lanes from 8 on have no pick
+    const float v = own * inv * ((dge * outside - others) * inv);
+    S *= inv;
     float* out = p.dlogits + row * p.E;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -931,26 +959,28 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_softmax_kernel(const 
   }
 }
 
+template <class Elem, int NV>
+cudaError_t bwd_softmax(const RouteBwdParams& p, int sms, cudaStream_t stream) {
+  const int64_t want = (p.T + kRouteWarps - 1) / kRouteWarps, most = int64_t(sms) * kBwdCtas<NV>;   // all at once
+  route_bwd_softmax_kernel<Elem, NV><<<int(want < most ? want : most), kRouteThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <class Elem>
 cudaError_t bwd_elem(const RouteBwdParams& p, int sms, cudaStream_t stream) {
-  const bool picks = !p.softmax || p.renorm;
-  const int64_t rows = int64_t(kRouteWarps) * (picks ? kMaxPer : 1), want = (p.T + rows - 1) / rows;
+  if (p.softmax && !p.renorm) {
+    if (p.E <= 4 * kWarp) return bwd_softmax<Elem, 4>(p, sms, stream);
+    if (p.E <= 8 * kWarp) return bwd_softmax<Elem, 8>(p, sms, stream);
+    if (p.E <= 12 * kWarp) return bwd_softmax<Elem, 12>(p, sms, stream);
+    return bwd_softmax<Elem, 32>(p, sms, stream);
+  }
+  const int64_t rows = int64_t(kRouteWarps) * kMaxPer, want = (p.T + rows - 1) / rows;
   const int64_t most = int64_t(sms) * 8;
   const int grid = int(want < most ? want : most);
-  if (picks) {
-    if (p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.dlogits) % 16 == 0)
-      route_bwd_picks_kernel<Elem, true><<<grid, kRouteThreads, 0, stream>>>(p);
-    else
-      route_bwd_picks_kernel<Elem, false><<<grid, kRouteThreads, 0, stream>>>(p);
-  } else if (p.E <= 4 * kWarp) {
-    route_bwd_softmax_kernel<Elem, 4><<<grid, kRouteThreads, 0, stream>>>(p);
-  } else if (p.E <= 8 * kWarp) {
-    route_bwd_softmax_kernel<Elem, 8><<<grid, kRouteThreads, 0, stream>>>(p);
-  } else if (p.E <= 12 * kWarp) {
-    route_bwd_softmax_kernel<Elem, 12><<<grid, kRouteThreads, 0, stream>>>(p);
-  } else {
-    route_bwd_softmax_kernel<Elem, 32><<<grid, kRouteThreads, 0, stream>>>(p);
-  }
+  if (p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.dlogits) % 16 == 0)
+    route_bwd_picks_kernel<Elem, true><<<grid, kRouteThreads, 0, stream>>>(p);
+  else
+    route_bwd_picks_kernel<Elem, false><<<grid, kRouteThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

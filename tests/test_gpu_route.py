@@ -391,3 +391,44 @@ def test_sigmoid_scores_at_the_end_of_double_precision(mr, E, G):
     for bias in (None, np.zeros(E, np.float32)):
         check(mr, z, 4, "sigmoid", bias, G, 3, "top2")
         check(mr, z, 4, "sigmoid", bias, G, 3, "max")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("E", [33, 100, 256, 384, 1000])
+def test_softmax_gradient_of_confident_rows(mr, E, dtype):
+    """A pick that has all of its row but 1e-4 to 1e-9: its gradient keeps the digits of what is left.
+    Bound: a pick's is p (D r + sum_j p_j (D - D_j)) over the other picks, r the share of what is not
+    picked and D an expert's sum of dgate; each share is off by (2 d + 96) 2^-24, d the row's spread,
+    two of them are multiplied, and 16 roundings cover the sums over picks."""
+    rng = np.random.default_rng(E)
+    gaps = np.repeat([6.0, 10.0, 12.0, 14.0, 16.0, 18.0, 20.0], 8)
+    T = len(gaps)
+    z = rng.uniform(-1, 1, (T, E)) * 0.5
+    top = rng.integers(0, E, T)
+    z[np.arange(T), top] = gaps
+    z = torch.from_numpy(z.astype(np.float32)).to(dtype)
+    zd = widen(z)
+    s = ref.scores(zd, "softmax")
+    eps = (2 * (2 * (zd.max(1) - zd.min(1)) + 96) + 16)[:, None] * ref.U32
+    for picks in (1, 2, 5, 8):
+        idx = np.stack([rng.permutation(E)[:picks] for _ in range(T)])
+        idx[:, 0] = top
+        idx[::4, -1] = top[::4]                                      # the same expert twice
+        idx[1::7, -1] = E                                            # no expert
+        dgate = rng.standard_normal((T, picks)).astype(np.float32)
+        got = mr.moe_route_bwd(z.cuda(), torch.from_numpy(idx.astype(np.int32)).cuda(), torch.from_numpy(dgate).cuda(),
+                               score="softmax", renorm=0, scale=1.5).cpu().numpy()
+        want = ref.route_grad(zd, idx, dgate, "softmax", False, 1.5)
+        D, picked = np.zeros((T, E)), np.zeros((T, E), bool)
+        for j in range(picks):
+            live = idx[:, j] < E
+            np.add.at(D, (np.arange(T)[live], idx[live, j]), 1.5 * dgate[live, j])
+            picked[np.arange(T)[live], idx[live, j]] = True
+        rest = np.where(picked, 0, s).sum(1, keepdims=True)
+        size = s * (s * np.abs(D)).sum(1, keepdims=True)
+        for t in range(T):
+            for e in np.flatnonzero(picked[t]):
+                o = picked[t].copy()
+                o[e] = False
+                size[t, e] = s[t, e] * (abs(D[t, e]) * rest[t, 0] + (s[t, o] * (abs(D[t, e]) + np.abs(D[t, o]))).sum())
+        ref.assert_near("dlogits", got, want, eps * size + 8 * FLT_MIN)
