@@ -432,3 +432,37 @@ def test_softmax_gradient_of_confident_rows(mr, E, dtype):
                 o[e] = False
                 size[t, e] = s[t, e] * (abs(D[t, e]) * rest[t, 0] + (s[t, o] * (abs(D[t, e]) + np.abs(D[t, o]))).sum())
         ref.assert_near("dlogits", got, want, eps * size + 8 * FLT_MIN)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("shift", [-300.0, -80.0, 0.0, 60.0])
+def test_gates_within_the_spread_of_the_row(mr, shift, score, dtype):
+    """Gates lose no digits by where a row's logits lie, only by how far they lie apart.  In units of
+    2^-24 of a gate:
+      shares     an exponential's argument z - max is rounded (d, the picks' spread, at most), expf
+                 is off by 4, a sigmoid's own exponential, sum and quotient by 6: d + 10 on either
+                 side of the share; 8 sums, quotient and scale: 2 d + 32
+      softmax    d + 4 of the own exponential; the row's sum: arguments rounded three times, at the
+                 mean distance from the maximum, below ln 1024 + 1 = 8: 24; ex2.approx 4; at most 23
+                 additions; quotient and scale: d + 58
+      sigmoid    exponential 4 on either side of 1 + e, sum, quotient and scale: 12
+    and the smallest normal number where an exponential underflows."""
+    for E, wide_by in ((24, 1.0), (256, 1.5), (1000, 2.0), (64, 15.0)):
+        z = (logits_of(200, E, torch.float32, seed=E, spread=wide_by) + shift).to(dtype)
+        zd = widen(z)
+        for k in (1, 4, 8):
+            for renorm in (True, False):
+                got = mr.moe_route_fwd(z.cuda(), k, score=score, renorm=int(renorm), scale=2.5)
+                idx = ref.choose(zd, k, score)
+                assert np.array_equal(got["idx"].cpu().numpy(), idx)
+                zp = np.take_along_axis(zd, idx, 1)
+                d = zp.max(1, keepdims=True) - zp.min(1, keepdims=True)
+                if renorm:
+                    units = 2 * d + 32
+                elif score == "softmax":
+                    units = zd.max(1, keepdims=True) - zp + 58
+                else:
+                    units = 12
+                w = ref.pick_weights(zd, idx, score, renorm)
+                ref.assert_near("gate", got["gate"].cpu().numpy(), 2.5 * w, 2.5 * (units * ref.U32 * w + FLT_MIN))
