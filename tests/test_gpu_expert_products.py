@@ -512,3 +512,71 @@ def test_a_call_beside_the_status_is_reported_or_right(mr, native_lib):
     s.synchronize()
     assert read == [2] and torch.equal(out, want)
     assert mr.moe_expert_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("value", [float("nan"), -float("nan"), float("inf"), -float("inf")])
+def test_not_finite_blocks_of_columns_and_weights(mr, value, dtype):
+    """One value that is not finite makes its block's scale NaN, whichever lane, warp and half of a
+    word meets it, and no other block's."""
+    counts = [130, 0, 300]
+    offsets, _, rows = split(counts)
+    M, K = sum(counts), 272
+    clean = values((M, K), 6, dtype)
+    q, scale = ref.quantize_cols(wide(clean), rows)
+    first = {0: 0, 130: 2}                                       # an expert's first row: its first block
+    for r, c in ((0, 0), (1, 1), (129, 271), (130, 128), (257, 127), (258, 8), (429, 143), (300, 200)):
+        x = clean.clone()
+        x[r, c] = value
+        got = mr.moe_quantize_cols(x.cuda(), offsets)
+        at = 0 if r < 130 else 130
+        b = first[at] + (r - at) // 128
+        bad = np.zeros_like(scale, bool)
+        bad[b, c] = True
+        s = wide(got["scale"])[:len(scale)]
+        assert np.array_equal(np.isnan(s), bad) and np.array_equal(s[~bad], scale[~bad])
+        same = np.ones_like(q, bool)
+        same[c, 128 * b:128 * (b + 1)] = False
+        assert np.array_equal(wide(got["q"])[:, :q.shape[1]][same], q[same])
+    clean = values((2, 144, 272), 7, dtype)
+    q, scale = ref.quantize_weights(wide(clean))
+    for e, n, c in ((0, 0, 0), (0, 127, 127), (1, 128, 3), (1, 143, 271), (0, 77, 130), (1, 16, 129)):
+        w = clean.clone()
+        w[e, n, c] = value
+        got = mr.moe_quantize_weights(w.cuda(), transposed=True)
+        bad = np.zeros_like(scale, bool)
+        bad[e, n // 128, c // 128] = True
+        s = wide(got["scale"])
+        assert np.array_equal(np.isnan(s), bad) and np.array_equal(s[~bad], scale[~bad])
+        assert np.array_equal(wide(got["scalet"]).transpose(0, 2, 1), s, equal_nan=True)
+        same = ~ref.spread(bad, q.shape)
+        assert np.array_equal(wide(got["q"])[same], q[same]) and np.array_equal(wide(got["qt"]).transpose(0, 2, 1)[same], q[same])
+
+
+@pytest.mark.parametrize("form", ["rows", "weights", "cols"])
+def test_every_product_with_a_block_that_is_not_finite_is_nan(mr, form):
+    """The NaN scale reaches every result that the block is part of, and no other."""
+    M, K, N = 200, 272, 144
+    x, w = values((M, K), 8, torch.float32), values((1, N, K), 9, torch.float32)
+    if form == "rows":
+        x[17, 200] = float("inf")
+    elif form == "weights":
+        w[0, 130, 5] = float("nan")
+    else:
+        x[150, 33] = -float("inf")
+    a, b = mr.moe_quantize_rows(x.cuda()), mr.moe_quantize_weights(w.cuda())
+    bad = np.zeros((M, N), bool)
+    if form == "cols":
+        offsets, kept, _ = split([M], [M])
+        dy = values((M, N), 10, torch.float32)
+        d, c = mr.moe_quantize_cols(dy.cuda(), offsets, kept), mr.moe_quantize_cols(x.cuda(), offsets, kept)
+        got = mr.moe_expert_wgrad(d["q"], d["scale"], c["q"], c["scale"], kept)[0]
+        bad = np.zeros((N, K), bool)
+        bad[:, 33] = True
+    else:
+        got = mr.moe_expert_matmul(a["q"], a["scale"], b["q"], b["scale"], out_dtype=torch.float32)
+        if form == "rows":
+            bad[17] = True
+        else:
+            bad[:, 128:] = True
+    assert np.array_equal(np.isnan(wide(got)), bad)
