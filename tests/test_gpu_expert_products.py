@@ -580,3 +580,44 @@ def test_every_product_with_a_block_that_is_not_finite_is_nan(mr, form):
         else:
             bad[:, 128:] = True
     assert np.array_equal(np.isnan(wide(got)), bad)
+
+
+@pytest.mark.parametrize("case", [
+    {"op": "route", "T": 300, "E": 96, "k": 4, "dtype": "bf16", "score": "sigmoid", "bias": True, "groups": 4, "keep": 2, "group_score": "top2",
+     "renorm": True, "scale": 2.5, "bwd": True},
+    {"op": "route", "T": 77, "E": 33, "k": 3, "dtype": "fp32", "score": "softmax", "bias": False, "groups": 3, "keep": 2, "group_score": "max",
+     "renorm": False, "scale": 1.0, "bwd": True},
+    {"op": "quantize", "form": "rows", "T": 50, "k": 2, "E": 8, "K": 272, "dtype": "bf16", "gather": True, "cf": 1.25},
+    {"op": "quantize", "form": "cols", "T": 150, "k": 2, "E": 4, "K": 144, "dtype": "fp32", "gather": False, "cf": 1.0},
+    {"op": "quantize", "form": "weights", "T": 1, "k": 1, "E": 2, "K": 272, "N": 144, "dtype": "bf16", "gather": False, "cf": 1.0},
+    {"op": "matmul", "T": 90, "k": 2, "E": 4, "K": 400, "N": 144, "out": "bf16", "cf": 1.0},
+    {"op": "wgrad", "T": 130, "k": 2, "E": 4, "K": 144, "N": 272, "cf": 1.25},
+    {"op": "combine", "T": 40, "k": 4, "E": 8, "H": 264, "dtype": "bf16", "cf": 1.0, "bwd": True},
+], ids=lambda c: "-".join(str(c[k]) for k in ("op", "form") if k in c))
+def test_measured_calls_against_their_plain_and_exact_forms(mr, monkeypatch, case):
+    """What perf/operators.py times: the calls, their plain torch forms and the definitions in 64 bits
+    agree.  Whole numbers, codes and scales are equal; a number is off by half a step of its type
+    and the sums' rounding, 1e-5 of the output's largest covers hundreds of 2^-24."""
+    import importlib.util
+    from pathlib import Path
+    spec = importlib.util.spec_from_file_location("operators", Path(__file__).resolve().parents[1] / "perf" / "operators.py")
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+
+    def flat(o):
+        return dict(o) if isinstance(o, dict) else {"out": o}
+
+    plain = {n: v.clone() for n, v in flat(ops.run(ops.prepare(case, 3))).items()}
+    monkeypatch.setattr(ops, "own", True)
+    got = flat(ops.run(ops.prepare(case, 3)))
+    want = flat(ops.exact(case, 3))
+    assert set(plain) == set(got) == set(want)
+    for name, w in want.items():
+        w = torch.as_tensor(w).double().cpu()
+        for side in (plain[name], got[name]):
+            v = side.double().cpu()
+            if not side.is_floating_point() or case["op"] == "quantize":
+                assert torch.equal(v, w), name
+            else:
+                step = 2.0 ** -8 if side.dtype == torch.bfloat16 else 0.0
+                assert ((v - w).abs() <= step * w.abs() + 1e-5 * w.abs().max()).all(), name
