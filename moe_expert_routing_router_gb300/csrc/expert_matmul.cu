@@ -166,8 +166,8 @@ __device__ __forceinline__ void turn(uint4* v, int lane) {
 
 // ---- the kernel ----------------------------------------------------------------
 // RB: blocks that share a stage, its barriers and its place in tensor memory.
-// STORE: the tile leaves through shared memory by tensor copies (two buffers of
-// 2 KB a warp), which costs a stage.
+// STORE: the tile leaves through shared memory by tensor copies (a buffer of 4 KB a
+// warp), which costs a stage.
 template <int BN, int RB, bool STORE>
 struct Tile {
   static constexpr int kBlockBytes = (kBM + BN) * kBK;

@@ -357,7 +357,7 @@ __device__ __noinline__ int route_settle(const RouteParams& p, int64_t row, int 
 // ---------------------------------------------------------------------------
 // Forward.
 //   LPR   lanes of a row; NV: experts of a lane, at least `tchunk`
-//   VB    bytes per load; above the element's size only with FULL: every lane has
+//   VB    bytes per load, 16 or the element's size; 16 only with FULL: every lane has
 //         NV experts or none, and rows, groups and the array are aligned
 //   MODE  0: the order of the logits decides everything and gates need no sum over the
 //         row; 1: sigmoid scores; 2: softmax scores
@@ -438,7 +438,6 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
       for (int i = 0; i < kPer; ++i) part[i] = Elem::kNegInf;
       if (row < p.T && (FULL ? n > 0 : v * kPer < n)) {
         if constexpr (VB == 16) *reinterpret_cast<uint4*>(part) = *reinterpret_cast<const uint4*>(src + v * kPer);
-        else if constexpr (VB == 8) *reinterpret_cast<uint2*>(part) = *reinterpret_cast<const uint2*>(src + v * kPer);
         else if constexpr (VB == 4) *reinterpret_cast<uint32_t*>(part) = *reinterpret_cast<const uint32_t*>(src + v * kPer);
         else part[0] = src[v];
       }
@@ -480,7 +479,12 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
         for (int i = 0; i < NV; ++i) c[i] *= inv;
         // In units of the row's largest score, 1 / sum: a score's rounded argument moves
         // it by 3 * 2^-24 x e^-x <= 0.7e-7, ex2.approx by 2^-22 of itself and of the
-        // sum, the sum's NV / 4 + 7 additions by 2^-24 each, the quotient by 2^-23
+        // sum, the sum's NV / 4 + 7 additions by 2^-24 each, the quotient by 2^-23.
+        // The sum's arguments move it too, by 3 * 2^-24 times the mean distance of the row's
+        // logits from the largest, which for E experts is below t - 1, (t - 1) e^t = E - 1:
+        // 8e-7 for 1024.  That is within tol: the sum's error scales all scores of the row
+        // alike, so a comparison meets it once, and tol counts it for either side; against
+        // scores from an exact sum (settling a row) it meets one side only.
         tol = (2.f * 6.7e-7f + (NV / 4 + 7) * 2.f * 6e-8f) * inv;
         const int from = (lane / kPickLanes - r0) * LPR;         // the row whose pick the lane will hold
         const bool mine = lane / kPickLanes >= r0 && lane / kPickLanes < r0 + R;
@@ -794,9 +798,9 @@ cudaError_t fwd_launch(const RouteParams& p, int sms, cudaStream_t stream) {
 
 template <class Elem, int LPR, int NV, int MODE>
 cudaError_t fwd_width(const RouteParams& p, int sms, cudaStream_t stream) {
-  constexpr int kSize = int(sizeof(typename Elem::Raw)), kRow = NV * kSize;
-  constexpr int VB = kRow % 16 == 0 ? 16 : 8;
-  // Loads of VB bytes: every lane has NV experts or none, and rows, groups and the array are aligned.
+  constexpr int kSize = int(sizeof(typename Elem::Raw)), VB = 16;
+  static_assert(NV * kSize % VB == 0, "a lane's experts are whole loads");
+  // Loads of 16 bytes: every lane has NV experts or none, and rows, groups and the array are aligned.
   const bool full = p.tchunk == NV && p.gs == (p.tchunk << p.tshift);
   if (full && int64_t(p.E) * kSize % VB == 0 && reinterpret_cast<uintptr_t>(p.logits) % VB == 0)
     return fwd_launch<Elem, LPR, NV, VB, true, MODE>(p, sms, stream);
