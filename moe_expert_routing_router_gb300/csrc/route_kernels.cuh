@@ -528,7 +528,7 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
           a = fmaxf(a, a2);
         }
         score = b > neg_inf() ? a + b : a;
-        size = fabsf(a) + (b > neg_inf() ? fabsf(b) : 0.f);
+        size = a > neg_inf() ? fabsf(a) + (b > neg_inf() ? fabsf(b) : 0.f) : 0.f;
       }
       if (MODE == 0 || !has_bias) {                              // without a bias the logits' order is the scores'
 #pragma unroll
@@ -567,8 +567,8 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
           // of 2^-24 of their sizes: where the bias was added, where the two were (which can
           // be far larger than their sum) and in the two lines below.  A masked group's is
           // exact; where the sizes pass fp32 nothing is known.
-          if (!p.top2) size = fabsf(score);
-          const float e = score > neg_inf() ? 1.8e-7f * size : 0.f;
+          if (!p.top2) size = score > neg_inf() ? fabsf(score) : 0.f;
+          const float e = 1.8e-7f * size;
           const bool known = e < __uint_as_float(0x7f800000u);
           const float least = known ? score - e : neg_inf(), most = known ? score + e : -neg_inf();
           const float lo = -row_max<LPR>(kept ? -least : none()), hi = row_max<LPR>(kept ? none() : most);

@@ -466,3 +466,18 @@ def test_gates_within_the_spread_of_the_row(mr, shift, score, dtype):
                     units = 12
                 w = ref.pick_weights(zd, idx, score, renorm)
                 ref.assert_near("gate", got["gate"].cpu().numpy(), 2.5 * w, 2.5 * (units * ref.U32 * w + FLT_MIN))
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_banned_groups_beside_masked_ones(mr, score):
+    """Groups whose two largest sum below fp32's range, beside groups whose experts are all masked: the
+    former come first, in the order of their sums."""
+    z = logits_of(40, 12, torch.float32, seed=5)
+    bias = np.full(12, -3.2e38, np.float32)
+    bias[8:10], bias[6:8] = -3.1e38, -3.0e38
+    for masked in ((0, 1), (0, 1, 4, 5), (4, 5, 10, 11), (0, 4, 8)):
+        zm = z.clone()
+        zm[:, list(masked)] = -float("inf")
+        for keep in (1, 2, 3, 4, 5):
+            check(mr, zm, 2, score, bias, 6, keep, "top2")
+            check(mr, zm, 1, score, np.roll(bias, 3), 6, keep, "max")
