@@ -150,11 +150,13 @@ MOE_API moe_status moe_quantize_weights(const void* w, moe_dtype dt, int32_t E, 
  *   q [M,K] e4m3, scale [ceil(K/128), M] fp32: as moe_quantize_rows
  *   wq [E,N,K] e4m3, wscale [E, ceil(N/128), ceil(K/128)] fp32: as moe_quantize_weights
  *   out [M,N] bf16 or fp32 (out_dt)
- * Scales may be any fp32 numbers; rows for which two scales' product is past fp32's
- * normal numbers are computed once more from the operands, which takes longer.  A block's 128 products are summed by the
- * tensor core in fp32 (where products below about 2^-25 of the block's largest
- * may be lost), the blocks in fp32 registers, in order; the one rounding to bf16
- * is at the end.  A row's result does not depend on the other rows.
+ * Scales may be any fp32 numbers.  Rows that meet a product of two scales outside
+ * fp32's normal numbers (2^-126 to 2^128) are computed once more from the operands,
+ * which takes longer: all rows some 30 times as long.
+ * A block's 128 products are summed by the tensor core in fp32 (where products below
+ * about 2^-25 of the block's largest may be lost), the blocks in fp32 registers, in
+ * order; the one rounding to bf16 is at the end.  A row's result does not depend on
+ * the other rows.
  * The data gradient is the same call with dy's rows and the transposed weights.
  * K and N are multiples of 16 up to MOE_MAX_WIDTH, E * N < 2^31, M >= 1, M < 2^31;
  * q, wq and out are 16-byte aligned.
@@ -171,7 +173,8 @@ MOE_API moe_status moe_expert_matmul(const void* q, const float* scale, int64_t 
  *   dyq [N,width], dyscale [width/128, N] and xq [K,width], xscale [width/128, K]:
  *   moe_quantize_cols of the rows of dy and x with the same offsets and kept
  *   kept [E]: the rows of each expert
- * Sums as in moe_expert_matmul.  K and N as there; width is a multiple of 128
+ * Sums and scales as in moe_expert_matmul (a scale of dy outside 2^-108 to 2^103
+ * takes the longer way).  K and N as there; width is a multiple of 128
  * below 2^31; all arrays but kept are 16-byte aligned. */
 MOE_API moe_status moe_expert_wgrad(const void* dyq, const float* dyscale, const void* xq, const float* xscale,
                                     int64_t width, int32_t N, int32_t K, int32_t E, const int32_t* kept, float* dw,

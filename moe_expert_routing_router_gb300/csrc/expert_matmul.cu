@@ -21,7 +21,6 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 #include <atomic>
 
@@ -191,7 +190,7 @@ struct alignas(16) Shared {
   uint64_t full[8], done[8], tempty[8], drain, scales[kScaleSlots];
   uint32_t tmem;
   int abort;
-  int redo;                                                    // weight gradient: a scale of a row is not plain
+  int redo;                                                    // a row's scales are not plain
   int block[kMaxE + 1];                                        // weight gradient: column blocks before expert e; product: its first row
   int first[WGRAD ? 1 : kMaxE + 1];                            // product: tiles before expert e
   int count[WGRAD ? 1 : kMaxE];                                // product: its rows
@@ -292,65 +291,128 @@ struct Walk {
 // turn by scales of which the first lies between 2^-108 and 2^103.  Other rows, whose term can
 // be an ordinary number all the same, are computed once more behind the last tile.
 // (Decided block by block, with a second way to add one: the weight gradient 218 -> 228 us,
-// 512 rows of 64 experts 94 -> 98 us.)
+// 512 rows of 64 experts 94 -> 98 us.)  Of 65,536 rows of 64 experts a 64th once more takes
+// 5 ms, all of them 16 ms; where scales of 0 have the rows looked at, a fifth of the call.
 template <bool WGRAD>
-__device__ __forceinline__ bool plain_scale(float s) {
-  return fabsf(s) >= (WGRAD ? 0x1p-108f : 0x1p-126f) && fabsf(s) <= (WGRAD ? 0x1p103f : 0x1.fffffep127f);
+__device__ __forceinline__ bool plain_scale(float s) {           // what is not a number stays one either way
+  return !(fabsf(s) < (WGRAD ? 0x1p-108f : 0x1p-126f)) && !(fabsf(s) > (WGRAD ? 0x1p103f : 0x1.fffffep127f));
+}
+
+// Of a row and of a column; what a scale of 0 makes of any sum is the same either way.
+template <bool WGRAD>
+__device__ __forceinline__ bool plain_pair(float sa, float sb) { return plain_scale<WGRAD>(sa * sb) || sa == 0.f || sb == 0.f; }
+
+// Two numbers with the product of r and f, by which a block's sum is multiplied in turn without
+// leaving the normal numbers before the whole term does: the same two, or both moved by a
+// power of two.  (Digits of f lost below 2^-126 belong to a term below fp32's smallest; an f
+// that is cut at 2^101 makes the same infinity.)
+__device__ __forceinline__ float2 apart(float r, float f) {
+  if (plain_scale<true>(r)) return make_float2(r, f);
+  if (fabsf(r) < 1.f) return make_float2(r * 0x1p64f, f * 0x1p-64f);
+  const bool cut = fabsf(f) > 0x1p101f && fabsf(f) <= 0x1.fffffep127f;
+  return make_float2(r * 0x1p-26f, (cut ? copysignf(0x1p101f, f) : f) * 0x1p26f);
 }
 
 // The epilogue's warps and the one that looks at the scales meet.
 __device__ __forceinline__ void scales_known() { asm volatile("bar.sync 1, %0;" :: "n"((kEpiWarps + 1) * kWarp) : "memory"); }
 
-// Four products of e4m3 codes added to `sum`; each is exact in fp32.
-__device__ __forceinline__ float dot4(uint32_t a, uint32_t b, float sum) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t x, y;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(x) : "h"(uint16_t(a >> 16 * i)));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(uint16_t(b >> 16 * i)));
-    const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&x)), v = __half22float2(*reinterpret_cast<const __half2*>(&y));
-    sum = fmaf(u.x, v.x, sum);
-    sum = fmaf(u.y, v.y, sum);
-  }
-  return sum;
+// Four e4m3 codes as fp16, which holds them.
+__device__ __forceinline__ void codes_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(uint16_t(codes)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(uint16_t(codes >> 16)));
+}
+// d [16, 8] += a [16, 16] b [16, 8]: lane l holds columns 2 (l % 4) and the next one of rows
+// l / 4 and l / 4 + 8 of d.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A warp's rows of a tile whose scales are not plain, from the operands: a column a lane,
-// blocks summed in fp32, scaled and added in double.  Row `row0` of a and column `col0` of
-// expert e are the first; `to` is out's row of row0.
-template <bool WGRAD, bool BF16>
-__device__ __noinline__ void redo_rows(const MatmulParams& p, int e, int row0, int rows, int col0, int cols, int block0, int blocks, int64_t to) {
-  const int lane = threadIdx.x % kWarp;
+// A warp's rows of a tile whose scales are not plain, from the operands: 16 such rows at a
+// time by all the warp's columns, on fp16 products; half a block's sum and its scales by
+// `apart`.  Row `row0` of a and column `col0` of expert e are the first; `to` is out's row of
+// row0.  Both operands' codes are taken in the same order, 16 neighbours a lane.  (Single
+// products, a column a lane: 132 ms instead of 16.)
+template <int CW, bool WGRAD, bool BF16>
+__device__ __forceinline__ void redo_rows(const MatmulParams& p, int e, int row0, int rows, int col0, int cols, int block0, int blocks, int64_t to) {
+  const int lane = threadIdx.x % kWarp, g = lane / 4, t = lane % 4;
   const int64_t width = WGRAD ? p.blocks * kBK : p.K;
   const int kblocks = (p.K + kBK - 1) / kBK, cblocks = (p.C + kBK - 1) / kBK;
   const int64_t b_row0 = (WGRAD ? 0 : int64_t(e) * p.C) + col0;
-  const float* b_scales = WGRAD ? p.b_scale : p.b_scale + (int64_t(e) * cblocks + col0 / kBK) * kblocks;
-  const auto a_scale = [&](int r, int b) { return p.a_scale[WGRAD ? int64_t(b) * p.R + row0 + r : int64_t(b) * p.M + row0 + r]; };
-  for (int r = 0; r < rows; ++r) {
-    bool redo = false;
-    for (int b = block0 + lane; b < block0 + blocks; b += kWarp) {
-      const float sa = a_scale(r, b), sb = WGRAD ? 1.f : b_scales[b], s = sa * sb;
-      redo |= sa != 0.f && sb != 0.f && s == s && !plain_scale<WGRAD>(s);
-    }
-    if (!__any_sync(kFull, redo)) continue;
-    for (int c = lane; c < cols; c += kWarp) {
-      double sum = 0.0;
-      for (int b = block0; b < block0 + blocks; ++b) {
-        const int64_t x = int64_t(b) * kBK;
-        const uint4* pa = reinterpret_cast<const uint4*>(p.a + int64_t(row0 + r) * width + x);
-        const uint4* pb = reinterpret_cast<const uint4*>(p.b + (b_row0 + c) * width + x);
-        const int pieces = int(min(width - x, int64_t(kBK))) / 16;
-        float dot = 0.f;
-        for (int i = 0; i < pieces; ++i) {
-          const uint4 u = pa[i], v = pb[i];
-          dot = dot4(u.w, v.w, dot4(u.z, v.z, dot4(u.y, v.y, dot4(u.x, v.x, dot))));
-        }
-        sum += double(dot) * (double(a_scale(r, b)) * double(WGRAD ? p.b_scale[int64_t(b) * p.C + col0 + c] : b_scales[b]));
+  const float* b_scales = WGRAD ? p.b_scale + col0 : p.b_scale + (int64_t(e) * cblocks + col0 / kBK) * kblocks;
+  const auto a_scale = [&](int r, int b) { return r < rows ? p.a_scale[int64_t(b) * (WGRAD ? p.R : p.M) + row0 + r] : 0.f; };
+  bool redo = false;                                             // row `lane`
+#pragma unroll 8
+  for (int b = block0; b < block0 + blocks; ++b) redo |= !plain_pair<WGRAD>(a_scale(lane, b), WGRAD ? 1.f : b_scales[b]);
+  unsigned which = __ballot_sync(kFull, redo);
+  while (which != 0u) {
+    int row[2] = {32, 32};                                       // the lane's rows: the g-th and (g + 8)-th, 32 for none
+    for (int i = 0; i < 16 && which != 0u; ++i, which &= which - 1u)
+      if (i % 8 == g) row[i / 8] = __ffs(which) - 1;
+    float sum[CW / 8][4];
+#pragma unroll
+    for (int n = 0; n < CW / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[n][i] = 0.f;
+    for (int h = 2 * block0; h < 2 * (block0 + blocks); ++h) {   // half a block
+      const int64_t x = int64_t(h) * (kBK / 2) + t * 16;
+      const auto piece = [&](const uint8_t* m, int64_t at, bool there) {
+        return there && x < width ? *reinterpret_cast<const uint4*>(m + at * width + x) : make_uint4(0u, 0u, 0u, 0u);
+      };
+      const uint4 v0 = piece(p.a, int64_t(row0) + row[0], row[0] < rows), v1 = piece(p.a, int64_t(row0) + row[1], row[1] < rows);
+      const float sa[2] = {a_scale(row[0], h / 2), a_scale(row[1], h / 2)};
+      uint32_t a[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        codes_f16(i == 0 ? v0.x : i == 1 ? v0.y : i == 2 ? v0.z : v0.w, a[i][0], a[i][2]);
+        codes_f16(i == 0 ? v1.x : i == 1 ? v1.y : i == 2 ? v1.z : v1.w, a[i][1], a[i][3]);
       }
-      const int64_t at = (to + r) * p.C + col0 + c;
-      if constexpr (BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(float(sum));
-      else static_cast<float*>(p.out)[at] = float(sum);
+#pragma unroll
+      for (int n = 0; n < CW / 8; ++n) {
+        const bool there = n * 8 < cols;                         // cols is a multiple of 16
+        const uint4 v = piece(p.b, b_row0 + n * 8 + g, there);
+        float dot[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t b0, b1;
+          codes_f16(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w, b0, b1);
+          mma_f16(dot, a[i][0], a[i][1], a[i][2], a[i][3], b0, b1);
+        }
+        float2 sb;
+        if constexpr (WGRAD) sb = there ? *reinterpret_cast<const float2*>(b_scales + int64_t(h / 2) * p.C + n * 8 + 2 * t) : make_float2(0.f, 0.f);
+        else sb.x = sb.y = b_scales[h / 2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 s = apart(sa[i / 2], i % 2 == 0 ? sb.x : sb.y);
+          sum[n][i] = fmaf(dot[i] * s.x, s.y, sum[n][i]);
+        }
+      }
     }
+#pragma unroll
+    for (int n = 0; n < CW / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (row[i] >= rows || n * 8 >= cols) continue;
+        const int64_t at = (to + row[i]) * p.C + col0 + n * 8 + 2 * t;
+        const float u = sum[n][2 * i], v = sum[n][2 * i + 1];
+        if constexpr (BF16) *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at) = __floats2bfloat162_rn(u, v);
+        else *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = make_float2(u, v);
+      }
+  }
+}
+
+// The warp's parts of the CTA's tiles.  Out of line, once, so that it takes no registers from the loop.
+template <int BN, bool WGRAD, bool BF16>
+__device__ __noinline__ void redo_tiles(const MatmulParams& p, const Shared<WGRAD>& sh, int n_tiles) {
+  constexpr int CW = BN / 4;
+  const int warp = threadIdx.x / kWarp, first = warp % 4 * 32;
+  Walk w;
+  for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
+    w.at<BN, WGRAD>(p, sh, tile);
+    const int col = w.col0 + (warp - kFirstEpi) / 4 * CW;
+    if (first < w.rows && col < p.C)
+      redo_rows<CW, WGRAD, BF16>(p, w.e, w.row0 + first, min(32, w.rows - first), col, min(CW, p.C - col), w.block0, w.blocks,
+                                 (WGRAD ? int64_t(w.e) * p.R : 0) + w.row0 + first);
   }
 }
 
@@ -539,17 +601,19 @@ expert_matmul_kernel(const __grid_constant__ MatmulParams p, const __grid_consta
         mbar_wait(&sh.drain, 0, p.timeout_ns);
       }
     } else if (WGRAD && warp == 2) {
-      // ---- the scales of the tiles' rows, from global memory: the epilogue has no time for
-      // a look at them (219 -> 227 us) ----
+      // ---- the scales of the tiles' rows, from global memory: a look at them in the
+      // epilogue costs it 227 us instead of 220.  (In the product it is the epilogue's that
+      // is free, and this one's that costs: 525 us instead of 515.) ----
       bool plain = true;
       Walk w;
       for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
         w.at<BN, WGRAD>(p, sh, tile);
-        for (int b = 0; b < w.blocks; ++b)
-          if (lane * 4 < w.rows) {                               // R is a multiple of 16, the array 16-byte aligned
-            const float4 v = *reinterpret_cast<const float4*>(p.a_scale + int64_t(w.block0 + b) * p.R + w.r0 + lane * 4);
-            plain = plain && plain_scale<true>(v.x) && plain_scale<true>(v.y) && plain_scale<true>(v.z) && plain_scale<true>(v.w);
-          }
+        if (lane * 4 >= w.rows) continue;                        // R is a multiple of 16, the array 16-byte aligned
+        const float* s = p.a_scale + int64_t(w.block0) * p.R + w.r0 + lane * 4;
+        for (int b = 0; b < w.blocks; ++b, s += p.R) {
+          const float4 v = *reinterpret_cast<const float4*>(s);
+          plain = plain && plain_pair<true>(v.x, 1.f) && plain_pair<true>(v.y, 1.f) && plain_pair<true>(v.z, 1.f) && plain_pair<true>(v.w, 1.f);
+        }
       }
       if (!plain) sh.redo = 1;
       __syncwarp();
@@ -748,16 +812,7 @@ expert_matmul_kernel(const __grid_constant__ MatmulParams p, const __grid_consta
       plain = sh.redo == 0;
     }
     __syncwarp();
-    if (ok && !__all_sync(kFull, plain)) {                       // the warp's parts of its tiles once more
-      Walk r;
-      for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
-        r.at<BN, WGRAD>(p, sh, tile);
-        const int first = quad * 32, col = r.col0 + cg * CW;
-        if (first < r.rows && col < p.C)
-          redo_rows<WGRAD, BF16>(p, r.e, r.row0 + first, min(32, r.rows - first), col, min(CW, p.C - col), r.block0, r.blocks,
-                                 (WGRAD ? int64_t(r.e) * p.R : 0) + r.row0 + first);
-      }
-    }
+    if (ok && !__all_sync(kFull, plain)) redo_tiles<BN, WGRAD, BF16>(p, sh, n_tiles);
   }
   __syncwarp();                                                  // the roles' single threads are back
   tc_fence_before();

@@ -621,3 +621,51 @@ def test_measured_calls_against_their_plain_and_exact_forms(mr, monkeypatch, cas
             else:
                 step = 2.0 ** -8 if side.dtype == torch.bfloat16 else 0.0
                 assert ((v - w).abs() <= step * w.abs() + 1e-5 * w.abs().max()).all(), name
+
+
+@pytest.mark.parametrize("share", [0.02, 0.4, 0.6, 1.0])
+@pytest.mark.parametrize("M,K,N", [(75, 208, 48), (517, 1040, 272), (333, 16, 16)])
+def test_few_and_many_rows_of_extreme_scales(mr, M, K, N, share):
+    """One row of a tile, more than half of its rows and all of them: those have scales whose product
+    fp32 holds no digits of, the others keep the bits that they have alone."""
+    g = torch.Generator().manual_seed(M)
+    blocks = -(-K // 128)
+    for dtype in (torch.bfloat16, torch.float32):
+        q, scale, wq, wscale = operands(M, K, 1, N, M)
+        wscale *= 2.0 ** -40
+        base = mr.moe_expert_matmul(q, scale, wq, wscale, out_dtype=dtype)
+        far = torch.rand(M, generator=g) < share
+        far[M // 2] = True
+        at = far.nonzero()[:, 0].cuda()
+        scale[:, at] *= 2.0 ** -95
+        scale[0, at[::2]] = 0
+        got = mr.moe_expert_matmul(q, scale, wq, wscale, out_dtype=dtype)
+        want, size = ref.matmul(wide(q), wide(scale), wide(wq), wide(wscale), [(0, M)])
+        u = ref.U16 if dtype == torch.bfloat16 else 0.0
+        tiny = blocks * TINY * 2 + (2.0 ** -134 if u else 0.0)
+        ref.assert_near("out", wide(got), want, (256 + 3 * blocks) * ref.U32 * size * (1 + u) + u * np.abs(want) + tiny)
+        assert torch.equal(got[~far.cuda()], base[~far.cuda()])
+        few = M - 20                                              # rows behind the kept ones stay
+        out = torch.full_like(got, 7.0)
+        mr.moe_expert_matmul(q, scale, wq, wscale, i32([0, M]), i32([few]), out=out)
+        assert torch.equal(out[:few], got[:few]) and (out[few:] == 7).all()
+
+
+@pytest.mark.parametrize("share", [0.02, 0.6, 1.0])
+def test_few_and_many_rows_of_extreme_scales_of_a_weight_gradient(mr, share):
+    g = torch.Generator().manual_seed(7)
+    N, K, counts = 304, 336, [150, 1, 0, 400]
+    rows = ref.expert_rows(np.concatenate([[0], np.cumsum(counts)]), None, sum(counts))
+    width = mr.moe_quantize_cols_width(sum(counts), len(counts))
+    dq, xq = ((torch.randn(n, width, generator=g) * 3).to(F8).cuda() for n in (N, K))
+    ds, xs = (torch.exp(torch.randn(width // 128, n, generator=g)).cuda() for n in (N, K))
+    base = mr.moe_expert_wgrad(dq, ds, xq, xs, i32(counts))
+    far = torch.rand(N, generator=g) < share
+    far[100] = True
+    at = far.nonzero()[:, 0].cuda()
+    ds[:, at] *= 2.0 ** -143                                      # a few bits of the scale and fewer of a product
+    xs2 = xs * 2.0 ** 90
+    got = mr.moe_expert_wgrad(dq, ds, xq, xs2, i32(counts))
+    want, size = ref.wgrad(wide(dq), wide(ds), wide(xq), wide(xs2), rows)
+    ref.assert_near("dw", wide(got), want, (256 + 3 * 4) * ref.U32 * size + 8 * TINY)
+    assert torch.equal(mr.moe_expert_wgrad(dq, ds, xq, xs, i32(counts))[:, ~far.cuda()], base[:, ~far.cuda()])
