@@ -563,16 +563,16 @@ route_fwd_kernel(const __grid_constant__ RouteParams p, const int per) {
         }
         const bool kept = open && rank < p.keep;
         if (MODE != 0 && (has_bias || p.top2)) {
-          // A score is the true one within tol / 2 for each of its values and three roundings
-          // of 2^-24 of their sizes: where the bias was added, where the two were (which can
-          // be far larger than their sum) and in the two lines below.  A masked group's is
-          // exact; where the sizes pass fp32 nothing is known.
+          // A score is the true one within tol / 2 for each of its values and two roundings of
+          // 2^-24 of their sizes: where the bias was added, and where the two were, which can
+          // be far larger than their sum.  (The lines below round outwards.)  A masked group's
+          // is exact; where the sizes pass fp32 nothing is known.
           if (!p.top2) size = score > neg_inf() ? fabsf(score) : 0.f;
-          const float e = 1.8e-7f * size;
+          const float e = 1.2e-7f * size;
           const bool known = e < __uint_as_float(0x7f800000u);
-          const float least = known ? score - e : neg_inf(), most = known ? score + e : -neg_inf();
+          const float least = known ? __fsub_rd(score, e) : neg_inf(), most = known ? __fadd_ru(score, e) : -neg_inf();
           const float lo = -row_max<LPR>(kept ? -least : none()), hi = row_max<LPR>(kept ? none() : most);
-          hangs = lo - hi <= (p.top2 ? 2.f * tol : tol);
+          hangs = __fsub_rd(lo, hi) <= (p.top2 ? 2.f * tol : tol);
         }
         open = kept;
         const unsigned lanes = __ballot_sync(kFull, kept);
