@@ -10,8 +10,11 @@
 // sums are fp32 in the order of j, and there are no atomics: repeated calls give
 // the same bits.  W warps work on a token; many tokens take one warp each (its
 // index loads and row loads overlap with the other warps' of the SM), few tokens
-// take up to eight.  16,384 x 6 rows of 2048 bf16: 74 us and 133 us backward, 6.4
-// and 6.5 TB/s.
+// take up to eight.  16,384 x 6 rows of 2048 bf16, none dropped: 74 us and 133 us
+// backward, 6.3 and 6.6 TB/s; an eighth dropped: 69 and 121 us, 6.1 and 6.4 TB/s of
+// the rows kept.  Rows that are not whole pieces of 16 bytes take an element a load:
+// of 2044 to 2047 bf16 170 and 308 us, of 2046 and 2047 fp32 197 and 405 us (2048: 145
+// and 265).
 #include "device_common.cuh"
 #include "expert_combine.h"
 

@@ -8,8 +8,8 @@
 // fewer than 32 bits.
 //
 // One persistent CTA per SM, 20 warps: a TMA producer (one thread), an MMA
-// issuer (one thread), two spare warps, and 16 epilogue warps of 32 rows by a
-// quarter of the tile's columns.  Shared memory is a ring of operand stages (one block
+// issuer (one thread), a warp that looks at the rows' scales (weight gradient), a spare
+// one, and 16 epilogue warps of 32 rows by a quarter of the tile's columns.  Shared memory is a ring of operand stages (one block
 // of 128 of both operands, 128-byte swizzled); tensor memory is a ring of block
 // products, so that the tensor core forms block b + 1 while the epilogue adds
 // block b, and runs ahead into the next tile while a tile is stored.
