@@ -12,6 +12,11 @@
  *                                   the experts' matrix products on such values,
  *                                   and their weight gradient
  *   moe_expert_combine / _bwd       the experts' rows summed by gate, and its gradient
+ *   moe_quantize_fp4 / moe_dequantize_fp4
+ *                                   4-bit values with one scale for a block of 32
+ *   moe_expert_matmul_fp4           the experts' matrix products on such values
+ *   moe_expert_glu / _bwd           the gated activation between the two products,
+ *                                   also quantised as it leaves, and its gradient
  *
  * A layer's forward: moe_route_fwd, moe_dispatch (moe_router.h), then
  * moe_quantize_rows with the dispatch's perm, moe_expert_matmul, the caller's
@@ -180,8 +185,8 @@ MOE_API moe_status moe_expert_wgrad(const void* dyq, const float* dyscale, const
                                     int64_t width, int32_t N, int32_t K, int32_t E, const int32_t* kept, float* dw,
                                     moe_stream_t stream);
 
-/* Reads and clears the error bits that moe_expert_matmul and moe_expert_wgrad
- * calls have left on the current device (synchronises `stream`, on which they
+/* Reads and clears the error bits that moe_expert_matmul, moe_expert_wgrad and
+ * moe_expert_matmul_fp4 calls have left on the current device (synchronises `stream`, on which they
  * were queued).  *flags = 0 when every wait completed; otherwise returns
  * MOE_ERR_TIMEOUT with bit 2 set: a wait of a kernel's pipeline expired and its
  * output is incomplete.  Bits are read and cleared in one step: each is given to one
@@ -211,6 +216,75 @@ MOE_API moe_status moe_expert_combine_bwd(const void* dout, const void* y, moe_d
                                           int32_t k, int32_t E, const int32_t* idx, const int32_t* slot,
                                           const int32_t* offsets, const float* gate, void* dy, float* dgate,
                                           moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 4-bit values with one scale for a block of 32                            */
+/* ------------------------------------------------------------------------ */
+
+/* Values that share a scale, along the contraction. */
+#define MOE_FP4_BLOCK 32
+
+/* A code has a sign (bit 3) and one of the sizes 0, 1/2, 1, 3/2, 2, 3, 4, 6; two
+ * codes lie in a byte, the even column's in the low four bits.  A block's scale is
+ * the power of two s with 3 < max|x| / s <= 6 (at least 2^-126; 1 for a block of
+ * zeros), held as a byte n that stands for 2^(n - 127); its codes are x / s rounded
+ * to nearest, ties to even.  A block with an infinity or a NaN gets n = 255, a NaN
+ * (its codes are unspecified), so that every product with it is NaN.
+ * x is fp32 or bf16 [rows,K].  q [M,K/2]: row r holds row perm[r] / k of x, or row r
+ * when perm is NULL (then M == rows); a perm entry outside [0, rows*k) gives a row of
+ * zeros.  scale [ceil(K/128), M, 4]: the bytes of the four blocks of 128 columns
+ * together, and the rows of one such column next to one another; bytes behind
+ * column K are 127.  Weights [E,N,K] are E*N rows.
+ * K is a multiple of 32 up to MOE_MAX_WIDTH; x and q are 16-byte aligned, scale is
+ * 4-byte aligned. */
+MOE_API moe_status moe_quantize_fp4(const void* x, moe_dtype dt, int64_t rows, int64_t M, int32_t K,
+                                    const int32_t* perm, int32_t k, void* q, void* scale, moe_stream_t stream);
+
+/* y[r,c] = code * 2^(n - 127), NaN where n = 255: exact in fp32 and bf16, but for sizes
+ * above their largest number, which give an infinity.  q [M,K/2] and scale as above, y [M,K]
+ * fp32 or bf16 (dt), 16-byte aligned as q is. */
+MOE_API moe_status moe_dequantize_fp4(const void* q, const void* scale, int64_t M, int32_t K, moe_dtype dt, void* y,
+                                      moe_stream_t stream);
+
+/* The product of moe_expert_matmul (rows, offsets, kept and out as there) on 4-bit
+ * operands:
+ *   q [M,K/2], scale [ceil(K/128), M, 4]: as moe_quantize_fp4 of the rows
+ *   wq [E,N,K/2], wscale [ceil(K/128), E, N, 4]: as moe_quantize_fp4 of E*N rows
+ * The tensor core multiplies a block's products by its two scales and adds them, over
+ * the whole contraction, in fp32 (where products below about 2^-25 of the largest that
+ * are added with them may be lost); the one rounding to bf16 is at the end.  A row's
+ * result does not depend on the other rows, and a row or column with a NaN scale is NaN.
+ * K is a multiple of 32, N of 16, both up to MOE_MAX_WIDTH; E * N < 2^31, M >= 1,
+ * M < 2^31; q, wq and out are 16-byte aligned, the scales 4-byte aligned.
+ * Needs no workspace.  A device wait that runs out is reported by
+ * moe_expert_device_status, and until that is read later products on the device write
+ * nothing. */
+MOE_API moe_status moe_expert_matmul_fp4(const void* q, const void* scale, int64_t M, int32_t K,
+                                         const void* wq, const void* wscale, int32_t E, int32_t N,
+                                         const int32_t* offsets, const int32_t* kept, moe_dtype out_dt, void* out,
+                                         moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The gated activation between the experts' products                       */
+/* ------------------------------------------------------------------------ */
+
+typedef enum { MOE_GLU_PLAIN = 0, MOE_GLU_E4M3 = 1, MOE_GLU_FP4 = 2 } moe_glu_form;
+
+/* y[r,i] = g * sigmoid(g) * u with g = h[r,i], u = h[r,I+i], of h [M,2I] (fp32 or bf16),
+ * in fp32.  It leaves as
+ *   MOE_GLU_PLAIN: out [M,I] in h's type (scale is NULL)
+ *   MOE_GLU_E4M3:  out [M,I] and scale [ceil(I/128), M] fp32, as moe_quantize_rows has them
+ *   MOE_GLU_FP4:   out [M,I/2] and scale [ceil(I/128), M, 4], as moe_quantize_fp4 has them
+ * (the blocks' scales are those of the fp32 values).  g = -infinity gives a NaN.
+ * I is a multiple of 16 (MOE_GLU_FP4: of 32) up to MOE_MAX_WIDTH; h and out are 16-byte
+ * aligned, scale is 4-byte aligned. */
+MOE_API moe_status moe_expert_glu(const void* h, moe_dtype dt, int64_t M, int32_t I, moe_glu_form form, void* out,
+                                  void* scale, moe_stream_t stream);
+
+/* Its gradient, with s = sigmoid(g): dh[r,i] = dy u s (1 + g (1 - s)), dh[r,I+i] = dy g s.
+ * dy [M,I] and dh [M,2I] have h's type and are 16-byte aligned. */
+MOE_API moe_status moe_expert_glu_bwd(const void* h, const void* dy, moe_dtype dt, int64_t M, int32_t I, void* dh,
+                                      moe_stream_t stream);
 
 #ifdef __cplusplus
 }

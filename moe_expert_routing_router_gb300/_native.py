@@ -73,6 +73,11 @@ EXPERT_SIGNATURES = {
     "moe_expert_device_status": (_i32, [_p, C.POINTER(_i32)]),
     "moe_expert_combine": (_i32, [_p, _i32, _i64, _i32, _i64, _i32, _i32, _p, _p, _p, _p, _p, _p]),
     "moe_expert_combine_bwd": (_i32, [_p, _p, _i32, _i64, _i32, _i64, _i32, _i32, _p, _p, _p, _p, _p, _p, _p]),
+    "moe_quantize_fp4": (_i32, [_p, _i32, _i64, _i64, _i32, _p, _i32, _p, _p, _p]),
+    "moe_dequantize_fp4": (_i32, [_p, _p, _i64, _i32, _i32, _p, _p]),
+    "moe_expert_matmul_fp4": (_i32, [_p, _p, _i64, _i32, _p, _p, _i32, _i32, _p, _p, _i32, _p, _p]),
+    "moe_expert_glu": (_i32, [_p, _i32, _i64, _i32, _i32, _p, _p, _p]),
+    "moe_expert_glu_bwd": (_i32, [_p, _p, _i32, _i64, _i32, _p, _p]),
 }
 
 _lock = threading.Lock()

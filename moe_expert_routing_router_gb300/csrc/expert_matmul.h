@@ -32,6 +32,8 @@ struct MatmulParams {
 
 // `error` receives a message when the result is cudaErrorUnknown (tensor map).
 cudaError_t launch_expert_matmul(const MatmulParams& p, int sms, const char** error, cudaStream_t stream);
+// The current device's error bits, which every product's kernel reads and sets.
+cudaError_t expert_error_word(int** word);
 // Reads and clears the current device's error bits (synchronises the stream).
 cudaError_t expert_matmul_errors(int* bits, cudaStream_t stream);
 

@@ -8,9 +8,12 @@
 
 #include "abi_common.h"
 #include "expert_combine.h"
+#include "expert_glu.h"
 #include "expert_matmul.h"
+#include "expert_matmul_fp4.h"
 #include "moe_experts.h"
 #include "quantize.h"
+#include "quantize_fp4.h"
 #include "route.h"
 
 namespace {
@@ -55,6 +58,13 @@ moe_status check_experts(int32_t E) {
 moe_status check_width(const char* name, int64_t n) {
   if (n < 16 || n > MOE_MAX_WIDTH || n % 16 != 0)
     return fail(MOE_ERR_INVALID, "%s = %lld must be a multiple of 16 in [16, %d]", name, (long long)n, MOE_MAX_WIDTH);
+  return MOE_OK;
+}
+
+// One whose values lie two in a byte.
+moe_status check_fp4_width(const char* name, int64_t n) {
+  if (n < MOE_FP4_BLOCK || n > MOE_MAX_WIDTH || n % MOE_FP4_BLOCK != 0)
+    return fail(MOE_ERR_INVALID, "%s = %lld must be a multiple of %d in [%d, %d]", name, (long long)n, MOE_FP4_BLOCK, MOE_FP4_BLOCK, MOE_MAX_WIDTH);
   return MOE_OK;
 }
 
@@ -308,6 +318,90 @@ moe_status moe_expert_combine_bwd(const void* dout, const void* y, moe_dtype dt,
   if ((s = moe::abi_sms(&sms)) != MOE_OK) return s;
   moe::CombineRowsBwdParams p = {dout, y, T, M, H, k, E, idx, slot, offsets, gate, dy, dgate};
   return launched(moe::launch_expert_combine_bwd(p, dt == MOE_DTYPE_BF16, sms, stream), "moe_expert_combine_bwd launch");
+}
+
+moe_status moe_quantize_fp4(const void* x, moe_dtype dt, int64_t rows, int64_t M, int32_t K,
+                            const int32_t* perm, int32_t k, void* q, void* scale, moe_stream_t stream) {
+  moe_status s;
+  if ((s = check_dtype(dt)) != MOE_OK || (s = check_gather(rows, M, perm, k)) != MOE_OK || (s = check_fp4_width("K", K)) != MOE_OK) return s;
+  if (!x || !q || !scale) return fail(MOE_ERR_INVALID, "an argument is NULL");
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return fail(MOE_ERR_INVALID, "x or q (16 bytes) or scale (4 bytes) is misaligned");
+  moe::QuantFp4Params p = {x, rows, M, K, k, perm, static_cast<uint8_t*>(q), static_cast<uint32_t*>(scale)};
+  return launched(moe::launch_quantize_fp4(p, dt == MOE_DTYPE_BF16, stream), "moe_quantize_fp4 launch");
+}
+
+moe_status moe_dequantize_fp4(const void* q, const void* scale, int64_t M, int32_t K, moe_dtype dt, void* y, moe_stream_t stream) {
+  moe_status s;
+  if ((s = check_dtype(dt)) != MOE_OK || (s = check_rows("M", M)) != MOE_OK || (s = check_fp4_width("K", K)) != MOE_OK) return s;
+  if (!q || !scale || !y) return fail(MOE_ERR_INVALID, "an argument is NULL");
+  if (!aligned(q, 16) || !aligned(y, 16) || !aligned(scale, 4)) return fail(MOE_ERR_INVALID, "q or y (16 bytes) or scale (4 bytes) is misaligned");
+  moe::DequantFp4Params p = {static_cast<const uint8_t*>(q), static_cast<const uint32_t*>(scale), M, K, y};
+  return launched(moe::launch_dequantize_fp4(p, dt == MOE_DTYPE_BF16, stream), "moe_dequantize_fp4 launch");
+}
+
+moe_status moe_expert_matmul_fp4(const void* q, const void* scale, int64_t M, int32_t K,
+                                 const void* wq, const void* wscale, int32_t E, int32_t N,
+                                 const int32_t* offsets, const int32_t* kept, moe_dtype out_dt, void* out,
+                                 moe_stream_t stream) {
+  moe_status s;
+  if ((s = check_dtype(out_dt)) != MOE_OK || (s = check_rows("M", M)) != MOE_OK || (s = check_experts(E)) != MOE_OK ||
+      (s = check_width("N", N)) != MOE_OK || (s = check_fp4_width("K", K)) != MOE_OK)
+    return s;
+  if (!q || !scale || !wq || !wscale || !out) return fail(MOE_ERR_INVALID, "an argument is NULL");
+  if (offsets == nullptr && (E != 1 || kept != nullptr)) return fail(MOE_ERR_INVALID, "without offsets there is one expert and no kept");
+  if (int64_t(E) * N >= kInt32Limit) return fail(MOE_ERR_INVALID, "E*N = %lld does not fit int32", (long long)E * N);
+  if (!aligned(q, 16) || !aligned(wq, 16) || !aligned(out, 16)) return fail(MOE_ERR_INVALID, "q, wq or out is not 16-byte aligned");
+  if (!aligned(scale, 4) || !aligned(wscale, 4) || !aligned(offsets, 4) || !aligned(kept, 4))
+    return fail(MOE_ERR_INVALID, "an array is not 4-byte aligned");
+  // the tiles of the launch are counted in int32
+  if ((M / 128 + E) * ((N + 127) / 128) >= kInt32Limit)
+    return fail(MOE_ERR_INVALID, "M = %lld by N = %d is too large", (long long)M, N);
+  int sms = 0;
+  if ((s = moe::abi_sms(&sms)) != MOE_OK) return s;
+  moe::MatmulFp4Params p = {};
+  p.M = M;
+  p.C = N;
+  p.K = K;
+  p.E = E;
+  p.a = static_cast<const uint8_t*>(q);
+  p.a_scale = static_cast<const uint32_t*>(scale);
+  p.b = static_cast<const uint8_t*>(wq);
+  p.b_scale = static_cast<const uint32_t*>(wscale);
+  p.offsets = offsets;
+  p.kept = kept;
+  p.out_bf16 = out_dt == MOE_DTYPE_BF16;
+  p.out = out;
+  p.timeout_ns = moe::abi_wait_ns();
+  p.extra = moe::abi_barrier_extra();
+  cudaError_t e = moe::expert_error_word(&p.errors);
+  if (e != cudaSuccess) return launched(e, "moe_expert_matmul_fp4 error word");
+  const char* error = nullptr;
+  e = moe::launch_expert_matmul_fp4(p, sms, &error, stream);
+  return error ? fail(MOE_ERR_CUDA, "moe_expert_matmul_fp4: %s", error) : launched(e, "moe_expert_matmul_fp4 launch");
+}
+
+moe_status moe_expert_glu(const void* h, moe_dtype dt, int64_t M, int32_t I, moe_glu_form form, void* out, void* scale, moe_stream_t stream) {
+  moe_status s;
+  if (form != MOE_GLU_PLAIN && form != MOE_GLU_E4M3 && form != MOE_GLU_FP4) return fail(MOE_ERR_INVALID, "form = %d is not 0, 1 or 2", int(form));
+  if ((s = check_dtype(dt)) != MOE_OK || (s = check_rows("M", M)) != MOE_OK ||
+      (s = form == MOE_GLU_FP4 ? check_fp4_width("I", I) : check_width("I", I)) != MOE_OK)
+    return s;
+  if (!h || !out) return fail(MOE_ERR_INVALID, "an argument is NULL");
+  if ((scale != nullptr) != (form != MOE_GLU_PLAIN)) return fail(MOE_ERR_INVALID, "codes have scales, plain values none");
+  if (!aligned(h, 16) || !aligned(out, 16) || !aligned(scale, 4)) return fail(MOE_ERR_INVALID, "h or out (16 bytes) or scale (4 bytes) is misaligned");
+  if (M * (I / 8) >= kInt32Limit * 256) return fail(MOE_ERR_INVALID, "M = %lld by I = %d is too large", (long long)M, I);
+  moe::GluParams p = {h, M, I, int(form), out, scale};
+  return launched(moe::launch_expert_glu(p, dt == MOE_DTYPE_BF16, stream), "moe_expert_glu launch");
+}
+
+moe_status moe_expert_glu_bwd(const void* h, const void* dy, moe_dtype dt, int64_t M, int32_t I, void* dh, moe_stream_t stream) {
+  moe_status s;
+  if ((s = check_dtype(dt)) != MOE_OK || (s = check_rows("M", M)) != MOE_OK || (s = check_width("I", I)) != MOE_OK) return s;
+  if (!h || !dy || !dh) return fail(MOE_ERR_INVALID, "an argument is NULL");
+  if (!aligned(h, 16) || !aligned(dy, 16) || !aligned(dh, 16)) return fail(MOE_ERR_INVALID, "h, dy or dh is not 16-byte aligned");
+  if (M * (I / 8) >= kInt32Limit * 256) return fail(MOE_ERR_INVALID, "M = %lld by I = %d is too large", (long long)M, I);
+  moe::GluBwdParams p = {h, dy, M, I, dh};
+  return launched(moe::launch_expert_glu_bwd(p, dt == MOE_DTYPE_BF16, stream), "moe_expert_glu_bwd launch");
 }
 
 }  // extern "C"

@@ -8,109 +8,13 @@
 //
 // All three kernels are bound by memory: every value is read once, held in
 // registers while its block's maximum is found, and written once as a byte.
-#include "device_common.cuh"
+#include "block_values.cuh"
 #include "quantize.h"
 
 #include <cuda_bf16.h>
 
 namespace moe {
 namespace {
-
-constexpr unsigned kFull = 0xffffffffu;
-
-// The block's scale and its inverse, from the bits of max|x|.
-struct Pow2Scale {
-  float scale, inv;
-};
-__device__ __forceinline__ Pow2Scale pow2_scale(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  // amax = m * 2^x, 1 <= m < 2: 448 = 1.75 * 2^8, so the exponent is x - 8, one more where
-  // m > 1.75 (the addition carries), and at least -126 (a subnormal amax has it).
-  const int n = max(int((b + 0x1fffffu) >> 23) - 8, 1);          // biased; 2^-126 .. 2^120
-  Pow2Scale s = {__uint_as_float(uint32_t(n) << 23), __uint_as_float(uint32_t(254 - n) << 23)};
-  if (b == 0u) s = {1.f, 1.f};
-  if (b >= 0x7f800000u) s = {__uint_as_float(0x7fc00000u), 0.f};
-  return s;
-}
-
-__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return uint32_t(lo) | uint32_t(hi) << 16;
-}
-
-__device__ __forceinline__ uint32_t scaled4(float2 x, float2 y, float inv) {
-  x = mul2(x, make_float2(inv, inv));
-  y = mul2(y, make_float2(inv, inv));
-  return pack4(x.x, x.y, y.x, y.y);
-}
-
-// N neighbouring values, kept as they were loaded (bf16: two in a register).
-template <bool BF16, int N>
-struct Values {
-  static constexpr int kWords = BF16 ? N / 2 : N;
-  uint32_t w[kWords];
-
-  __device__ __forceinline__ void load(const void* x, int64_t at) {
-    const uint32_t* s = reinterpret_cast<const uint32_t*>(static_cast<const char*>(x) + at * (BF16 ? 2 : 4));
-    if constexpr (kWords % 4 == 0) {
-#pragma unroll
-      for (int i = 0; i < kWords; i += 4) {
-        const uint4 u = *reinterpret_cast<const uint4*>(s + i);
-        w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kWords; i += 2) {
-        const uint2 u = *reinterpret_cast<const uint2*>(s + i);
-        w[i] = u.x; w[i + 1] = u.y;
-      }
-    }
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0u;
-  }
-  __device__ __forceinline__ float get(int i) const {
-    if constexpr (BF16) return __uint_as_float(i % 2 == 0 ? w[i / 2] << 16 : w[i / 2] & 0xffff0000u);
-    else return __uint_as_float(w[i]);
-  }
-  // Larger |x|, word by word (bf16: half by half), a NaN above every number.  Signs are
-  // whatever they are.
-  __device__ __forceinline__ static uint32_t larger(uint32_t a, uint32_t b) {
-    uint32_t m;
-    if constexpr (BF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
-    else asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(*reinterpret_cast<float*>(&m)) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
-    return m;
-  }
-  // |x| of the larger half (bf16), or of the word; of one half.
-  __device__ __forceinline__ static float size(uint32_t m) {
-    if constexpr (BF16) return __uint_as_float(max(m << 16 & 0x7fffffffu, m & 0x7fff0000u));
-    else return __uint_as_float(m & 0x7fffffffu);
-  }
-  __device__ __forceinline__ static float size(uint32_t m, int half) {
-    return __uint_as_float((half == 0 ? m << 16 : m) & (BF16 ? 0x7fff0000u : 0x7fffffffu));
-  }
-  __device__ __forceinline__ uint32_t largest() const {
-    uint32_t m = w[0];
-#pragma unroll
-    for (int i = 1; i < kWords; ++i) m = larger(m, w[i]);
-    return m;
-  }
-  // Four neighbouring values from the i-th on, scaled and rounded.
-  __device__ __forceinline__ uint32_t codes(int i, float inv) const {
-    return scaled4(make_float2(get(i), get(i + 1)), make_float2(get(i + 2), get(i + 3)), inv);
-  }
-};
-
-// The row of x that row r of the output holds, or -1: zeros.  All rows fit int32.
-__device__ __forceinline__ int source_row(const int32_t* perm, int k, int64_t r, int64_t rows) {
-  if (perm == nullptr) return int(r);
-  const int a = perm[r];
-  const uint32_t t = uint32_t(a) / uint32_t(k);
-  return a >= 0 && t < uint64_t(rows) ? int(t) : -1;
-}
 
 // ---------------------------------------------------------------------------
 // Rows: blocks of 1 x 128.  Eight lanes, a team, hold a block, 16 values each; a

@@ -1,0 +1,140 @@
+// Quantisation to 4 bits (e2m1: 0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives) with one
+// scale for a block of 32 values of a row, and the values of such blocks.
+//
+// The scale is the power of two s with 3 < max|x| / s <= 6: dividing by it is exact, no
+// value saturates, and each is rounded once (to nearest, ties to even: by at most a fifth
+// of itself, or a fourth of s).  It is held as its exponent, a byte; those of the four
+// blocks of 128 columns lie in one word, and the words of one block column one row after
+// another, as the tiles of a product read them.
+//
+// Both kernels are bound by memory and move every value once: a team of eight lanes
+// holds 128 values of a row, 16 each, so that a block is two neighbouring lanes'.
+#include "block_values.cuh"
+#include "quantize_fp4.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kLanes = 8, kVals = kScaleBlock / kLanes, kTeams = kWarp / kLanes;
+constexpr int kBlocks = 4;                    // columns of a CTA, in blocks of 128
+constexpr int kIter = 4;                      // rows of a lane, loaded together
+constexpr int kTileRows = kThreads / kWarp / kBlocks * kTeams * kIter;
+
+// Where a lane works: its block column, its first column, and its team's first row.
+struct Place {
+  int l, kb, col;
+  int64_t r0;
+  __device__ __forceinline__ Place() {
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+    l = lane % kLanes;
+    kb = blockIdx.y * kBlocks + warp % kBlocks;
+    col = kb * kScaleBlock + l * kVals;
+    r0 = int64_t(blockIdx.x) * kTileRows + warp / kBlocks * (kTeams * kIter) + lane / kLanes;
+  }
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(const QuantFp4Params p) {
+  using V = Values<BF16, kVals>;
+  const Place at;
+  if (at.kb * kScaleBlock >= p.K) return;
+  // Lane i of the team finds the source of its i-th row.
+  const int64_t mine = at.r0 + at.l % kIter * kTeams;
+  const int token = at.l < kIter && mine < p.M ? source_row(p.perm, p.k, mine, p.rows) : -1;
+  V v[kIter];
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const int t = __shfl_sync(kFull, token, i, kLanes);
+    if (t >= 0 && at.col < p.K) v[i].load(p.x, int64_t(t) * p.K + at.col);
+    else v[i].zero();
+  }
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    uint32_t m = v[i].largest();
+    m = V::larger(m, __shfl_xor_sync(kFull, m, 1));
+    const Fp4Scale s = fp4_scale(V::size(m));
+    const uint32_t word = fp4_scale_word(s.code, at.l);
+    const int64_t r = at.r0 + i * kTeams;
+    if (r >= p.M) continue;
+    if (at.l == i) p.scale[int64_t(at.kb) * p.M + r] = word;
+    if (at.col >= p.K) continue;
+    uint32_t c[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 inv = make_float2(s.inv, s.inv);
+      float2 f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = mul2(make_float2(v[i].get(8 * h + 2 * j), v[i].get(8 * h + 2 * j + 1)), inv);
+      c[h] = fp4_pack8(f[0], f[1], f[2], f[3]);
+    }
+    *reinterpret_cast<uint2*>(p.q + (r * p.K + at.col) / 2) = make_uint2(c[0], c[1]);
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) dequantize_fp4_kernel(const DequantFp4Params p) {
+  const Place at;
+  if (at.col >= p.K) return;
+  uint2 c[kIter];
+  uint32_t word[kIter];
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const int64_t r = at.r0 + i * kTeams;
+    if (r >= p.M) break;
+    c[i] = *reinterpret_cast<const uint2*>(p.q + (r * p.K + at.col) / 2);
+    word[i] = p.scale[int64_t(at.kb) * p.M + r];
+  }
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const int64_t r = at.r0 + i * kTeams;
+    if (r >= p.M) break;
+    const float s = fp4_scale_value(word[i] >> (at.l / 2 * 8) & 255u);
+    float2 f[kVals / 2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t u[4];
+      fp4_unpack8(h == 0 ? c[i].x : c[i].y, u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[4 * h + j] = mul2(__half22float2(*reinterpret_cast<const __half2*>(&u[j])), make_float2(s, s));
+    }
+    uint4* to = reinterpret_cast<uint4*>(static_cast<char*>(p.y) + (r * p.K + at.col) * (BF16 ? 2 : 4));
+    if constexpr (BF16) {                                        // exact: two digits and a power of two
+      uint32_t b[kVals / 2];
+#pragma unroll
+      for (int j = 0; j < kVals / 2; ++j) {
+        const __nv_bfloat162 q = __floats2bfloat162_rn(f[j].x, f[j].y);
+        b[j] = *reinterpret_cast<const uint32_t*>(&q);
+      }
+      to[0] = make_uint4(b[0], b[1], b[2], b[3]);
+      to[1] = make_uint4(b[4], b[5], b[6], b[7]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVals / 4; ++j)
+        to[j] = make_uint4(__float_as_uint(f[2 * j].x), __float_as_uint(f[2 * j].y), __float_as_uint(f[2 * j + 1].x), __float_as_uint(f[2 * j + 1].y));
+    }
+  }
+}
+
+dim3 tiles(int64_t M, int K) {
+  const int kb = (K + kScaleBlock - 1) / kScaleBlock;
+  return dim3(unsigned((M + kTileRows - 1) / kTileRows), unsigned((kb + kBlocks - 1) / kBlocks));
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_fp4(const QuantFp4Params& p, bool bf16, cudaStream_t stream) {
+  if (bf16) quantize_fp4_kernel<true><<<tiles(p.M, p.K), kThreads, 0, stream>>>(p);
+  else quantize_fp4_kernel<false><<<tiles(p.M, p.K), kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dequantize_fp4(const DequantFp4Params& p, bool bf16, cudaStream_t stream) {
+  if (bf16) dequantize_fp4_kernel<true><<<tiles(p.M, p.K), kThreads, 0, stream>>>(p);
+  else dequantize_fp4_kernel<false><<<tiles(p.M, p.K), kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace moe
