@@ -17,6 +17,8 @@
  *   moe_expert_matmul_fp4           the experts' matrix products on such values
  *   moe_expert_glu / _bwd           the gated activation between the two products,
  *                                   also quantised as it leaves, and its gradient
+ *   moe_layer_small                 all that follows the routing, for the few tokens of
+ *                                   a decode step, in two kernels
  *
  * A layer's forward: moe_route_fwd, moe_dispatch (moe_router.h), then
  * moe_quantize_rows with the dispatch's perm, moe_expert_matmul, the caller's
@@ -285,6 +287,38 @@ MOE_API moe_status moe_expert_glu(const void* h, moe_dtype dt, int64_t M, int32_
  * dy [M,I] and dh [M,2I] have h's type and are 16-byte aligned. */
 MOE_API moe_status moe_expert_glu_bwd(const void* h, const void* dy, moe_dtype dt, int64_t M, int32_t I, void* dh,
                                       moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The experts of a layer for few tokens                                    */
+/* ------------------------------------------------------------------------ */
+
+#define MOE_SMALL_TOKENS 64
+#define MOE_SMALL_WIDTH 16384
+typedef enum { MOE_WEIGHTS_E4M3 = 0, MOE_WEIGHTS_FP4 = 1 } moe_weight_kind;
+
+/* out[t,:] = sum_j gate[t,j] * W2_e glu(W1_e x[t,:]) with e = idx[t,j] and glu as in
+ * moe_expert_glu: what dispatch, the two products, the activation between them and the
+ * combine compute, without a capacity, for T <= MOE_SMALL_TOKENS tokens.  The weights are
+ * quantised, the tokens' values are not.
+ *   x [T,H], out [T,H] bf16; idx, gate [T,k] as moe_route_fwd gives them: an idx outside
+ *   [0,E) adds nothing, a token without any other gets zeros, an expert picked twice counts twice
+ *   w1 [E,2I,H]: the gates' I rows, then the other I; w2 [E,H,I]; each either
+ *     MOE_WEIGHTS_E4M3: q and scale as moe_quantize_weights gives them, or
+ *     MOE_WEIGHTS_FP4:  q and scale as moe_quantize_fp4 gives them
+ * Sums are fp32.  Of each 128 values of x that scales share, those below 2^-28 of the
+ * largest lose digits; the activations are rounded to 11 bits, relative to the larger of
+ * themselves and 2^-28 of the largest of their 128.  A token's result does not depend on the
+ * others, nor on T; repeated calls give the same bits.
+ * H and I are multiples of 16 (of 32 where a matrix of 4 bits has them as its row length)
+ * up to MOE_SMALL_WIDTH; x, out and the codes are 16-byte aligned, the scales, idx and
+ * gate 4-byte aligned.  work: moe_layer_small_work_size bytes, 16-byte aligned, of any
+ * content; calls that may run at the same time each take their own. */
+MOE_API size_t moe_layer_small_work_size(int64_t T, int32_t H, int32_t I, int32_t k);
+MOE_API moe_status moe_layer_small(const void* x, int64_t T, int32_t H, int32_t I, int32_t E, int32_t k,
+                                   const int32_t* idx, const float* gate,
+                                   moe_weight_kind kind1, const void* w1q, const void* w1scale,
+                                   moe_weight_kind kind2, const void* w2q, const void* w2scale,
+                                   void* out, void* work, size_t work_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

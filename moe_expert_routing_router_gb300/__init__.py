@@ -47,6 +47,7 @@ from .layer import (  # noqa: F401
     moe_expert_glu,
     moe_expert_glu_bwd,
     moe_expert_matmul_fp4,
+    moe_layer_small,
     moe_quantize_fp4,
 )
 
@@ -56,4 +57,5 @@ __all__ = [
     "moe_expert_combine", "moe_expert_combine_bwd", "moe_expert_device_status", "moe_expert_matmul", "moe_expert_wgrad",
     "moe_quantize_cols", "moe_quantize_cols_width", "moe_quantize_rows", "moe_quantize_weights", "moe_route_bwd",
     "moe_route_fwd", "moe_quantize_fp4", "moe_dequantize_fp4", "moe_expert_matmul_fp4", "moe_expert_glu", "moe_expert_glu_bwd",
+    "moe_layer_small",
 ]

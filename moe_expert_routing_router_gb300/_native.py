@@ -78,6 +78,8 @@ EXPERT_SIGNATURES = {
     "moe_expert_matmul_fp4": (_i32, [_p, _p, _i64, _i32, _p, _p, _i32, _i32, _p, _p, _i32, _p, _p]),
     "moe_expert_glu": (_i32, [_p, _i32, _i64, _i32, _i32, _p, _p, _p]),
     "moe_expert_glu_bwd": (_i32, [_p, _p, _i32, _i64, _i32, _p, _p]),
+    "moe_layer_small_work_size": (_sz, [_i64, _i32, _i32, _i32]),
+    "moe_layer_small": (_i32, [_p, _i64, _i32, _i32, _i32, _i32, _p, _p, _i32, _p, _p, _i32, _p, _p, _p, _p, _sz, _p]),
 }
 
 _lock = threading.Lock()

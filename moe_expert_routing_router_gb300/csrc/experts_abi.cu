@@ -5,12 +5,14 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <tuple>
 
 #include "abi_common.h"
 #include "expert_combine.h"
 #include "expert_glu.h"
 #include "expert_matmul.h"
 #include "expert_matmul_fp4.h"
+#include "layer_small.h"
 #include "moe_experts.h"
 #include "quantize.h"
 #include "quantize_fp4.h"
@@ -402,6 +404,50 @@ moe_status moe_expert_glu_bwd(const void* h, const void* dy, moe_dtype dt, int64
   if (M * (I / 8) >= kInt32Limit * 256) return fail(MOE_ERR_INVALID, "M = %lld by I = %d is too large", (long long)M, I);
   moe::GluBwdParams p = {h, dy, M, I, dh};
   return launched(moe::launch_expert_glu_bwd(p, dt == MOE_DTYPE_BF16, stream), "moe_expert_glu_bwd launch");
+}
+
+size_t moe_layer_small_work_size(int64_t T, int32_t H, int32_t I, int32_t k) {
+  if (T < 1 || T > MOE_SMALL_TOKENS || H < 16 || H > MOE_SMALL_WIDTH || I < 16 || I > MOE_SMALL_WIDTH || k < 1 || k > MOE_MAX_TOPK) return 0;
+  return moe::small_layer_work_size(int(T), H, I, k);
+}
+
+moe_status moe_layer_small(const void* x, int64_t T, int32_t H, int32_t I, int32_t E, int32_t k,
+                           const int32_t* idx, const float* gate,
+                           moe_weight_kind kind1, const void* w1q, const void* w1scale,
+                           moe_weight_kind kind2, const void* w2q, const void* w2scale,
+                           void* out, void* work, size_t work_bytes, moe_stream_t stream) {
+  static_assert(MOE_SMALL_TOKENS == moe::kSmallTokens && MOE_SMALL_WIDTH == moe::kSmallWidth, "limits of the call and of its kernels");
+  moe_status s;
+  if ((s = check_tokens(T, k)) != MOE_OK || (s = check_experts(E)) != MOE_OK) return s;
+  if (T > MOE_SMALL_TOKENS) return fail(MOE_ERR_INVALID, "T = %lld is more than the %d tokens of this call", (long long)T, MOE_SMALL_TOKENS);
+  for (const moe_weight_kind kind : {kind1, kind2})
+    if (kind != MOE_WEIGHTS_E4M3 && kind != MOE_WEIGHTS_FP4) return fail(MOE_ERR_INVALID, "a weight kind is %d, not 0 or 1", int(kind));
+  for (const auto& [name, n, fp4] : {std::tuple<const char*, int32_t, bool>{"H", H, kind1 == MOE_WEIGHTS_FP4}, {"I", I, kind2 == MOE_WEIGHTS_FP4}}) {
+    if ((s = fp4 ? check_fp4_width(name, n) : check_width(name, n)) != MOE_OK) return s;
+    if (n > MOE_SMALL_WIDTH) return fail(MOE_ERR_INVALID, "%s = %d is more than %d", name, n, MOE_SMALL_WIDTH);
+  }
+  if (!x || !idx || !gate || !w1q || !w1scale || !w2q || !w2scale || !out || !work) return fail(MOE_ERR_INVALID, "an argument is NULL");
+  if (!aligned(x, 16) || !aligned(w1q, 16) || !aligned(w2q, 16) || !aligned(out, 16)) return fail(MOE_ERR_INVALID, "x, out or a weight is not 16-byte aligned");
+  if (!aligned(idx, 4) || !aligned(gate, 4) || !aligned(w1scale, 4) || !aligned(w2scale, 4)) return fail(MOE_ERR_INVALID, "an array is not 4-byte aligned");
+  if (!aligned(work, 16)) return fail(MOE_ERR_INVALID, "work is not 16-byte aligned");
+  if (work_bytes < moe_layer_small_work_size(T, H, I, k))
+    return fail(MOE_ERR_WORKSPACE, "work holds %zu bytes of %zu", work_bytes, moe_layer_small_work_size(T, H, I, k));
+  int sms = 0;
+  if ((s = moe::abi_sms(&sms)) != MOE_OK) return s;
+  moe::SmallLayerParams p = {};
+  p.x = x;
+  p.T = int(T);
+  p.H = H;
+  p.I = I;
+  p.E = E;
+  p.k = k;
+  p.idx = idx;
+  p.gate = gate;
+  p.w1 = {kind1 == MOE_WEIGHTS_FP4, static_cast<const uint8_t*>(w1q), w1scale};
+  p.w2 = {kind2 == MOE_WEIGHTS_FP4, static_cast<const uint8_t*>(w2q), w2scale};
+  p.out = out;
+  moe::small_layer_work(p, work);
+  return launched(moe::launch_layer_small(p, sms, stream), "moe_layer_small launch");
 }
 
 }  // extern "C"

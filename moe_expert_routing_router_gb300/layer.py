@@ -1,5 +1,5 @@
 """Python binding of what include/moe_experts.h has around the experts' 8-bit operators: 4-bit quantisation, the experts'
-products on it, and the gated activation between two products.  Argument marshalling only, by the rules of ``experts``.
+products on it, the gated activation between two products, and the experts of a layer for few tokens.  Argument marshalling only, by the rules of ``experts``.
 """
 
 from __future__ import annotations
@@ -8,9 +8,9 @@ import torch
 
 from ._native import check, lib
 from .api import _DTYPES, _out, _ptr
-from .experts import _F8, _VALUES, _blocks, _choice, _entry, _gathered, _need, _need_dims, _stream
+from .experts import _F8, _I32, _VALUES, _blocks, _choice, _entry, _gathered, _need, _need_dims, _stream
 
-__all__ = ["moe_quantize_fp4", "moe_dequantize_fp4", "moe_expert_matmul_fp4", "moe_expert_glu", "moe_expert_glu_bwd"]
+__all__ = ["moe_quantize_fp4", "moe_dequantize_fp4", "moe_expert_matmul_fp4", "moe_expert_glu", "moe_expert_glu_bwd", "moe_layer_small"]
 
 _U8 = (torch.uint8,)                           # 4-bit codes, two in a byte, and their scales' exponents
 _GLU_FORMS = {"plain": 0, "e4m3": 1, "fp4": 2}
@@ -119,3 +119,44 @@ def moe_expert_glu_bwd(h: torch.Tensor, dy: torch.Tensor, out: torch.Tensor | No
     dh = _out({"out": out}, "out", (M, width), h.dtype, h.device)
     check(lib().moe_expert_glu_bwd(_ptr(h), _ptr(dy), _DTYPES[h.dtype], M, width // 2, _ptr(dh), _stream()), "moe_expert_glu_bwd")
     return dh
+
+
+def _weights(name: str, w: dict, E: int | None, N: int | None, K: int | None, at: int) -> tuple[int, int, int, int, torch.Tensor, torch.Tensor]:
+    """(kind, E, N, K, codes, scales) of quantised weights, whose sizes are as given where they are."""
+    if not isinstance(w, dict) or "q" not in w or "scale" not in w:
+        raise ValueError(f"{name} must be a dict of q and scale, as moe_quantize_weights or moe_quantize_fp4 give it")
+    q, scale = w["q"], w["scale"]
+    e, n, width = _need_dims(f"{name}['q']", q, 3, (_F8, torch.uint8), at)
+    fp4 = q.dtype is torch.uint8
+    k = 2 * width if fp4 else width
+    if (E is not None and e != E) or (N is not None and n != N) or (K is not None and k != K):
+        raise ValueError(f"{name} must hold weights {(E, N, K)}, got {(e, n, k)}")
+    if fp4:
+        _need(f"{name}['scale']", scale, at, torch.uint8, (_blocks(k), e, n, 4))
+    else:
+        _need(f"{name}['scale']", scale, at, torch.float32, (e, _blocks(n), _blocks(k)))
+    return int(fp4), e, n, k, q, scale
+
+
+@_entry
+def moe_layer_small(x: torch.Tensor, idx: torch.Tensor, gate: torch.Tensor, w1: dict, w2: dict, out: torch.Tensor | None = None,
+                    stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """out [T, H] bf16 = sum_j gate[t, j] * W2_e silu(G_e x_t) * (U_e x_t), e = idx[t, j], for up to 64 tokens x [T, H] bf16:
+    what follows moe_route_fwd in a layer, in two kernels.  w1 holds the weights [E, 2I, H] (G's rows, then U's) and w2
+    [E, H, I], each as moe_quantize_weights or moe_quantize_fp4 gives them; idx and gate are [T, k], and an idx outside
+    [0, E) adds nothing (C: moe_layer_small)."""
+    T, H = _need_dims("x", x, 2, (torch.bfloat16,))
+    at = x.get_device()
+    k = _need_dims("idx", idx, 2, _I32, at)[1]
+    _need("idx", idx, at, torch.int32, (T, k))
+    _need("gate", gate, at, torch.float32, (T, k))
+    kind1, E, N1, _, q1, s1 = _weights("w1", w1, None, None, H, at)
+    if N1 % 2 != 0:
+        raise ValueError(f"w1 must hold weights [E, 2I, H], got {N1} rows")
+    kind2, _, _, I, q2, s2 = _weights("w2", w2, E, H, N1 // 2, at)
+    o = _out({"out": out}, "out", (T, H), torch.bfloat16, x.device)
+    need = int(lib().moe_layer_small_work_size(T, H, I, k))
+    work = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+    check(lib().moe_layer_small(_ptr(x), T, H, I, E, k, _ptr(idx), _ptr(gate), kind1, _ptr(q1), _ptr(s1), kind2, _ptr(q2), _ptr(s2),
+                                _ptr(o), _ptr(work), need, _stream()), "moe_layer_small")
+    return o

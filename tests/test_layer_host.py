@@ -17,6 +17,7 @@ GOOD = {
     "moe_expert_matmul_fp4": [FAKE, FAKE, 64, 128, FAKE, FAKE, 8, 64, FAKE, FAKE, 1, FAKE, None],
     "moe_expert_glu": [FAKE, 1, 64, 128, 2, FAKE, FAKE, None],
     "moe_expert_glu_bwd": [FAKE, FAKE, 1, 64, 128, FAKE, None],
+    "moe_layer_small": [FAKE, 4, 128, 64, 8, 2, FAKE, FAKE, 1, FAKE, FAKE, 0, FAKE, FAKE, FAKE, FAKE, 1 << 20, None],
 }
 BAD = [("moe_quantize_fp4", p, v, w) for p, v, w in [
     (0, None, 1), (0, FAKE + 8, 1), (1, 3, 2), (2, 0, 1), (2, BIG, 1), (3, 0, 1), (3, BIG, 1), (4, 0, 1), (4, 16, 1), (4, 144, 1), (4, 1 << 21, 1),
@@ -32,6 +33,12 @@ BAD += [("moe_expert_glu", p, v, w) for p, v, w in [
     (5, FAKE + 8, 1), (6, None, 1), (6, FAKE + 2, 1)]]
 BAD += [("moe_expert_glu_bwd", p, v, w) for p, v, w in [
     (0, None, 1), (0, FAKE + 8, 1), (1, None, 1), (1, FAKE + 4, 1), (2, 2, 2), (3, 0, 1), (4, 8, 1), (4, 24, 1), (5, None, 1), (5, FAKE + 8, 1)]]
+
+BAD += [("moe_layer_small", p, v, w) for p, v, w in [
+    (0, None, 1), (0, FAKE + 8, 1), (1, 0, 1), (1, 65, 1), (1, BIG, 1), (2, 0, 1), (2, 112, 1), (2, 16416, 1), (3, 0, 1), (3, 24, 1), (3, 16400, 1), (4, 0, 1),
+    (4, 1025, 1), (5, 0, 1), (5, 9, 1), (6, None, 1), (6, FAKE + 2, 1), (7, None, 1), (7, FAKE + 1, 1), (8, 2, 1), (8, -1, 1), (9, None, 1), (9, FAKE + 8, 1),
+    (10, None, 1), (10, FAKE + 2, 1), (11, 3, 1), (12, None, 1), (12, FAKE + 4, 1), (13, None, 1), (13, FAKE + 1, 1), (14, None, 1), (14, FAKE + 2, 1),
+    (15, None, 1), (15, FAKE + 8, 1), (16, 0, 5), (16, 100, 5)]]
 
 
 @pytest.mark.parametrize("name,pos,value,status", BAD)
@@ -58,6 +65,13 @@ def test_refusals_of_combinations(native_lib):
     assert native_lib.moe_expert_glu(*a) == 1
 
 
+def test_small_layer_work_size(native_lib):
+    size = native_lib.moe_layer_small_work_size
+    assert size(4, 128, 64, 2) >= 4 * 2 * (128 + 64) * 4 and size(4, 128, 64, 2) % 256 == 0
+    for bad in ((0, 128, 64, 2), (65, 128, 64, 2), (4, 8, 64, 2), (4, 16400, 64, 2), (4, 128, 0, 2), (4, 128, 64, 0), (4, 128, 64, 9)):
+        assert size(*bad) == 0
+
+
 M, K = 8, 64
 u8 = torch.zeros(M, K // 2, dtype=torch.uint8)
 sc = torch.zeros(1, M, 4, dtype=torch.uint8)
@@ -67,6 +81,8 @@ HOST = {
     "moe_expert_matmul_fp4": lambda **a: mr.moe_expert_matmul_fp4(u8, sc, u8[None], sc[:, None], **a),
     "moe_expert_glu": lambda **a: mr.moe_expert_glu(torch.zeros(M, K), **a),
     "moe_expert_glu_bwd": lambda **a: mr.moe_expert_glu_bwd(torch.zeros(M, K), torch.zeros(M, K // 2), **a),
+    "moe_layer_small": lambda **a: mr.moe_layer_small(torch.zeros(M, K, dtype=torch.bfloat16), torch.zeros(M, 2, dtype=torch.int32), torch.zeros(M, 2),
+                                                      {"q": u8[None], "scale": sc[:, None]}, {"q": u8[None], "scale": sc[:, None]}, **a),
 }
 
 
@@ -82,6 +98,13 @@ def test_host_tensors_are_refused_before_the_library(name, monkeypatch):
     monkeypatch.setattr(layer, "lib", reached)
     with pytest.raises(ValueError, match="CUDA tensor"):
         HOST[name]()
+
+
+def test_perf_cases_make_public_calls():
+    import re
+    from pathlib import Path
+    text = (Path(__file__).resolve().parents[1] / "perf" / "more_operators.py").read_text()
+    assert set(re.findall(r"\bmr\.(\w+)\(", text)) <= set(mr.__all__)
 
 
 # -- the reference forms against independent ones ----------------------------------------
