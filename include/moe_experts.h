@@ -305,10 +305,12 @@ typedef enum { MOE_WEIGHTS_E4M3 = 0, MOE_WEIGHTS_FP4 = 1 } moe_weight_kind;
  *   w1 [E,2I,H]: the gates' I rows, then the other I; w2 [E,H,I]; each either
  *     MOE_WEIGHTS_E4M3: q and scale as moe_quantize_weights gives them, or
  *     MOE_WEIGHTS_FP4:  q and scale as moe_quantize_fp4 gives them
- * Sums are fp32.  Of each 128 values of x that scales share, those below 2^-28 of the
- * largest lose digits; the activations are rounded to 11 bits, relative to the larger of
- * themselves and 2^-28 of the largest of their 128.  A token's result does not depend on the
- * others, nor on T; repeated calls give the same bits.
+ * Sums are fp32.  Of each 128 values of x, those below 2^-28 of the largest lose digits;
+ * the activations are rounded to 11 bits, relative to the larger of themselves and 2^-28 of
+ * the largest of their 128; 4-bit weights whose scale is below 2^-23 of the largest of the
+ * four that 128 columns have may count as zero.  Repeated calls give the same bits.  With
+ * e4m3 weights a token's result does not depend on the others; with 4-bit ones its last
+ * bits may, on whether more than 4 tokens have its expert.
  * H and I are multiples of 16 (of 32 where a matrix of 4 bits has them as its row length)
  * up to MOE_SMALL_WIDTH; x, out and the codes are 16-byte aligned, the scales, idx and
  * gate 4-byte aligned.  work: moe_layer_small_work_size bytes, 16-byte aligned, of any

@@ -28,7 +28,8 @@ SOURCES = ["router_bf16_staged.cu", "router_bf16_direct.cu", "router_fp32_staged
            "router_step_ext_fp32_direct.cu",
            "router_dispatch.cu", "router_ext_bf16.cu", "router_ext_fp32.cu", "router_combine.cu", "sinkhorn.cu", "taot_match.cu", "eplb.cu", "abi.cu",
            "route_bf16.cu", "route_fp32.cu", "quantize.cu", "quantize_fp4.cu", "expert_matmul.cu", "expert_matmul_fp4.cu",
-           "expert_glu.cu", "expert_combine.cu", "layer_small.cu", "experts_abi.cu"]
+           "expert_glu.cu", "expert_combine.cu", "layer_small.cu", "layer_small_fp4_up.cu", "layer_small_fp4_down.cu",
+           "layer_small_e4m3_up.cu", "layer_small_e4m3_down.cu", "experts_abi.cu"]
 
 
 def nvcc() -> str:

@@ -9,8 +9,6 @@
 namespace moe {
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
-
 // The block's scale and its inverse, from the bits of max|x|.
 struct Pow2Scale {
   float scale, inv;

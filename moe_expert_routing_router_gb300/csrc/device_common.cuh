@@ -9,6 +9,7 @@
 namespace moe {
 
 constexpr int kWarp = 32;
+constexpr unsigned kFull = 0xffffffffu;          // all lanes of a warp
 constexpr float kLog2e = 1.4426950408889634f;   // log2(e)
 
 // ---------------------------------------------------------------------------

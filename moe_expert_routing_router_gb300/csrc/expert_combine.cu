@@ -25,7 +25,6 @@ namespace {
 
 constexpr int kMaxK = 8;
 constexpr int kWarps = 8;            // of a CTA
-constexpr unsigned kFull = 0xffffffffu;
 
 // VEC neighbouring values, kept as they were loaded.
 template <bool BF16, int VEC>

@@ -1,0 +1,8 @@
+// The second kernel of the layer for few tokens, on 8-bit weights.
+#include "layer_small.cuh"
+
+namespace moe {
+
+cudaError_t launch_small_e4m3_down(const SmallLayerParams& p, int sms, cudaStream_t stream) { return launch<false, false>(p, sms, stream); }
+
+}  // namespace moe

@@ -30,7 +30,6 @@ namespace {
 
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / kWarp;
-constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
 // No choice value: above and below nothing, and passed over by fmaxf.

@@ -10,7 +10,6 @@
 namespace moe {
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
 constexpr int kTmemCols = 512;                // of an SM: its one CTA takes all
 constexpr int kRowBytes = 128;                // of an operand's row in a stage
 

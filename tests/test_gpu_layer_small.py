@@ -117,17 +117,26 @@ def test_no_expert_and_the_same_expert_twice(mr, kind):
     assert not bool(mr.moe_layer_small(x, i32(np.full((T, k), -1)), gate, w1, w2, out=none).any())
 
 
-@pytest.mark.parametrize("kind", ["fp4", "e4m3"])
-def test_a_token_alone_and_among_others(mr, kind):
-    """The same bits, whatever its place among its experts' tokens and the passes over them."""
-    T, k, E, H, I = 64, 2, 3, 288, 160
-    x, idx, gate = inputs(T, k, E, H, 3)
+@pytest.mark.parametrize("kind,T,E", [("e4m3", 64, 3), ("fp4", 12, 8)])
+def test_a_token_alone_and_among_others(mr, kind, T, E):
+    """The same bits, whatever its place among its experts' tokens and the passes over them (4-bit weights: of up to 4)."""
+    k, H, I = 2, 288, 160
+    x, _, gate = inputs(T, k, E, H, 3)
+    t = np.arange(T)
+    idx = i32(np.stack([2 * t % E, (2 * t + 1) % E], axis=1))      # fp4: three tokens an expert
     w1, w2 = weights(mr, kind, E, 2 * I, H, 1), weights(mr, kind, E, H, I, 2)
     base = mr.moe_layer_small(x, idx, gate, w1, w2)
-    assert torch.equal(base, mr.moe_layer_small(x, idx, gate, w1, w2))
-    for part in ([0], [17], [63], [5, 4, 3], list(range(20, 43))):
+    for part in ([0], [T - 1], [5, 4, 3], list(range(2, T // 2 + 3))):
         got = mr.moe_layer_small(x[part].contiguous(), idx[part].contiguous(), gate[part].contiguous(), w1, w2)
         assert torch.equal(got, base[part])
+
+
+@pytest.mark.parametrize("kind", ["fp4", "e4m3"])
+def test_repeated_calls_give_the_same_bits(mr, kind):
+    x, idx, gate = inputs(64, 4, 5, 288, 3)
+    w1, w2 = weights(mr, kind, 5, 320, 288, 1), weights(mr, kind, 5, 288, 160, 2)
+    base = mr.moe_layer_small(x, idx, gate, w1, w2)
+    assert all(torch.equal(base, mr.moe_layer_small(x, idx, gate, w1, w2)) for _ in range(5))
 
 
 @pytest.mark.parametrize("kind", ["fp4", "e4m3"])
