@@ -257,8 +257,7 @@ MOE_API moe_status moe_dequantize_fp4(const void* q, const void* scale, int64_t 
  * are added with them may be lost); the one rounding to bf16 is at the end.  A row's
  * result does not depend on the other rows, and a row or column with a NaN scale is NaN.
  * K is a multiple of 32, N of 16, both up to MOE_MAX_WIDTH; E * N < 2^31, M >= 1,
- * M < 2^31; q, wq and out are 16-byte aligned, the scales 4-byte aligned.
- * Needs no workspace.  A device wait that runs out is reported by
+ * M < 2^31; q, wq, wscale and out are 16-byte aligned, scale 4-byte aligned.  Needs no workspace.  A device wait that runs out is reported by
  * moe_expert_device_status, and until that is read later products on the device write
  * nothing. */
 MOE_API moe_status moe_expert_matmul_fp4(const void* q, const void* scale, int64_t M, int32_t K,

@@ -352,9 +352,9 @@ moe_status moe_expert_matmul_fp4(const void* q, const void* scale, int64_t M, in
   if (!q || !scale || !wq || !wscale || !out) return fail(MOE_ERR_INVALID, "an argument is NULL");
   if (offsets == nullptr && (E != 1 || kept != nullptr)) return fail(MOE_ERR_INVALID, "without offsets there is one expert and no kept");
   if (int64_t(E) * N >= kInt32Limit) return fail(MOE_ERR_INVALID, "E*N = %lld does not fit int32", (long long)E * N);
-  if (!aligned(q, 16) || !aligned(wq, 16) || !aligned(out, 16)) return fail(MOE_ERR_INVALID, "q, wq or out is not 16-byte aligned");
-  if (!aligned(scale, 4) || !aligned(wscale, 4) || !aligned(offsets, 4) || !aligned(kept, 4))
-    return fail(MOE_ERR_INVALID, "an array is not 4-byte aligned");
+  if (!aligned(q, 16) || !aligned(wq, 16) || !aligned(wscale, 16) || !aligned(out, 16))
+    return fail(MOE_ERR_INVALID, "q, wq, wscale or out is not 16-byte aligned");
+  if (!aligned(scale, 4) || !aligned(offsets, 4) || !aligned(kept, 4)) return fail(MOE_ERR_INVALID, "an array is not 4-byte aligned");
   // the tiles of the launch are counted in int32
   if ((M / 128 + E) * ((N + 127) / 128) >= kInt32Limit)
     return fail(MOE_ERR_INVALID, "M = %lld by N = %d is too large", (long long)M, N);
