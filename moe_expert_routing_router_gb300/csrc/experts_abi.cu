@@ -337,6 +337,7 @@ moe_status moe_dequantize_fp4(const void* q, const void* scale, int64_t M, int32
   if ((s = check_dtype(dt)) != MOE_OK || (s = check_rows("M", M)) != MOE_OK || (s = check_fp4_width("K", K)) != MOE_OK) return s;
   if (!q || !scale || !y) return fail(MOE_ERR_INVALID, "an argument is NULL");
   if (!aligned(q, 16) || !aligned(y, 16) || !aligned(scale, 4)) return fail(MOE_ERR_INVALID, "q or y (16 bytes) or scale (4 bytes) is misaligned");
+  if (M * (K / 8) >= kInt32Limit * 1024) return fail(MOE_ERR_INVALID, "M = %lld by K = %d is too large", (long long)M, K);
   moe::DequantFp4Params p = {static_cast<const uint8_t*>(q), static_cast<const uint32_t*>(scale), M, K, y};
   return launched(moe::launch_dequantize_fp4(p, dt == MOE_DTYPE_BF16, stream), "moe_dequantize_fp4 launch");
 }
