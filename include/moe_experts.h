@@ -18,7 +18,7 @@
  *   moe_expert_glu / _bwd           the gated activation between the two products,
  *                                   also quantised as it leaves, and its gradient
  *   moe_layer_small                 all that follows the routing, for the few tokens of
- *                                   a decode step, in two kernels
+ *                                   a decode step, in three kernels
  *
  * A layer's forward: moe_route_fwd, moe_dispatch (moe_router.h), then
  * moe_quantize_rows with the dispatch's perm, moe_expert_matmul, the caller's

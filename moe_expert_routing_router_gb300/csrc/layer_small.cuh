@@ -2,7 +2,7 @@
 //
 //   h_a = glu(W1_e x_t),  out_t = sum_j gate_tj W2_e h_a      a = (t, j), e = idx_tj
 //
-// in two kernels, of which each reads the weights of the experts that have tokens once;
+// in two kernels (and a small one), of which each reads the weights of the experts that have tokens once;
 // that reading is what bounds them.  (The tensor core's own 4-bit and 8-bit products take
 // 128 rows at a time and quantised activations; here an expert has a token or two.)
 //
@@ -24,16 +24,16 @@
 // values of h are rounded to 11 bits (three more than bf16 has).  All sums are fp32.
 //
 // What is under way waits in L1, so that shared memory is kept small: eight tokens of an expert are
-// staged at a time, in a large batch 16, and more take the same tiles again, some at a time, from L2.
+// staged at a time, or up to 16, and more take the same tiles again, some at a time, from L2.
 // (16 tokens, 8 of 64 experts of 4096 and 2048, 8 bits: 240 us with 182 KB of shared memory, 390 with 230 KB.)
 // Copies to shared memory were slower: of 16 bytes a lane 320 us, tensor copies of 8 x 128 bytes by each warp 298, of 8 x 2048
 // by a producer warp 268, bulk copies of rows 309.
 //
 // The first kernel's tiles are 8 rows of the gate and the 8 rows of the other half that go
-// with them.  The second one's sums go to memory by assignment, and the CTA that completes
-// a block of 128 columns adds them up by gate, in the order of j: no result depends on an order of
-// arrival.  It is launched while the first one ends (programmatic dependent launch), and has its first
-// weights under way when that is done.
+// with them.  The second one's sums go to memory by assignment, and a third, small kernel adds
+// them up by gate, in the order of j: no result depends on an order of arrival.  Each is launched while
+// the one before it ends (programmatic dependent launch); the second has its first weights under way
+// when the first one is done.
 #pragma once
 
 #include "block_values.cuh"
@@ -41,6 +41,8 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <atomic>
 
 namespace moe {
 namespace {
@@ -52,7 +54,6 @@ constexpr int kTokens = 8;                    // columns of a product
 constexpr int kFew = 4;                       // tokens that take four columns each
 constexpr int kChunk = 16;                    // tiles that are taken again for more tokens
 constexpr int kMaxE = 1024, kMaxA = kSmallTokens * 8;
-constexpr int kJoin = kSmallJoin;
 constexpr int kZeros = 2 * kUnit;             // bytes: a token's unit where there is none
 constexpr int kMaxSlots = 8;                  // tiles whose parts are added up together
 
@@ -64,20 +65,23 @@ struct Lists {
   int work[kMaxA];                            // what stands before them, by tile
   int tile0[kMaxA], tile1[kMaxA];             // their tiles that are this CTA's
   int active, run0, run1;                     // experts that have tokens; the first and last of which this CTA has tiles
-  int ready[kSmallWidth / kJoin], n_ready;    // blocks of columns that this CTA joins
 };
 
-// What a tile of an expert with n tokens takes, in fourths of one that its weights' reading
-// bounds: `cap` tokens are taken at a time.
+// What a tile of an expert with n tokens takes, in eighths of one that its weights' reading
+// bounds: `cap` tokens are taken at a time.  (Of 64 experts of 4096 and 2048 with 1, 4, 8, 12 and 16 tokens
+// each one takes, 13 at a time, 2.7, 3.6, 3.7, 5.6 and 9.6 us at 4 bits, 4.1, 4.2, 4.5, 5.3 and 9.1 at 8.  Where
+// experts' tokens differ, of 64 with 8 of 64 experts each, 8 more for a time over the tiles that is not the last
+// share the work best: 304 us, with 2 more 336.)
 template <bool FP4>
 __device__ __forceinline__ int tile_cost(int n, int cap) {
   const auto pass = [](int tokens) {
-    if (tokens <= kFew / 2) return 4;
-    if (tokens <= kFew) return FP4 ? 6 : 4;
-    if (tokens <= kTokens) return FP4 ? 7 : 5;
-    return FP4 ? 10 : 6;
+    if (tokens <= kFew / 2) return 8;
+    if (tokens <= kFew) return FP4 ? 11 : 8;
+    if (tokens <= kTokens) return FP4 ? 11 : 9;
+    return FP4 ? 16 : 11;
   };
-  return n <= cap ? pass(n) : n / cap * pass(cap) + (n % cap != 0 ? pass(n % cap) : 0);
+  const int passes = (n + cap - 1) / cap, rest = n - (passes - 1) * cap;
+  return (passes - 1) * (pass(cap) + 8) + pass(rest);
 }
 
 __device__ __forceinline__ int warp_prefix(int v, int lane) {    // with the lane's own
@@ -162,7 +166,7 @@ __device__ __forceinline__ void plan(Lists& s, const SmallLayerParams& p, int ti
       if (at < active) s.work[at] = (all + incl - c) * tiles;
       all += __shfl_sync(kFull, incl, kWarp - 1);
     }
-    // the tiles whose work, in order, begins in the CTA's share; all of it is less than 2^23
+    // the tiles whose work, in order, begins in the CTA's share; all of it is less than 2^24
     const int from = int(uint32_t(all * tiles) * blockIdx.x / gridDim.x), to = int(uint32_t(all * tiles) * (blockIdx.x + 1) / gridDim.x);
     int run0 = kMaxA, run1 = -1;
     for (int at0 = 0; at0 < active; at0 += kWarp) {
@@ -382,7 +386,7 @@ __device__ __forceinline__ void run_tiles(const SmallLayerParams& p, const Lists
     if (d % PER == PER - 1) next_tile();
   }
   if constexpr (!UP) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");           // h, and joined, are there
+    asm volatile("griddepcontrol.wait;" ::: "memory");           // h is there
     fetch<UP>(p, s, m, first, n, warp, fresh);
   }
   __syncthreads();                                               // the tokens before, and their parts, are no longer read
@@ -580,12 +584,10 @@ __global__ void __launch_bounds__(kThreads, 1) layer_small_kernel(const __grid_c
   m.red = m.power + m.units * columns;
   m.x = kZeros + (m.units * columns + 2 * slots * kWarps * kRows) * 4;
   if (threadIdx.x < kZeros / 4) reinterpret_cast<uint32_t*>(s_dyn)[threadIdx.x] = 0u;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if constexpr (UP) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t line = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 128;
     if (line < int64_t(p.T) * p.H * 2) asm volatile("prefetch.global.L2 [%0];" :: "l"(static_cast<const char*>(p.x) + line));
-    const int blocks = (p.H + kJoin - 1) / kJoin;
-    if (blockIdx.x == 0 && threadIdx.x < blocks) p.joined[threadIdx.x] = 0;
   }
   const int tiles = UP ? p.I / 8 : p.H / kRows;                  // of an expert
   plan<FP4>(s, p, tiles, cap);
@@ -605,80 +607,43 @@ __global__ void __launch_bounds__(kThreads, 1) layer_small_kernel(const __grid_c
       }
     }
   }
-  if constexpr (UP) return;
-
-  // Blocks of columns whose last sums are this CTA's are joined by it.
-  asm volatile("griddepcontrol.wait;" ::: "memory");             // where it had no tile
-  const int blocks = (p.H + kJoin - 1) / kJoin, in_block = kJoin / kRows;
-  if (threadIdx.x == 0) s.n_ready = 0;
-  __syncthreads();
-  for (int b = threadIdx.x; b < blocks; b += kThreads) {
-    const int b0 = b * in_block, b1 = min(tiles, b0 + in_block);
-    int done = 0;
-    for (int at = run0; at <= run1; ++at) {
-      done += max(0, min(s.tile1[at], b1) - max(s.tile0[at], b0));
-    }
-    const int want = s.active * (b1 - b0);
-    bool mine = want == 0 && blockIdx.x == 0;
-    if (done > 0) {                                              // the CTA's sums come before the count, which comes before the other CTAs' sums
-      int old;
-      asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p.joined + b), "r"(done) : "memory");
-      mine = old + done == want;
-    }
-    if (mine) s.ready[atomicAdd(&s.n_ready, 1)] = b;
-  }
-  __syncthreads();
-  const int n_ready = s.n_ready;
-  constexpr int kFours = kJoin / 4;
-  for (int i = threadIdx.x; i < n_ready * p.T * kFours; i += kThreads) {
-    const int c = s.ready[i / (p.T * kFours)] * kJoin + i % kFours * 4, t = i / kFours % p.T;
-    if (c >= p.H) continue;
-    float4 v[8];
-    float g[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool some = j < p.k && s.idx[t * p.k + j] >= 0;
-      v[j] = some ? __ldcg(reinterpret_cast<const float4*>(p.y + int64_t(t * p.k + j) * p.H + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      g[j] = some ? __ldg(p.gate + t * p.k + j) : 0.f;
-    }
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      sum.x = fmaf(g[j], v[j].x, sum.x);
-      sum.y = fmaf(g[j], v[j].y, sum.y);
-      sum.z = fmaf(g[j], v[j].z, sum.z);
-      sum.w = fmaf(g[j], v[j].w, sum.w);
-    }
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y), hi = __floats2bfloat162_rn(sum.z, sum.w);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + int64_t(t) * p.H + c) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  }
+  if constexpr (!UP) asm volatile("griddepcontrol.wait;" ::: "memory");   // where it had no tile: the third kernel ends behind the first
 }
 
 // Of dynamic shared memory: what leaves L1 room for the weights under way.
-constexpr size_t kShared = 168 * 1024;
-constexpr int kManyTokens = 32;
+constexpr size_t kShared = 144 * 1024;
 
 template <bool FP4, bool UP, int PER, bool WHOLE>
 cudaError_t launch_per(const SmallLayerParams& p, int sms, cudaStream_t stream) {
   const int K = UP ? p.H : p.I, units = (K + kUnit - 1) / kUnit;
   const int pitch = units * kUnit * 2 + 16;                      // rows' same pieces lie in different banks
   // Tokens of an expert that are staged at once, and parts of tiles: of a round's tiles at least, of eight at most.
-  // Twice as many tokens, which leave L1 less, where most experts are likely to have more than eight.
-  int cap = p.T <= kManyTokens ? (p.T < kTokens ? p.T : kTokens) : 2 * kTokens, columns = 0, slots = 0;
+  // More of them, which leave L1 less, where experts have more than four on average.  (64 experts of 4096 and 2048, 8 bits:
+  // 8 a token: 64 tokens 442 us with 8 at once, 387 with 12; 16 tokens 231 and 237.)
+  int cap = p.T * p.k > 4 * p.E ? 2 * kTokens : kTokens, columns = 0, slots = 0;
+  if (cap > p.T) cap = p.T;
   size_t smem = 0;
   for (;; --cap) {
     constexpr int kAhead = FP4 ? 4 : 2, kRound = PER < kAhead ? kAhead / PER : 1, kRound2 = PER < 2 ? 2 / PER : 1;
     columns = cap > kTokens ? 2 * kTokens : kTokens;
     const int least = cap > kTokens && kRound2 * cap > kRound * kTokens ? kRound2 * cap : kRound * (cap < kTokens ? cap : kTokens);
-    slots = least > 2 * kTokens ? least : 2 * kTokens;
+    slots = cap > kTokens || least > 2 * kTokens ? least : 2 * kTokens;
     if (slots > kMaxSlots * cap) slots = kMaxSlots * cap;
     smem = kZeros + size_t(units) * columns * 4 + size_t(cap) * pitch + size_t(slots) * 2 * kWarps * kRows * 4;
     if (smem <= kShared) break;
   }
   const auto kernel = layer_small_kernel<FP4, UP, PER, WHOLE>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kShared));
+  // The limit of shared memory is raised once on each device: the host's time is a good part of a small call's.
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev > 63 || (raised.load(std::memory_order_relaxed) & bit) == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kShared));
+    if (e != cudaSuccess) return e;
+    raised.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(sms));
   cfg.blockDim = dim3(kThreads);

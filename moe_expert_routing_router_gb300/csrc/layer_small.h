@@ -7,7 +7,6 @@
 namespace moe {
 
 constexpr int kSmallTokens = 64, kSmallWidth = 16384;
-constexpr int kSmallJoin = 128;               // columns of the result that are joined together
 
 // Weights of all experts: 4-bit codes [E, N, K/2] with words of four exponents
 // [ceil(K/128), E N], or e4m3 codes [E, N, K] with scales [E, ceil(N/128), ceil(K/128)].
@@ -26,10 +25,9 @@ struct SmallLayerParams {
   void* out;              // [T, H] bf16
   float* h;               // [T k, I]: scratch
   float* y;               // [T k, H]: scratch
-  int* joined;            // [ceil(H / kSmallJoin)]: scratch
 };
 size_t small_layer_work_size(int T, int H, int I, int k);
-// Sets h, y and joined within `work`.
+// Sets h and y within `work`.
 void small_layer_work(SmallLayerParams& p, void* work);
 // The first kernel (up) and the second by the kind of their weights.
 cudaError_t launch_small_fp4_up(const SmallLayerParams& p, int sms, cudaStream_t stream);

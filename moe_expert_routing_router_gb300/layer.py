@@ -142,7 +142,7 @@ def _weights(name: str, w: dict, E: int | None, N: int | None, K: int | None, at
 def moe_layer_small(x: torch.Tensor, idx: torch.Tensor, gate: torch.Tensor, w1: dict, w2: dict, out: torch.Tensor | None = None,
                     stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """out [T, H] bf16 = sum_j gate[t, j] * W2_e silu(G_e x_t) * (U_e x_t), e = idx[t, j], for up to 64 tokens x [T, H] bf16:
-    what follows moe_route_fwd in a layer, in two kernels.  w1 holds the weights [E, 2I, H] (G's rows, then U's) and w2
+    what follows moe_route_fwd in a layer, in three kernels.  w1 holds the weights [E, 2I, H] (G's rows, then U's) and w2
     [E, H, I], each as moe_quantize_weights or moe_quantize_fp4 gives them; idx and gate are [T, k], and an idx outside
     [0, E) adds nothing (C: moe_layer_small)."""
     T, H = _need_dims("x", x, 2, (torch.bfloat16,))
