@@ -188,8 +188,8 @@ MOE_API moe_status moe_expert_wgrad(const void* dyq, const float* dyscale, const
                                     moe_stream_t stream);
 
 /* Reads and clears the error bits that moe_expert_matmul, moe_expert_wgrad and
- * moe_expert_matmul_fp4 calls have left on the current device (synchronises `stream`, on which they
- * were queued).  *flags = 0 when every wait completed; otherwise returns
+ * moe_expert_matmul_fp4 calls have left on the current device (synchronises `stream`, on
+ * which they were queued).  *flags = 0 when every wait completed; otherwise returns
  * MOE_ERR_TIMEOUT with bit 2 set: a wait of a kernel's pipeline expired and its
  * output is incomplete.  Bits are read and cleared in one step: each is given to one
  * reader, whichever stream its call ran on. */
@@ -257,9 +257,9 @@ MOE_API moe_status moe_dequantize_fp4(const void* q, const void* scale, int64_t 
  * are added with them may be lost); the one rounding to bf16 is at the end.  A row's
  * result does not depend on the other rows, and a row or column with a NaN scale is NaN.
  * K is a multiple of 32, N of 16, both up to MOE_MAX_WIDTH; E * N < 2^31, M >= 1,
- * M < 2^31; q, wq, wscale and out are 16-byte aligned, scale 4-byte aligned.  Needs no workspace.  A device wait that runs out is reported by
- * moe_expert_device_status, and until that is read later products on the device write
- * nothing. */
+ * M < 2^31; q, wq, wscale and out are 16-byte aligned, scale 4-byte aligned.  Needs no
+ * workspace.  A device wait that runs out is reported by moe_expert_device_status, and
+ * until that is read later products on the device write nothing. */
 MOE_API moe_status moe_expert_matmul_fp4(const void* q, const void* scale, int64_t M, int32_t K,
                                          const void* wq, const void* wscale, int32_t E, int32_t N,
                                          const int32_t* offsets, const int32_t* kept, moe_dtype out_dt, void* out,

@@ -22,10 +22,11 @@
 // A stage's scales have columns of their own in tensor memory, so that their reuse is
 // ordered by the stage's.
 //
-// What bounds it: with few rows of an expert the weights' reading, 64 us for 64 experts of 2048 by
-// 4096 (285 MB, 4.5 TB/s; 8 rows each); with many the way from L2 to an SM, which takes
-// 52 KB a stage at 55 to 64 bytes a cycle, while its products take 400 cycles: 205 us and
-// 5.0 PFLOP/s with 1024 rows each.
+// What bounds it: with few rows of an expert the weights' reading, 50 us for 64 experts of 2048 by
+// 4096 (285 MB, 5.7 TB/s; 8 rows each); with many the way from L2 to an SM, which takes
+// 52 KB a stage at 55 to 64 bytes a cycle, while its products would take 400 cycles: 205 us and
+// 5.0 PFLOP/s with 1024 rows each.  (CTA pairs, which bring 35 KB a stage, were no more than 6 percent
+// faster there, 590 cycles a stage however full the ring was, and slower with 256 rows each.)
 //
 // Every wait is bounded: when one runs out, the CTA records the pipeline's error
 // bit, drains its copies and returns.

@@ -1,5 +1,6 @@
 """Python binding of what include/moe_experts.h has around the experts' 8-bit operators: 4-bit quantisation, the experts'
-products on it, the gated activation between two products, and the experts of a layer for few tokens.  Argument marshalling only, by the rules of ``experts``.
+products on it, the gated activation between two products, and the experts of a layer for few tokens.  Argument
+marshalling only, by the rules of ``experts``.
 """
 
 from __future__ import annotations

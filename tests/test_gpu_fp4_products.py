@@ -75,8 +75,13 @@ SHAPES = [([1], None, 32, 16), ([128], None, 64, 128), ([129], None, 96, 272), (
           ([40] * 20, None, 320, 64), ([1, 2, 3, 0, 700], [1, 1, 3, 0, 650], 1440, 1040), ([31, 33], [0, 33], 4096, 48), ([1100], None, 256, 528)]
 
 
+# Enough tiles for the wide ones, and for several rounds of the narrow ones; ragged rows, columns and ends of the contraction.
+MANY = [([700, 300, 900, 513], None, 96, 1552), ([2413], None, 544, 1552), ([900, 0, 1501, 70, 2600], [900, 0, 1300, 70, 2555], 288, 2064),
+        ([75] * 16, [75, 3] * 8, 320, 2064), ([5000, 1, 129], None, 1184, 272), ([1024] * 3, None, 768, 2048)]
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("counts,kept,K,N", SHAPES)
+@pytest.mark.parametrize("counts,kept,K,N", SHAPES + MANY)
 def test_products(mr, counts, kept, K, N, dtype):
     M, E = sum(counts), len(counts)
     ops = operands(M, K, E, N, M + K)
@@ -84,6 +89,19 @@ def test_products(mr, counts, kept, K, N, dtype):
     before = torch.full((M, N), 7.0, dtype=dtype, device="cuda")
     got = mr.moe_expert_matmul_fp4(*ops, offsets, kt, out=before.clone())
     check(got, *expected(*ops, rows), K, before)
+
+
+def test_scales_at_any_word(mr):
+    """The rows' scales begin anywhere in 4 bytes; the weights' in 16, or the call is refused."""
+    counts, K, N = [3, 150, 61], 160, 144
+    offsets, _, rows = split(counts)
+    q, s, wq, ws = operands(sum(counts), K, len(counts), N, 9)
+    want = mr.moe_expert_matmul_fp4(q, s, wq, ws, offsets)
+    for words in (1, 2, 3):
+        moved = [torch.cat([t.flatten().new_zeros(4 * words), t.flatten()])[4 * words:].view(t.shape) for t in (s, ws)]
+        assert torch.equal(mr.moe_expert_matmul_fp4(q, moved[0], wq, ws, offsets), want)
+        with pytest.raises(mr._native.MoeRouterError, match="aligned"):
+            mr.moe_expert_matmul_fp4(q, s, wq, moved[1], offsets)
 
 
 @pytest.mark.parametrize("K", [32, 64, 96, 128, 160, 224, 256, 288, 352, 480, 512, 544])

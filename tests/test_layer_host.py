@@ -26,7 +26,7 @@ BAD += [("moe_dequantize_fp4", p, v, w) for p, v, w in [
     (0, None, 1), (0, FAKE + 8, 1), (1, None, 1), (1, FAKE + 1, 1), (2, 0, 1), (2, BIG, 1), (3, 48, 1), (3, 0, 1), (4, 2, 2), (5, None, 1), (5, FAKE + 4, 1)]]
 BAD += [("moe_expert_matmul_fp4", p, v, w) for p, v, w in [
     (0, None, 1), (0, FAKE + 8, 1), (1, None, 1), (1, FAKE + 2, 1), (2, 0, 1), (2, BIG, 1), (3, 0, 1), (3, 16, 1), (3, 112, 1), (3, 1 << 21, 1), (4, None, 1),
-    (4, FAKE + 4, 1), (5, None, 1), (5, FAKE + 1, 1), (6, 0, 1), (6, 1025, 1), (7, 40, 1), (7, 0, 1), (8, None, 1), (8, FAKE + 2, 1), (9, FAKE + 2, 1),
+    (4, FAKE + 4, 1), (5, None, 1), (5, FAKE + 1, 1), (5, FAKE + 8, 1), (6, 0, 1), (6, 1025, 1), (7, 40, 1), (7, 0, 1), (8, None, 1), (8, FAKE + 2, 1), (9, FAKE + 2, 1),
     (10, 2, 2), (11, None, 1), (11, FAKE + 8, 1)]]
 BAD += [("moe_expert_glu", p, v, w) for p, v, w in [
     (0, None, 1), (0, FAKE + 8, 1), (1, 2, 2), (2, 0, 1), (2, BIG, 1), (3, 0, 1), (3, 16, 1), (3, 1 << 21, 1), (4, 3, 1), (4, -1, 1), (4, 0, 1), (5, None, 1),
@@ -58,6 +58,9 @@ def test_refusals_of_combinations(native_lib):
     m = list(GOOD["moe_expert_matmul_fp4"])
     m[2], m[6], m[7] = BIG - 1, 1024, 1 << 20                    # E * N fills 2^30 rows; M rows make too many tiles
     assert native_lib.moe_expert_matmul_fp4(*m) == 1
+    d = list(GOOD["moe_dequantize_fp4"])
+    d[2], d[3] = BIG - 1, 1 << 20                                # more pieces than a grid has
+    assert native_lib.moe_dequantize_fp4(*d) == 1
     a = list(GOOD["moe_expert_glu"])
     a[3], a[4] = 24, 1                                           # e4m3 takes multiples of 16
     assert native_lib.moe_expert_glu(*a) == 1
