@@ -165,7 +165,7 @@ struct Walk {
     // work share both operands' tiles in L2.
     const int group = rt <= kGroupM ? 0 : i / (kGroupM * ct), in = i - group * kGroupM * ct;
     const int gm = min(kGroupM, rt - group * kGroupM);
-    const int col = int(__fdividef(float(in) + 0.5f, float(gm)));   // in / gm: in is at most 16 * 2^9
+    const int col = int(__fdividef(float(in) + 0.5f, float(gm)));   // in / gm, of at most 2^17: off by less than 1 / 32
     const int r0 = (group * kGroupM + in - col * gm) * kBM;
     col0 = col * BN;
     cols = min(BN, p.C - col0);

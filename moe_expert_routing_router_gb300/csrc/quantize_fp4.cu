@@ -8,7 +8,9 @@
 // another, as the tiles of a product read them.
 //
 // Both kernels are bound by memory and move every value once.  Quantising, a team of eight lanes
-// holds 128 values of a row, 16 each, so that a block is two neighbouring lanes'.
+// holds 128 values of a row, 16 each, so that a block is two neighbouring lanes'.  65560 rows of 4096, bf16:
+// 108 us (6.3 TB/s); gathered, eight of each row, 76 us, where the rows come from L2 and 70 percent of the
+// issue slots are taken (96, 80, 76 and 76 us with 1, 2, 4 and 8 rows a lane).
 #include "block_values.cuh"
 #include "quantize_fp4.h"
 
