@@ -77,7 +77,8 @@ SHAPES = [([1], None, 32, 16), ([128], None, 64, 128), ([129], None, 96, 272), (
 
 # Enough tiles for the wide ones, and for several rounds of the narrow ones; ragged rows, columns and ends of the contraction.
 MANY = [([700, 300, 900, 513], None, 96, 1552), ([2413], None, 544, 1552), ([900, 0, 1501, 70, 2600], [900, 0, 1300, 70, 2555], 288, 2064),
-        ([75] * 16, [75, 3] * 8, 320, 2064), ([5000, 1, 129], None, 1184, 272), ([1024] * 3, None, 768, 2048)]
+        ([75] * 16, [75, 3] * 8, 320, 2064), ([5000, 1, 129], None, 1184, 272), ([1024] * 3, None, 768, 2048),
+        ([1, 0, 2, 0] * 256, [1, 0, 1, 0] * 256, 64, 32), ([0] * 1023 + [140], None, 96, 144)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
