@@ -25,7 +25,7 @@
 //
 // What is under way waits in L1, so that shared memory is kept small: eight tokens of an expert are
 // staged at a time, or up to 16, and more take the same tiles again, some at a time, from L2.
-// (16 tokens, 8 of 64 experts of 4096 and 2048, 8 bits: 240 us with 182 KB of shared memory, 390 with 230 KB.)
+// (16 tokens, 8 of 64 experts of 4096 and 2048, 8 bits: 231 us with 144 KB of shared memory, 240 with 182 KB, 390 with 230 KB.)
 // Copies to shared memory were slower: of 16 bytes a lane 320 us, tensor copies of 8 x 128 bytes by each warp 298, of 8 x 2048
 // by a producer warp 268, bulk copies of rows 309.
 //
@@ -34,6 +34,10 @@
 // them up by gate, in the order of j: no result depends on an order of arrival.  Each is launched while
 // the one before it ends (programmatic dependent launch); the second has its first weights under way
 // when the first one is done.
+//
+// 8 of 64 experts of 4096 and 2048, a call in a graph: 4 bits, 1 token 30 us, 16 tokens 162 us (5 TB/s of weights,
+// 45 percent of the issue slots: unpacking beside the loads); 8 bits, 16 tokens 218 us (6.4 TB/s), 64 tokens 304 us.
+// About 10 us of each are the launches, the lists and the sums over experts.
 #pragma once
 
 #include "block_values.cuh"
@@ -462,13 +466,12 @@ __device__ __forceinline__ void run_tiles(const SmallLayerParams& p, const Lists
         s0 = there ? make_float2(a, a) : make_float2(0.f, 0.f);
         s1 = there ? make_float2(b, b) : make_float2(0.f, 0.f);
       }
-      constexpr int C = NT == 1 ? 2 : 1;                         // chains of products
-      float dot[NT * C][4];
+      float dot[NT][4];                                          // one chain of products for any NT, so that a token's sums are alike
       const uint8_t* at[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
-        for (int v = 0; v < 4 * C; ++v) dot[j * C + v / 4][v % 4] = 0.f;
+        for (int v = 0; v < 4; ++v) dot[j][v] = 0.f;
         if constexpr (!kHeld) at[j] = values(j, lu);
       }
 #pragma unroll
@@ -492,13 +495,9 @@ __device__ __forceinline__ void run_tiles(const SmallLayerParams& p, const Lists
           uint4 b;
           if constexpr (kHeld) b = held[j * PER + lu][i];
           else b = *reinterpret_cast<const uint4*>(at[j] + piece(i));
-          mma_f16(dot[j * C], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
-          mma_f16(dot[j * C + C - 1], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
+          mma_f16(dot[j], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+          mma_f16(dot[j], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
         }
-      }
-      if constexpr (C == 2) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) dot[0][v] += dot[1][v];
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j) {

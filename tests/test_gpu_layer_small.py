@@ -117,13 +117,16 @@ def test_no_expert_and_the_same_expert_twice(mr, kind):
     assert not bool(mr.moe_layer_small(x, i32(np.full((T, k), -1)), gate, w1, w2, out=none).any())
 
 
-@pytest.mark.parametrize("kind,T,E", [("e4m3", 64, 3), ("fp4", 12, 8)])
-def test_a_token_alone_and_among_others(mr, kind, T, E):
-    """The same bits, whatever its place among its experts' tokens and the passes over them (4-bit weights: of up to 4)."""
-    k, H, I = 2, 288, 160
+@pytest.mark.parametrize("kind,T,E,H,I,spread", [("e4m3", 64, 3, 288, 160, 0.0), ("fp4", 12, 8, 288, 160, 0.0), ("e4m3", 64, 3, 1056, 544, 3.0), ("fp4", 12, 8, 1056, 544, 3.0),
+                                                 ("fp4", 16, 8, 2080, 1056, 3.0), ("e4m3", 21, 4, 2080, 1056, 3.0)])
+def test_a_token_alone_and_among_others(mr, kind, T, E, H, I, spread):
+    """The same bits, whatever its place among its experts' tokens and the passes over them (4-bit weights: of up to 4), also
+    where sums of values of very different sizes are rounded at every step."""
+    k = 2
     x, _, gate = inputs(T, k, E, H, 3)
+    x = (x.float() * torch.exp(spread * torch.randn(T, H, generator=torch.Generator().manual_seed(4))).cuda()).to(torch.bfloat16)
     t = np.arange(T)
-    idx = i32(np.stack([2 * t % E, (2 * t + 1) % E], axis=1))      # fp4: three tokens an expert
+    idx = i32(np.stack([2 * t % E, (2 * t + 1) % E], axis=1))      # fp4: three or four tokens an expert
     w1, w2 = weights(mr, kind, E, 2 * I, H, 1), weights(mr, kind, E, H, I, 2)
     base = mr.moe_layer_small(x, idx, gate, w1, w2)
     for part in ([0], [T - 1], [5, 4, 3], list(range(2, T // 2 + 3))):
