@@ -176,7 +176,7 @@ def test_not_a_number_scales(mr):
 
 
 def test_rows_do_not_depend_on_one_another(mr):
-    """A row alone, among few and among many (both tile widths): the same bits."""
+    """A row alone and among others: the same bits."""
     K, N, E = 512, 384, 2
     q, s, wq, ws = operands(600, K, E, N, 9)
     offsets, kept, _ = split([300, 300], [250, 300])
@@ -184,6 +184,15 @@ def test_rows_do_not_depend_on_one_another(mr):
     for r in (0, 249, 300, 599):
         one = mr.moe_expert_matmul_fp4(q[r:r + 1].contiguous(), s[:, r:r + 1].contiguous(), wq, ws, i32([0, 1, 1] if r < 300 else [0, 0, 1]), out_dtype=torch.float32)
         assert torch.equal(one[0], base[r])
+
+
+def test_rows_alike_in_tiles_of_either_width(mr):
+    """Rows of a call with many, and alone in a small one: the same bits, of sums that are rounded at every step."""
+    M, K, N = 2413, 1184, 1552
+    q, s, wq, ws = operands(M, K, 1, N, 4, spread=12)
+    many = mr.moe_expert_matmul_fp4(q, s, wq, ws, out_dtype=torch.float32)
+    for at in (slice(0, 40), slice(1201, 1330), slice(2412, 2413)):
+        assert torch.equal(mr.moe_expert_matmul_fp4(q[at].contiguous(), s[:, at].contiguous(), wq, ws, out_dtype=torch.float32), many[at])
 
 
 def test_positions_outside_the_arrays_stay_inside(mr):
