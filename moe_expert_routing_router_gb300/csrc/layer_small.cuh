@@ -59,12 +59,15 @@ constexpr int kFew = 4;                       // tokens that take four columns e
 constexpr int kChunk = 16;                    // tiles that are taken again for more tokens
 constexpr int kMaxE = 1024, kMaxA = kSmallTokens * 8;
 constexpr int kZeros = 2 * kUnit;             // bytes: a token's unit where there is none
+constexpr uint32_t kOnes = 0x01010101u;       // a byte each
 constexpr int kMaxSlots = 8;                  // tiles whose parts are added up together
 
+extern __shared__ __align__(16) uint8_t s_dyn[];                 // begins with kZeros bytes of zeros
+
 struct Lists {
-  alignas(16) int idx[kMaxA];                 // the assignments' experts, -1 for none
   int order[kMaxA];                           // assignments by expert
-  int count[kMaxE];                           // of an expert; then the place of its first assignment
+  int count[kMaxE];                           // the place of an expert's first assignment
+  int share[2 * kWarps];                      // assignments and experts of a warp's share of the experts
   int expert[kMaxA], start[kMaxA + 1];        // of the experts that have tokens: which, and where theirs start
   int work[kMaxA];                            // what stands before them, by tile
   int tile0[kMaxA], tile1[kMaxA];             // their tiles that are this CTA's
@@ -104,7 +107,6 @@ __device__ __forceinline__ void plan(Lists& s, const SmallLayerParams& p, int ti
   const unsigned below = (1u << lane) - 1u;
   int e = threadIdx.x < A ? p.idx[threadIdx.x] : -1;             // A is kThreads at most
   if (e < 0 || e >= p.E) e = -1;
-  if (threadIdx.x < A) s.idx[threadIdx.x] = e;
   if (A <= kWarp) {                                              // one warp: groups of equal experts, by their first
     if (threadIdx.x < kWarp) {
       const unsigned peers = __match_any_sync(kFull, e);
@@ -123,43 +125,55 @@ __device__ __forceinline__ void plan(Lists& s, const SmallLayerParams& p, int ti
       }
     }
   } else {
-    for (int i = threadIdx.x; i < p.E; i += kThreads) s.count[i] = 0;
+    // How many of an expert's assignments each warp has, in a byte; the warps list 32 experts at a time each.
+    uint4* const table = reinterpret_cast<uint4*>(s_dyn + kZeros);
+    for (int i = threadIdx.x; i < p.E; i += kThreads) table[i] = make_uint4(0u, 0u, 0u, 0u);
+    const unsigned peers = __match_any_sync(kFull, e);
+    const int warp = threadIdx.x / kWarp;
     __syncthreads();
-    if (e >= 0) atomicAdd(&s.count[e], 1);
+    if (e >= 0 && __ffs(peers) - 1 == lane) reinterpret_cast<uint8_t*>(table + e)[warp] = uint8_t(__popc(peers));
     __syncthreads();
-    if (threadIdx.x < kWarp) {
-      int active = 0, before = 0;
-      for (int e0 = 0; e0 < p.E; e0 += kWarp) {
-        const int n = e0 + lane < p.E ? s.count[e0 + lane] : 0;
-        const unsigned some = __ballot_sync(kFull, n > 0);
-        if (some == 0u) continue;
-        const int incl = warp_prefix(n, lane);
-        if (n > 0) {
-          const int at = active + __popc(some & below);
-          s.expert[at] = e0 + lane;
-          s.start[at] = s.count[e0 + lane] = before + incl - n;
-        }
-        active += __popc(some);
-        before += __shfl_sync(kFull, incl, kWarp - 1);
-      }
-      if (lane == 0) {
-        s.active = active;
-        s.start[active] = before;
-      }
+    const auto sum = [](uint4 v) { return int(__dp4a(v.x, kOnes, __dp4a(v.y, kOnes, __dp4a(v.z, kOnes, __dp4a(v.w, kOnes, 0u))))); };
+    constexpr int kGroups = kMaxE / kThreads;                    // of 32 experts, of a warp
+    const int e0 = warp * kGroups * kWarp + lane;
+    int n[kGroups], incl[kGroups], all = 0, some = 0;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      n[i] = e0 + i * kWarp < p.E ? sum(table[e0 + i * kWarp]) : 0;
+      incl[i] = all + warp_prefix(n[i], lane);
+      all = __shfl_sync(kFull, incl[i], kWarp - 1);
+      some += __popc(__ballot_sync(kFull, n[i] > 0));
+    }
+    if (lane == 0) {
+      s.share[warp] = all;
+      s.share[kWarps + warp] = some;
+    }
+    int place = __popc(peers & below);                           // among the assignments of its expert
+    if (e >= 0) {
+      uint4 v = table[e];
+      const auto before = [&](int i) { return warp / 4 > i ? 0xffffffffu : warp / 4 == i ? (1u << warp % 4 * 8) - 1u : 0u; };
+      place += sum(make_uint4(v.x & before(0), v.y & before(1), v.z & before(2), v.w & before(3)));
     }
     __syncthreads();
-    if (e >= 0) {                                                // its place: those before it that have the same expert
-      const int4* idx = reinterpret_cast<const int4*>(s.idx);
-      const int a = threadIdx.x;
-      int at = s.count[e];
-      for (int i = 0; i < a / 4; ++i) {
-        const int4 v = idx[i];
-        at += (v.x == e) + (v.y == e) + (v.z == e) + (v.w == e);
+    const int shares = lane < kWarps ? s.share[lane] : 0, experts = lane < kWarps ? s.share[kWarps + lane] : 0;
+    const int first = __reduce_add_sync(kFull, lane < warp ? shares : 0);
+    int at = __reduce_add_sync(kFull, lane < warp ? experts : 0);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const unsigned mask = __ballot_sync(kFull, n[i] > 0);
+      if (n[i] > 0) {
+        const int to = at + __popc(mask & below);
+        s.expert[to] = e0 + i * kWarp;
+        s.start[to] = s.count[e0 + i * kWarp] = first + incl[i] - n[i];
       }
-      for (int i = a / 4 * 4; i < a; ++i) at += s.idx[i] == e;
-      s.order[at] = a;
+      at += __popc(mask);
+    }
+    if (warp == kWarps - 1 && lane == 0) {
+      s.active = at;
+      s.start[at] = first + all;
     }
     __syncthreads();
+    if (e >= 0) s.order[s.count[e] + place] = threadIdx.x;
   }
   if (threadIdx.x < kWarp) {
     __syncwarp();
@@ -196,7 +210,7 @@ __device__ __forceinline__ void plan(Lists& s, const SmallLayerParams& p, int ti
   }
   __syncthreads();
 }
-static_assert(kMaxA <= kThreads, "an assignment a thread");
+static_assert(kMaxA <= kThreads && kWarps == 16 && kMaxE % kThreads == 0, "an assignment a thread, a byte a warp");
 
 // Where a CTA's shared memory lies behind the lists.
 struct Staged {
@@ -206,7 +220,6 @@ struct Staged {
   int pitch, columns, units;
   int slots;                                  // tiles times tokens that `red` holds
 };
-extern __shared__ __align__(16) uint8_t s_dyn[];                 // begins with kZeros bytes of zeros
 
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
@@ -631,6 +644,7 @@ cudaError_t launch_per(const SmallLayerParams& p, int sms, cudaStream_t stream) 
     smem = kZeros + size_t(units) * columns * 4 + size_t(cap) * pitch + size_t(slots) * 2 * kWarps * kRows * 4;
     if (smem <= kShared) break;
   }
+  if (smem < kZeros + size_t(p.E) * kWarps) smem = kZeros + size_t(p.E) * kWarps;   // the lists' table
   const auto kernel = layer_small_kernel<FP4, UP, PER, WHOLE>;
   // The limit of shared memory is raised once on each device: the host's time is a good part of a small call's.
   static std::atomic<uint64_t> raised{0};
