@@ -91,6 +91,7 @@ CASES = [
     (7, 2, 5, 2080, 288, "fp4", "fp4"), (16, 4, 8, 256, 544, "e4m3", "fp4"), (9, 8, 8, 288, 144, "fp4", "e4m3"), (64, 8, 16, 128, 128, "fp4", "fp4"),
     (64, 1, 1, 192, 64, "fp4", "fp4"), (64, 2, 2, 144, 272, "e4m3", "e4m3"), (33, 5, 6, 416, 32, "fp4", "fp4"), (3, 2, 1024, 64, 32, "fp4", "fp4"),
     (20, 1, 1, 16384, 32, "fp4", "fp4"), (12, 1, 1, 64, 16384, "e4m3", "e4m3"), (1, 2, 2, 16, 16, "e4m3", "e4m3"), (40, 1, 1, 4096, 64, "e4m3", "e4m3"),
+    (64, 8, 1024, 32, 32, "fp4", "fp4"), (50, 7, 700, 64, 32, "fp4", "fp4"), (64, 8, 513, 48, 32, "e4m3", "fp4"),
 ]
 
 
