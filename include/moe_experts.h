@@ -304,7 +304,8 @@ typedef enum { MOE_WEIGHTS_E4M3 = 0, MOE_WEIGHTS_FP4 = 1 } moe_weight_kind;
  *   w1 [E,2I,H]: the gates' I rows, then the other I; w2 [E,H,I]; each either
  *     MOE_WEIGHTS_E4M3: q and scale as moe_quantize_weights gives them, or
  *     MOE_WEIGHTS_FP4:  q and scale as moe_quantize_fp4 gives them
- * Sums are fp32.  Of each 128 values of x, those below 2^-28 of the largest lose digits;
+ * Sums are fp32, and what they are formed of stays finite where they do, however large or small
+ * the values and the scales are.  Of each 128 values of x, those below 2^-28 of the largest lose digits;
  * the activations are rounded to 11 bits, relative to the larger of themselves and 2^-28 of
  * the largest of their 128; 4-bit weights whose scale is below 2^-23 of the largest of the
  * four that 128 columns have may count as zero.  Repeated calls give the same bits.  With

@@ -22,6 +22,9 @@
 // The tokens' values are staged in shared memory as fp16 with a power of two for each 128, so that
 // their largest is between 2^14 and 2^15: bf16 values are exact down to 2^-28 of it, and the fp32
 // values of h are rounded to 11 bits (three more than bf16 has).  All sums are fp32.
+// A unit's sum, of codes times such values, is multiplied by the token's power and then by the weights' scale.  Where a
+// power is so far from one that the first product could leave fp32 though the second comes back, `run_far` takes the
+// tiles, in an order that cannot.
 //
 // What is under way waits in L1, so that shared memory is kept small: eight tokens of an expert are
 // staged at a time, or up to 16, and more take the same tiles again, some at a time, from L2.
@@ -71,6 +74,7 @@ struct Lists {
   int expert[kMaxA], start[kMaxA + 1];        // of the experts that have tokens: which, and where theirs start
   int work[kMaxA];                            // what stands before them, by tile
   int tile0[kMaxA], tile1[kMaxA];             // their tiles that are this CTA's
+  int far;                                    // a power of the staged tokens is far from one
   int active, run0, run1;                     // experts that have tokens; the first and last of which this CTA has tiles
 };
 
@@ -226,6 +230,16 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// A unit's sum is at most 2^31 and a multiple of 2^-33: its product with a power in [2^-93, 2^96], one over
+// 2^(up - 127), is exact, and then any scale may follow.
+constexpr uint32_t kNearest = 127 - 96, kFarthest = 127 + 93;
+// to + sum power scale, rounded once, for any power.
+__device__ __forceinline__ float add_scaled(float sum, float power, float scale, float to) {
+  const float c = power * scale;                                 // exact where it is a normal number
+  if ((fabsf(c) >= 0x1p-126f && fabsf(c) < __int_as_float(0x7f800000)) || scale == 0.f) return fmaf(sum, c, to);
+  return fmaf(sum * power, scale, to);                           // both are above 1; or power is below 2^24, and where it is below 1 so is scale
+}
+
 // Rows `order[first ..]` of the tokens (UP: bf16 x) or of the assignments (h), as fp16, in pieces of a
 // unit of a row a warp, four at a time; the rest of the last unit is zero.
 constexpr int kPieces = 4;
@@ -253,7 +267,7 @@ __device__ __forceinline__ void fetch(const SmallLayerParams& p, const Lists& s,
   }
 }
 template <bool UP>
-__device__ __forceinline__ void put(const Staged& m, int n, int i0, const uint32_t (&v)[kPieces][UP ? 2 : 4]) {
+__device__ __forceinline__ void put(Lists& s, const Staged& m, int n, int i0, const uint32_t (&v)[kPieces][UP ? 2 : 4]) {
   const int lane = threadIdx.x % kWarp;
 #pragma unroll
   for (int d = 0; d < kPieces; ++d) {
@@ -269,6 +283,7 @@ __device__ __forceinline__ void put(const Staged& m, int n, int i0, const uint32
     *reinterpret_cast<uint2*>(s_dyn + m.x + row * m.pitch + (u * kUnit + lane * 4) * 2) =
         make_uint2(pack_half2(__uint_as_float(f[0]) * by, __uint_as_float(f[1]) * by), pack_half2(__uint_as_float(f[2]) * by, __uint_as_float(f[3]) * by));
     if (lane == 0) m.power[u * m.columns + row] = __uint_as_float((254u - up) << 23);
+    if (up - kNearest > kFarthest - kNearest && top != 0u && top < 0x7f800000u) s.far = 1;   // zeros and infinities stay so in any order
   }
 }
 
@@ -320,11 +335,33 @@ __device__ __forceinline__ float silu(float g) {
   return g * (g >= 0.f ? r : t * r);
 }
 
+// The sums of `tiles` tiles from the `done`-th on, of the warps' parts in their order, to where they belong.
+template <bool UP>
+__device__ __forceinline__ void add_parts(const SmallLayerParams& p, const Lists& s, const float* red, int done, int tiles, int first, int n) {
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  for (int o0 = warp * kWarp; o0 < tiles * n * kRows; o0 += kThreads) {
+    const int o = o0 + lane, at = o / (n * kRows), in = o - at * n * kRows, row = in % kRows;
+    const bool live = at < tiles;
+    float sum = 0.f;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) sum += red[(at * kWarps + i) * n * kRows + in];
+    }
+    const int64_t a = live ? s.order[first + in / kRows] : 0;
+    if constexpr (UP) {
+      const float other = __shfl_down_sync(kFull, sum, 8);
+      if (live && row < 8) p.h[a * p.I + (done + at) * 8 + row] = silu(sum) * other;
+    } else {
+      if (live) p.y[a * p.H + (done + at) * kRows + row] = sum;
+    }
+  }
+}
+
 // Tiles [tile0, tile1) of expert e for the `n` tokens whose assignments are order[first ..],
 // which are staged meanwhile.  A warp has PER units of each tile, next to one another; WHOLE: all warps
 // have, and no unit ends inside.  NT products are side by side, of eight tokens each or (FEW, 4 bits) of two.
 template <bool FP4, bool UP, int PER, bool WHOLE, bool FEW, int NT>
-__device__ __forceinline__ void run_tiles(const SmallLayerParams& p, const Lists& s, const Staged& m, int e, int tile0, int tile1, int first, int n) {
+__device__ __forceinline__ void run_tiles(const SmallLayerParams& p, Lists& s, const Staged& m, int e, int tile0, int tile1, int first, int n) {
   constexpr int L = FP4 ? 1 : 2, UB = 64 * L;                    // 16-byte pieces a lane, and bytes, of a row's unit
   constexpr int D = FP4 && (FEW || NT == 1) ? 4 : 2;             // units under way
   constexpr int kTile = UP ? 8 : kRows;                          // rows from a tile to the next
@@ -406,13 +443,15 @@ __device__ __forceinline__ void run_tiles(const SmallLayerParams& p, const Lists
     asm volatile("griddepcontrol.wait;" ::: "memory");           // h is there
     fetch<UP>(p, s, m, first, n, warp, fresh);
   }
+  if (threadIdx.x == 0) s.far = 0;                               // all have read what it was: they have met since
   __syncthreads();                                               // the tokens before, and their parts, are no longer read
-  put<UP>(m, n, warp, fresh);
+  put<UP>(s, m, n, warp, fresh);
   for (int i = warp + kPieces * kWarps; i < n * m.units; i += kPieces * kWarps) {
     fetch<UP>(p, s, m, first, n, i, fresh);
-    put<UP>(m, n, i, fresh);
+    put<UP>(s, m, n, i, fresh);
   }
   __syncthreads();
+  if (s.far) return;                                             // run_far takes the tiles
 
   // The values of the lane's token, and the powers of those whose sums it gets: zeros where there is no token or unit.
   const auto values = [&](int j, int lu) {
@@ -562,24 +601,85 @@ __device__ __forceinline__ void run_tiles(const SmallLayerParams& p, const Lists
     // Those of some tiles are there: they are added in the order of the warps.  The next ones go
     // elsewhere, and here again only behind the next barrier.
     __syncthreads();
-    const int done = min(tile + TPI, tile1) - slot;              // the first of them
-    for (int o0 = warp * kWarp; o0 < slot * n * kRows; o0 += kThreads) {
-      const int o = o0 + lane, at = o / (n * kRows), in = o - at * n * kRows, row = in % kRows;
-      const bool live = at < slot;
-      float sum = 0.f;
-      if (live) {
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) sum += red[(at * kWarps + i) * n * kRows + in];
-      }
-      const int64_t a = live ? s.order[first + in / kRows] : 0;
-      if constexpr (UP) {
-        const float other = __shfl_down_sync(kFull, sum, 8);
-        if (live && row < 8) p.h[a * p.I + (done + at) * 8 + row] = silu(sum) * other;
-      } else {
-        if (live) p.y[a * p.H + (done + at) * kRows + row] = sum;
-      }
-    }
+    add_parts<UP>(p, s, red, min(tile + TPI, tile1) - slot, slot, first, n);
     slot = 0;
+    red = red == m.red ? m.red + m.slots * kWarps * kRows : m.red;
+  }
+}
+
+// What run_tiles leaves: the same tiles and tokens, which are staged.  4 bits: one block at a time, for which the
+// other lanes' codes are 0.  Where run_tiles is right these are its bits (4 bits: those for up to 4 tokens), so that a
+// far token does not change the others of its expert.
+template <bool FP4, bool UP>
+__device__ __noinline__ void run_far(const SmallLayerParams& p, const Lists& s, const Staged m, int per, int e, int tile0, int tile1, int first, int n) {
+  constexpr int L = FP4 ? 1 : 2, UB = 64 * L;                    // as in run_tiles
+  const int K = UP ? p.H : p.I, N = UP ? 2 * p.I : p.H, row_bytes = FP4 ? K / 2 : K, others = UP ? p.I : 8;
+  const SmallWeights& w = UP ? p.w1 : p.w2;
+  const uint32_t* const scales = static_cast<const uint32_t*>(w.scale);
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, g = lane / 4, t = lane % 4;
+  float* red = m.red;
+  for (int tile = tile0; tile < tile1; ++tile) {
+    const int in = tile * (UP ? 8 : kRows);                      // the tile's first row
+    const int64_t row0 = int64_t(e) * N + in + g;
+    float* const part_of = red + warp * n * kRows;
+    for (int j0 = 0; j0 < n; j0 += kTokens) {
+      float acc[2][4] = {};                                      // 4 bits: of the first two blocks and of the others
+      for (int u = warp * per; u < min((warp + 1) * per, m.units); ++u) {
+        const uint8_t* values = s_dyn + (j0 + g < n ? m.x + (j0 + g) * m.pitch + u * (2 * kUnit) + t * (FP4 ? 64 : 32) : 0);
+        const float2 f = *reinterpret_cast<const float2*>(m.power + u * m.columns + j0 + t * 2);
+        uint4 codes[2][L];                                       // of rows g and g + 8
+        uint32_t scale[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int i = 0; i < L; ++i) {
+            const int c = u * UB + i * 64 + t * 16;
+            codes[r][i] = c < row_bytes ? load_weights(w.q + (row0 + r * others) * row_bytes + c) : make_uint4(0u, 0u, 0u, 0u);
+          }
+          scale[r] = load_scale(scales + (FP4 ? int64_t(u) * p.E * N + row0 + r * others
+                                              : (int64_t(e) * ((N + 127) / 128) + (in + r * others) / 128) * m.units + u));
+        }
+        const auto add = [&](float (&to)[4], int b) {
+          if (FP4 && u * kUnit + b * 32 >= K) return;
+          float dot[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              if constexpr (FP4) {
+                fp4_unpack8(t == b ? word(codes[r][0], i) : 0u, a[r]);
+              } else {
+                e4m3_half(word(codes[r][i / 2], i % 2 * 2), a[r][0], a[r][1]);
+                e4m3_half(word(codes[r][i / 2], i % 2 * 2 + 1), a[r][2], a[r][3]);
+              }
+            }
+            const uint4 v = *reinterpret_cast<const uint4*>(values + (FP4 ? i * 16 : i / 2 * 128 + i % 2 * 16));
+            mma_f16(dot, a[0][0], a[1][0], a[0][1], a[1][1], v.x, v.y);
+            mma_f16(dot, a[0][2], a[1][2], a[0][3], a[1][3], v.z, v.w);
+          }
+          const float2 two = FP4 ? two_scales((scale[0] >> b * 8 & 255u) | (scale[1] >> b * 8 & 255u) << 8)
+                                 : make_float2(__uint_as_float(scale[0]), __uint_as_float(scale[1]));
+          to[0] = add_scaled(dot[0], f.x, two.x, to[0]);
+          to[1] = add_scaled(dot[1], f.y, two.x, to[1]);
+          to[2] = add_scaled(dot[2], f.x, two.y, to[2]);
+          to[3] = add_scaled(dot[3], f.y, two.y, to[3]);
+        };
+        if constexpr (FP4) {
+          add(acc[0], 1);
+          add(acc[0], 0);
+          add(acc[1], 3);
+          add(acc[1], 2);
+        } else {
+          add(acc[0], 0);
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (j0 + t * 2 + v % 2 < n) part_of[(j0 + t * 2 + v % 2) * kRows + v / 2 * 8 + g] = acc[0][v] + acc[1][v];
+    }
+    __syncthreads();
+    add_parts<UP>(p, s, red, tile, 1, first, n);                 // the next tile's go elsewhere
     red = red == m.red ? m.red + m.slots * kWarps * kRows : m.red;
   }
 }
@@ -616,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_small_kernel(const __grid_c
         else if (FP4 && n <= kFew) run_tiles<FP4, UP, PER, WHOLE, FP4, FP4 ? 2 : 1>(p, s, m, e, t0, t1, first, n);
         else if (n <= kTokens) run_tiles<FP4, UP, PER, WHOLE, false, 1>(p, s, m, e, t0, t1, first, n);
         else run_tiles<FP4, UP, PER, WHOLE, false, 2>(p, s, m, e, t0, t1, first, n);
+        if (s.far) run_far<FP4, UP>(p, s, m, PER, e, t0, t1, first, n);
       }
     }
   }

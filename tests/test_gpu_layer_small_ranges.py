@@ -1,0 +1,97 @@
+"""The experts of a layer for few tokens, where the sizes of values and of scales are far from one: against float64, by the
+bounds of test_gpu_layer_small.  A token's power of two, a weights' scale and the product of both may each lie anywhere in
+fp32, and beyond it, as long as the sums do not."""
+
+import numpy as np
+import pytest
+import torch
+
+import layer_reference as ref
+from test_gpu_layer_small import check, expected, i32, inputs, stands_for, weights, wide
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mr(native_lib):
+    import moe_expert_routing_router_gb300 as m
+    return m
+
+
+def shifted(w, n, rows=slice(None)):
+    """The weights times 2^n, of some rows (e4m3: whole blocks of 128 rows)."""
+    s = w["scale"].clone()
+    if s.dtype is torch.uint8:
+        s[:, :, rows] = (s[:, :, rows].int() + n).clamp(0, 254).to(torch.uint8)
+    else:
+        b = slice(None) if rows == slice(None) else slice(rows.start // 128, None)
+        s[:, b] = (s[:, b].double() * 2.0 ** n).float()
+    return {**w, "scale": s}
+
+
+def layer(mr, x, idx, gate, w1, w2):
+    got = mr.moe_layer_small(x, idx, gate, w1, w2)
+    want, bound = expected(wide(x), idx.cpu().numpy(), wide(gate), stands_for(w1), stands_for(w2))
+    assert np.isfinite(want).all() and np.median(np.abs(want)) > 2.0 ** -100
+    check(got, want, bound)
+
+
+# Up to 2, 4, 8 tokens of an expert and more take different arithmetic or products side by side; of 4 experts' 8 are taken at a time.
+TOKENS = [(1, 1), (2, 1), (4, 1), (5, 1), (8, 1), (9, 1), (16, 1), (9, 4), (33, 1)]
+
+
+@pytest.mark.parametrize("kind", ["fp4", "e4m3"])
+@pytest.mark.parametrize("T,E", TOKENS)
+@pytest.mark.parametrize("top", [127, 124, 116, 64, -60, -100, -112])
+def test_tokens_of_any_size(mr, kind, T, E, top):
+    """The largest value of x is just below 2^top (or, in whole numbers of 2^-126, bf16's smallest); weights bring the sums back."""
+    H, I = 288, 256
+    x, _, gate = inputs(T, 1, E, H, 5)
+    x = (x.double() * (2.0 ** top * 0.99 / float(x.abs().max()))).to(torch.bfloat16)
+    w1, w2 = shifted(weights(mr, kind, E, 2 * I, H, 1), 8 - top), weights(mr, kind, E, H, I, 2)
+    layer(mr, x, i32(np.zeros((T, 1))), gate, w1, w2)
+
+
+@pytest.mark.parametrize("kind", ["fp4", "e4m3"])
+@pytest.mark.parametrize("T,E", TOKENS)
+@pytest.mark.parametrize("up,down,gates", [(110, -112, 0), (-110, 108, 0), (60, 60, -118), (-60, -60, 120), (-100, 0, 100), (70, -20, -50)])
+def test_activations_of_any_size(mr, kind, T, E, up, down, gates):
+    """The activations are near 2^up, the second product's weights near 2^down, and the gates bring the result back."""
+    H, I = 288, 256
+    x, _, gate = inputs(T, 1, E, H, 6)
+    w1, w2 = shifted(weights(mr, kind, E, 2 * I, H, 1), up, slice(I, 2 * I)), shifted(weights(mr, kind, E, H, I, 2), down)
+    x = (x.float() / x.float().abs().amax(1, keepdim=True)).to(torch.bfloat16)
+    layer(mr, x, i32(np.zeros((T, 1))), (gate.double() * 2.0 ** gates).float(), w1, w2)
+
+
+@pytest.mark.parametrize("kind", ["fp4", "e4m3"])
+@pytest.mark.parametrize("T", [1, 4, 5, 9, 16])
+def test_a_large_value_that_meets_zero(mr, kind, T):
+    """A power times a scale of 2^129, past fp32, whose sum is a number: the value that has the power has the weight 0."""
+    H, I, n = 128, 128, 24 if kind == "e4m3" else 18
+    x = torch.zeros(T, H)
+    x[:, 0], x[:, 40] = 2.0 ** 127, 2.0 ** 92                      # the power is 2^113
+    w = torch.zeros(1, 2 * I, H)
+    w[:, :, 40] = 1.0                                            # a scale of 2^-8 (4 bits: 2^-2), 2^16 once it is shifted
+    make = mr.moe_quantize_fp4 if kind == "fp4" else mr.moe_quantize_weights
+    w1, w2 = make(w.cuda()), make(torch.ones(1, H, I).cuda())
+    w1 = shifted(shifted(w1, n), -100 - n, slice(I, 2 * I))
+    # g = 2^(92 + n), whose sigmoid is 1, and u = 2^-8; the 128 activations are added up
+    got = mr.moe_layer_small(x.to(torch.bfloat16).cuda(), i32(np.zeros((T, 1))), torch.full((T, 1), 2.0 ** -(91 + n), device="cuda"), w1, w2)
+    assert np.array_equal(wide(got), np.ones((T, H)))
+
+
+@pytest.mark.parametrize("kind,T", [("fp4", 4), ("fp4", 2), ("e4m3", 16), ("e4m3", 5)])
+@pytest.mark.parametrize("top", [120, -120])
+def test_a_token_far_from_one_leaves_the_others(mr, kind, T, top):
+    """The other tokens of its expert keep their bits, also where sums of values of very different sizes are rounded at every step."""
+    E, H, I = 1, 1056, 544
+    x, _, gate = inputs(T, 1, E, H, 3)
+    x = (x.float() * torch.exp(3.0 * torch.randn(T, H, generator=torch.Generator().manual_seed(4))).cuda()).to(torch.bfloat16)
+    idx, w1, w2 = i32(np.zeros((T, 1))), weights(mr, kind, E, 2 * I, H, 1), weights(mr, kind, E, H, I, 2)
+    base = mr.moe_layer_small(x, idx, gate, w1, w2)
+    far = x.clone()
+    far[1] = (x[1].double() * 2.0 ** top / float(x[1].abs().max())).to(torch.bfloat16)
+    got = mr.moe_layer_small(far, idx, gate, w1, w2)
+    others = [t for t in range(T) if t != 1]
+    assert torch.equal(got[others], base[others]) and not torch.equal(got[1], base[1])
