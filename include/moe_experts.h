@@ -307,10 +307,10 @@ typedef enum { MOE_WEIGHTS_E4M3 = 0, MOE_WEIGHTS_FP4 = 1 } moe_weight_kind;
  * Sums are fp32, and what they are formed of stays finite where they do, however large or small
  * the values and the scales are.  Of each 128 values of x, those below 2^-28 of the largest lose digits;
  * the activations are rounded to 11 bits, relative to the larger of themselves and 2^-28 of
- * the largest of their 128; 4-bit weights whose scale is below 2^-23 of the largest of the
- * four that 128 columns have may count as zero.  Repeated calls give the same bits.  With
- * e4m3 weights a token's result does not depend on the others; with 4-bit ones its last
- * bits may, on whether more than 4 tokens have its expert.
+ * the largest of their 128.  Repeated calls give the same bits.  With e4m3 weights a token's
+ * result does not depend on the others; with 4-bit ones its last bits may, on how many
+ * tokens have its expert and on its place among them (up to 4 are computed in one way, more in
+ * another, and of many the last few by themselves).
  * H and I are multiples of 16 (of 32 where a matrix of 4 bits has them as its row length)
  * up to MOE_SMALL_WIDTH; x, out and the codes are 16-byte aligned, the scales, idx and
  * gate 4-byte aligned.  work: moe_layer_small_work_size bytes, 16-byte aligned, of any

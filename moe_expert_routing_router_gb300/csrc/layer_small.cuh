@@ -18,7 +18,8 @@
 //            Up to 4 tokens: a token takes four of the eight columns, and each sees one block: the
 //            other lanes' part of its column is zero.  Sums come out by block, and are multiplied by its scale.
 //            More: the codes are multiplied, as fp16, by their scale over the largest of the four,
-//            a power of two (exact down to 2^-23 of it), whose own multiplies the unit's sum.
+//            a power of two (exact down to 2^-23 of it), whose own multiplies the unit's sum.  Tiles with a scale
+//            that is 2^-16 of it or less are left to `run_far`.
 // The tokens' values are staged in shared memory as fp16 with a power of two for each 128, so that
 // their largest is between 2^14 and 2^15: bf16 values are exact down to 2^-28 of it, and the fp32
 // values of h are rounded to 11 bits (three more than bf16 has).  All sums are fp32.
@@ -74,7 +75,7 @@ struct Lists {
   int expert[kMaxA], start[kMaxA + 1];        // of the experts that have tokens: which, and where theirs start
   int work[kMaxA];                            // what stands before them, by tile
   int tile0[kMaxA], tile1[kMaxA];             // their tiles that are this CTA's
-  int far;                                    // a power of the staged tokens is far from one
+  int far, apart;                             // a power of the staged tokens is far from one; four scales are far from one another
   int active, run0, run1;                     // experts that have tokens; the first and last of which this CTA has tiles
 };
 
@@ -443,7 +444,7 @@ __device__ __forceinline__ void run_tiles(const SmallLayerParams& p, Lists& s, c
     asm volatile("griddepcontrol.wait;" ::: "memory");           // h is there
     fetch<UP>(p, s, m, first, n, warp, fresh);
   }
-  if (threadIdx.x == 0) s.far = 0;                               // all have read what it was: they have met since
+  if (threadIdx.x == 0) s.far = s.apart = 0;                               // all have read what it was: they have met since
   __syncthreads();                                               // the tokens before, and their parts, are no longer read
   put<UP>(s, m, n, warp, fresh);
   for (int i = warp + kPieces * kWarps; i < n * m.units; i += kPieces * kWarps) {
@@ -485,6 +486,7 @@ __device__ __forceinline__ void run_tiles(const SmallLayerParams& p, Lists& s, c
   const int slots = min(m.slots / n, kMaxSlots);                 // tiles whose parts are added up together: TPI at least
   int slot = 0;
   float* red = m.red;                                            // of two, in turn
+  uint32_t lacks = 0u;                                           // of all units' scales to the largest of their four
 
   for (int tile = tile0; tile < tile1; tile += TPI) {
     uint32_t top = 0u;
@@ -498,8 +500,13 @@ __device__ __forceinline__ void run_tiles(const SmallLayerParams& p, Lists& s, c
       if constexpr (FP4) {
         if (lu % 2 == 0) {                                       // the lane's own word, of one of two units
           const int u = u0 + lu + (PER > 1 ? t / 2 : 0);
-          if (!WHOLE) scale[ti][lu / 2] &= u + 1 < m.units ? 0xffffffffu : u + 1 == m.units ? last_used : 0u;
-          if (!FEW) top = largest_scale(scale[ti][lu / 2]);
+          const uint32_t used = WHOLE || u + 1 < m.units ? 0xffffffffu : u + 1 == m.units ? last_used : 0u;
+          if (!WHOLE) scale[ti][lu / 2] &= used;
+          if constexpr (!FEW) {
+            top = largest_scale(scale[ti][lu / 2]);
+            if (!WHOLE) scale[ti][lu / 2] &= used;
+            lacks |= scale[ti][lu / 2];
+          }
         }
         const int lane0 = lane / 4 * 4 + (PER > 1 ? lu % 2 * 2 : 0);
         const uint32_t w0 = __shfl_sync(kFull, scale[ti][lu / 2], lane0), w1 = __shfl_sync(kFull, scale[ti][lu / 2], lane0 + 1);
@@ -598,6 +605,7 @@ __device__ __forceinline__ void run_tiles(const SmallLayerParams& p, Lists& s, c
     }
     slot += min(TPI, tile1 - tile);
     if (slot + TPI <= slots && tile + TPI < tile1) continue;
+    if (FP4 && !FEW && (lacks & 0xf0f0f0f0u) != 0u) s.apart = 1; // of 16 or more
     // Those of some tiles are there: they are added in the order of the warps.  The next ones go
     // elsewhere, and here again only behind the next barrier.
     __syncthreads();
@@ -607,7 +615,7 @@ __device__ __forceinline__ void run_tiles(const SmallLayerParams& p, Lists& s, c
   }
 }
 
-// What run_tiles leaves: the same tiles and tokens, which are staged.  4 bits: one block at a time, for which the
+// What run_tiles leaves, or has got wrong: the same tiles and tokens, which are staged.  4 bits: one block at a time, for which the
 // other lanes' codes are 0.  Where run_tiles is right these are its bits (4 bits: those for up to 4 tokens), so that a
 // far token does not change the others of its expert.
 template <bool FP4, bool UP>
@@ -618,6 +626,7 @@ __device__ __noinline__ void run_far(const SmallLayerParams& p, const Lists& s, 
   const uint32_t* const scales = static_cast<const uint32_t*>(w.scale);
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, g = lane / 4, t = lane % 4;
   float* red = m.red;
+  __syncthreads();                                               // run_tiles' parts are no longer read
   for (int tile = tile0; tile < tile1; ++tile) {
     const int in = tile * (UP ? 8 : kRows);                      // the tile's first row
     const int64_t row0 = int64_t(e) * N + in + g;
@@ -716,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_small_kernel(const __grid_c
         else if (FP4 && n <= kFew) run_tiles<FP4, UP, PER, WHOLE, FP4, FP4 ? 2 : 1>(p, s, m, e, t0, t1, first, n);
         else if (n <= kTokens) run_tiles<FP4, UP, PER, WHOLE, false, 1>(p, s, m, e, t0, t1, first, n);
         else run_tiles<FP4, UP, PER, WHOLE, false, 2>(p, s, m, e, t0, t1, first, n);
-        if (s.far) run_far<FP4, UP>(p, s, m, PER, e, t0, t1, first, n);
+        if (s.far || (FP4 && s.apart)) run_far<FP4, UP>(p, s, m, PER, e, t0, t1, first, n);
       }
     }
   }

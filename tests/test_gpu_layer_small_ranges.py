@@ -95,3 +95,62 @@ def test_a_token_far_from_one_leaves_the_others(mr, kind, T, top):
     got = mr.moe_layer_small(far, idx, gate, w1, w2)
     others = [t for t in range(T) if t != 1]
     assert torch.equal(got[others], base[others]) and not torch.equal(got[1], base[1])
+
+
+def uneven(w, steps, seed, tail=0):
+    """4-bit weights with a word's exponents `steps` apart, in an order of each word's own, the largest as they were; `tail`
+    more behind the last column, where any byte may be."""
+    s = w["scale"]
+    g = torch.Generator().manual_seed(seed)
+    order = torch.argsort(torch.rand(*s.shape, generator=g), dim=3).cuda()
+    s = (s.int() - torch.tensor(steps, device="cuda")[order]).clamp(min=0)
+    blocks = w["q"].shape[2] // 16
+    if blocks % 4 and tail:
+        s[-1, :, :, blocks % 4:] = tail
+    return {"q": w["q"], "scale": s.to(torch.uint8)}
+
+
+@pytest.mark.parametrize("T,E", TOKENS)
+@pytest.mark.parametrize("steps", [(0, 7, 15, 23), (0, 1, 22, 24), (0, 24, 30, 31), (0, 33, 50, 90), (0, 0, 0, 25)])
+def test_scales_far_apart_in_a_word(mr, T, E, steps):
+    """Four exponents that differ by up to 23 and by more, also where all that a token has in the largest block is zero."""
+    H, I = 288, 160
+    x, _, gate = inputs(T, 1, E, H, 7)
+    w1, w2 = (uneven(weights(mr, "fp4", E, n, k, i), steps, i, 200) for n, k, i in ((2 * I, H, 1), (H, I, 2)))
+    idx = i32(np.zeros((T, 1)))
+    layer(mr, x, idx, gate, w1, w2)
+    # of every word of the gates' and the others' first 16 rows, the last block is the largest by far: tokens have zeros there
+    s = w1["scale"].clone()
+    s[:, :, :, 3] = 150
+    s[:, :, :, 0] = 150 - steps[3]
+    x = x.clone().view(T, H)
+    x[:, 96:128] = 0
+    x[:, 224:256] = 0
+    layer(mr, x, idx, gate, {"q": w1["q"], "scale": s}, w2)
+
+
+@pytest.mark.parametrize("T,E", TOKENS)
+def test_a_block_of_zeros_beside_small_ones(mr, T, E):
+    """The scale of a block of zeros is 1, far above those of weights near 2^-40."""
+    H, I = 288, 160
+    x, _, gate = inputs(T, 1, E, H, 8)
+    w = torch.randn(E, 2 * I, H, generator=torch.Generator().manual_seed(1))
+    w[:, I:] *= 2.0 ** -40
+    w[:, :, 32:64] = 0
+    w[:, :, 256:] = 0
+    w1, w2 = mr.moe_quantize_fp4((w / H ** 0.5).cuda()), shifted(weights(mr, "fp4", E, H, I, 2), 40)
+    layer(mr, x, i32(np.zeros((T, 1))), gate, w1, w2)
+
+
+@pytest.mark.parametrize("steps", [(0, 3, 7, 9), (0, 33, 50, 90)])
+def test_equal_tokens_of_one_expert(mr, steps):
+    """Nine, of which eight are taken at a time and the last one alone: their results differ by roundings."""
+    E, H, I, T = 4, 288, 160, 9
+    x, _, gate = inputs(1, 1, E, H, 9)
+    x, gate = x.expand(T, H).contiguous(), gate.expand(T, 1).contiguous()
+    w1, w2 = (uneven(weights(mr, "fp4", E, n, k, i), steps, i) for n, k, i in ((2 * I, H, 1), (H, I, 2)))
+    x[:, :32] = 0
+    got = mr.moe_layer_small(x, i32(np.zeros((T, 1))), gate, w1, w2)
+    want, bound = expected(wide(x), np.zeros((T, 1), dtype=int), wide(gate), stands_for(w1), stands_for(w2))
+    check(got, want, bound)
+    assert all(torch.equal(got[0], got[t]) for t in range(1, 8))
