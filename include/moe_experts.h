@@ -276,13 +276,15 @@ typedef enum { MOE_GLU_PLAIN = 0, MOE_GLU_E4M3 = 1, MOE_GLU_FP4 = 2 } moe_glu_fo
  *   MOE_GLU_PLAIN: out [M,I] in h's type (scale is NULL)
  *   MOE_GLU_E4M3:  out [M,I] and scale [ceil(I/128), M] fp32, as moe_quantize_rows has them
  *   MOE_GLU_FP4:   out [M,I/2] and scale [ceil(I/128), M, 4], as moe_quantize_fp4 has them
- * (the blocks' scales are those of the fp32 values).  g = -infinity gives a NaN.
+ * (the blocks' scales are those of the fp32 values).  g = -infinity gives a NaN.  A sigmoid below
+ * 2^-126 has fewer digits than others, and one below 2^-149 is 0.
  * I is a multiple of 16 (MOE_GLU_FP4: of 32) up to MOE_MAX_WIDTH; h and out are 16-byte
  * aligned, scale is 4-byte aligned. */
 MOE_API moe_status moe_expert_glu(const void* h, moe_dtype dt, int64_t M, int32_t I, moe_glu_form form, void* out,
                                   void* scale, moe_stream_t stream);
 
 /* Its gradient, with s = sigmoid(g): dh[r,i] = dy u s (1 + g (1 - s)), dh[r,I+i] = dy g s.
+ * A result that fp32 holds is finite, though dy u may not be; an infinite g gives a NaN.
  * dy [M,I] and dh [M,2I] have h's type and are 16-byte aligned. */
 MOE_API moe_status moe_expert_glu_bwd(const void* h, const void* dy, moe_dtype dt, int64_t M, int32_t I, void* dh,
                                       moe_stream_t stream);

@@ -16,6 +16,8 @@
 
 #include <cuda_bf16.h>
 
+#include <cfloat>
+
 namespace moe {
 namespace {
 
@@ -102,7 +104,8 @@ __global__ void __launch_bounds__(kThreads) glu_bwd_kernel(const GluBwdParams p)
   for (int j = 0; j < N; ++j) {
     const float2 s = sigmoids<BF16>(g.get(j));
     du[j] = d.get(j) * (g.get(j) * s.x);
-    dg[j] = d.get(j) * u.get(j) * (s.x * fmaf(g.get(j), s.y, 1.f));
+    const float slope = s.x * fmaf(g.get(j), s.y, 1.f), both = d.get(j) * u.get(j);   // the slope is below 1.1, and may be small
+    dg[j] = fabsf(both) <= FLT_MAX ? both * slope : d.get(j) * (u.get(j) * slope);
   }
   store<BF16>(p.dh, r * 2 * p.I + c, dg);
   store<BF16>(p.dh, r * 2 * p.I + p.I + c, du);
