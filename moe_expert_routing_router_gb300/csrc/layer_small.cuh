@@ -780,14 +780,19 @@ cudaError_t launch_per(const SmallLayerParams& p, int sms, cudaStream_t stream) 
   return cudaLaunchKernelEx(&cfg, kernel, p, cap, columns, pitch, slots);
 }
 
-// PER by the length of the contraction.
+// PER by the length of the contraction, and whether it fills the warps' units: then no address or scale is checked against
+// its end.  (Without that form: 8 experts of 16384 and 4096, 16 tokens, 8 bits 599 us instead of 449, 4 bits 409 and 400; 64 of
+// 4096 and 2048, 64 tokens, 8 bits 318 and 311, one token, 4 bits 30.6 and 29.8.)
+template <bool FP4, bool UP, int PER>
+cudaError_t launch_units(const SmallLayerParams& p, int sms, cudaStream_t stream) {
+  return (UP ? p.H : p.I) == PER * kWarps * kUnit ? launch_per<FP4, UP, PER, true>(p, sms, stream) : launch_per<FP4, UP, PER, false>(p, sms, stream);
+}
 template <bool FP4, bool UP>
 cudaError_t launch(const SmallLayerParams& p, int sms, cudaStream_t stream) {
-  const int K = UP ? p.H : p.I, units = (K + kUnit - 1) / kUnit, per = (units + kWarps - 1) / kWarps;
-  const bool whole = K % (kUnit * kWarps) == 0;
-  if (per <= 1) return whole ? launch_per<FP4, UP, 1, true>(p, sms, stream) : launch_per<FP4, UP, 1, false>(p, sms, stream);
-  if (per <= 2) return whole ? launch_per<FP4, UP, 2, true>(p, sms, stream) : launch_per<FP4, UP, 2, false>(p, sms, stream);
-  return per <= 4 ? launch_per<FP4, UP, 4, false>(p, sms, stream) : launch_per<FP4, UP, 8, false>(p, sms, stream);
+  const int units = ((UP ? p.H : p.I) + kUnit - 1) / kUnit, per = (units + kWarps - 1) / kWarps;
+  if (per <= 1) return launch_units<FP4, UP, 1>(p, sms, stream);
+  if (per <= 2) return launch_units<FP4, UP, 2>(p, sms, stream);
+  return per <= 4 ? launch_units<FP4, UP, 4>(p, sms, stream) : launch_units<FP4, UP, 8>(p, sms, stream);
 }
 
 }  // namespace

@@ -154,3 +154,13 @@ def test_equal_tokens_of_one_expert(mr, steps):
     want, bound = expected(wide(x), np.zeros((T, 1), dtype=int), wide(gate), stands_for(w1), stands_for(w2))
     check(got, want, bound)
     assert all(torch.equal(got[0], got[t]) for t in range(1, 8))
+
+
+@pytest.mark.parametrize("kind", ["fp4", "e4m3"])
+@pytest.mark.parametrize("T", [1, 4, 5, 9])
+@pytest.mark.parametrize("length", [2016, 2048, 2080, 4096, 4064, 6144, 8160, 8192, 8224, 12288, 16352, 16384])
+def test_contractions_that_fill_the_warps_and_others(mr, kind, T, length):
+    """Lengths of both products at, just below and above those that all warps share evenly."""
+    for H, I in ((length, 32), (32, length)):
+        x, _, gate = inputs(T, 1, 1, H, T + length)
+        layer(mr, x, i32(np.zeros((T, 1))), gate, weights(mr, kind, 1, 2 * I, H, 1), weights(mr, kind, 1, H, I, 2))
