@@ -164,3 +164,114 @@ def test_contractions_that_fill_the_warps_and_others(mr, kind, T, length):
     for H, I in ((length, 32), (32, length)):
         x, _, gate = inputs(T, 1, 1, H, T + length)
         layer(mr, x, i32(np.zeros((T, 1))), gate, weights(mr, kind, 1, 2 * I, H, 1), weights(mr, kind, 1, H, I, 2))
+
+
+@pytest.mark.parametrize("T,E", TOKENS)
+def test_bytes_behind_the_last_column(mr, T, E):
+    """Scale bytes that stand for no column may be anything, however many tokens an expert has."""
+    H, I = 288, 160
+    x, _, gate = inputs(T, 1, E, H, 10)
+    idx, w1, w2 = i32(np.zeros((T, 1))), weights(mr, "fp4", E, 2 * I, H, 1), weights(mr, "fp4", E, H, I, 2)
+    base = mr.moe_layer_small(x, idx, gate, w1, w2)
+    for byte in (255, 254, 0):
+        w1["scale"][2, :, :, 1:] = byte
+        w2["scale"][1, :, :, 1:] = byte
+        assert torch.equal(mr.moe_layer_small(x, idx, gate, w1, w2), base)
+
+
+@pytest.mark.parametrize("kind", ["fp4", "e4m3"])
+@pytest.mark.parametrize("T,E", TOKENS)
+def test_not_a_number(mr, kind, T, E):
+    """A NaN scale, of a row or of a block of weights, is its results', and an infinite or NaN value its token's."""
+    H, I = 288, 160
+    x, _, gate = inputs(T, 1, E, H, 11)
+    idx, w1, w2 = i32(np.zeros((T, 1))), weights(mr, kind, E, 2 * I, H, 1), weights(mr, kind, E, H, I, 2)
+    base = mr.moe_layer_small(x, idx, gate, w1, w2)
+    s = w2["scale"].clone()
+    if kind == "fp4":
+        s[1, 0, 7, 0] = 255
+    else:
+        s[0, 1, 1] = float("nan")
+    rows = torch.zeros(H, dtype=torch.bool, device="cuda")
+    rows[slice(7, 8) if kind == "fp4" else slice(128, 256)] = True
+    got = mr.moe_layer_small(x, idx, gate, w1, {**w2, "scale": s})
+    assert bool(got[:, rows].isnan().all())
+    if kind == "e4m3" or T <= 4:
+        assert torch.equal(got[:, ~rows], base[:, ~rows])
+    else:                                                        # the tiles of that row are computed by blocks: other roundings
+        off = (got[:, ~rows].double() - base[:, ~rows].double()).norm() / base.double().norm()
+        assert float(off) <= 2.0 ** -8 and bool(got[:, ~rows].isfinite().all())
+    bad = x.clone()
+    bad[0, 3] = float("inf")
+    bad[-1, 287] = float("nan")
+    got = mr.moe_layer_small(bad, idx, gate, w1, w2)
+    others = list(range(1, T - 1))
+    assert torch.equal(got[others], base[others]) and not bool(got[[0, T - 1]].isfinite().any())
+
+
+def exact_weights(w, e):
+    """Expert e's weights in float64, on the GPU, from their codes and scales."""
+    q, scale = w["q"][e], w["scale"]
+    if q.dtype is torch.uint8:
+        code = torch.stack([q & 15, q >> 4], 2).flatten(1).long()
+        sizes = torch.tensor(ref.FP4, dtype=torch.float64, device="cuda")
+        v = torch.where(code >= 8, -sizes[code % 8], sizes[code % 8])
+        n = scale[:, e].transpose(0, 1).flatten(1)[:, :code.shape[1] // 32].double()
+        return v * torch.exp2(n - 127).repeat_interleave(32, 1)
+    s = scale[e].double().repeat_interleave(128, 0)[:q.shape[0]].repeat_interleave(128, 1)[:, :q.shape[1]]
+    return q.double() * s
+
+
+def check_on_gpu(got, x, idx, gate, w1, w2):
+    """test_gpu_layer_small's comparison, for sizes that numpy would take long for."""
+    (T, H), k, I = x.shape, idx.shape[1], w1["q"].shape[1] // 2
+    out, bound = (torch.zeros(T, H, dtype=torch.float64, device="cuda") for _ in range(2))
+    n1, n2 = (110 + 3 * H / 2048) * ref.U32, (110 + 3 * I / 2048 + 2 * k) * ref.U32
+    for e in range(w1["q"].shape[0]):
+        t, j = torch.nonzero(idx == e, as_tuple=True)
+        if len(t) == 0:
+            continue
+        w, v = exact_weights(w1, e), x[t].double()
+        h, size = v @ w.t(), v.abs() @ w.abs().t()
+        g, u, dg, du = h[:, :I], h[:, I:], n1 * size[:, :I], n1 * size[:, I:]
+        s = torch.sigmoid(g)
+        act = g * s * u
+        block = torch.nn.functional.pad(act.abs(), (0, -I % 128)).view(len(t), -1, 128).amax(2).repeat_interleave(128, 1)[:, :I]
+        off = 1.1 * dg * u.abs() + (g * s).abs() * du + 1.1 * dg * du + act.abs() * ((g.abs() + 8) * ref.U32)
+        off += (act.abs() + off) * 2.0 ** -11 + block * 2.0 ** -39
+        w, a = exact_weights(w2, e), gate[t, j].double()[:, None]
+        out.index_add_(0, t, a * (act @ w.t()))
+        bound.index_add_(0, t, a.abs() * ((off + n2 * (act.abs() + off)) @ w.abs().t()))
+    bound = bound + (out.abs() + bound) * ref.U16 + 2.0 ** -134
+    off = (got.double() - out).abs()
+    assert bool((off <= bound).all()), float((off / bound).max())
+    assert float((got.double() - out).norm()) <= 1.25 * ref.U16 * float(out.norm())
+
+
+def made_weights(kind, E, N, K, seed):
+    """Quantised weights near 1 / sqrt(K), made on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    top = -int(np.log2(K) / 2)
+    if kind == "fp4":
+        return {"q": torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, generator=g, device="cuda"),
+                "scale": torch.randint(125 + top, 128 + top, (-(-K // 128), E, N, 4), dtype=torch.uint8, generator=g, device="cuda")}
+    q = torch.empty(E, N, K, dtype=torch.float8_e4m3fn, device="cuda")
+    for e in range(E):
+        q[e] = (64 * torch.randn(N, K, generator=g, device="cuda")).clamp(-448, 448).to(torch.float8_e4m3fn)
+    n = torch.randint(-8, -5, (E, -(-N // 128), -(-K // 128)), generator=g, device="cuda") + top
+    return {"q": q, "scale": torch.exp2(n.float())}
+
+
+@pytest.mark.parametrize("kind", ["fp4", "e4m3"])
+@pytest.mark.parametrize("T,k,E,H,I", [(64, 8, 64, 4096, 2048), (64, 2, 3, 128, 16384), (64, 2, 4, 16384, 128), (37, 3, 5, 160, 8224), (16, 8, 64, 2048, 768)])
+def test_many_tiles_of_experts_with_many_tokens(mr, kind, T, k, E, H, I):
+    """More tiles of an expert on an SM than are taken again at a time for more tokens than are staged; once with a token
+    far from one among them."""
+    x, idx, gate = inputs(T, k, E, H, 12)
+    x = (x.float() / x.float().abs().amax(1, keepdim=True) * 4).to(torch.bfloat16)
+    w1, w2 = made_weights(kind, E, 2 * I, H, 1), made_weights(kind, E, H, I, 2)
+    got = mr.moe_layer_small(x, idx, gate, w1, w2)
+    check_on_gpu(got, x, idx, gate, w1, w2)
+    far = x.clone()
+    far[5] = (far[5].double() * 2.0 ** -115).to(torch.bfloat16)
+    check_on_gpu(mr.moe_layer_small(far, idx, gate, w1, w2), far, idx, gate, w1, w2)
