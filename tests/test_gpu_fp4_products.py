@@ -287,3 +287,27 @@ def test_refusals(mr):
         mr.moe_expert_matmul_fp4(q, s, wq, ws)                    # two experts without offsets
     with pytest.raises(mr._native.MoeRouterError):
         mr.moe_expert_matmul_fp4(q, s, wq[:, :24].contiguous(), ws[:, :, :24].contiguous(), o)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("offsets,kept", [([0, 900, 64, 64], [9, 9, 9]), ([-5, 30, 20, 1 << 30], None), ([64, 64, 64, 64], None), ([0, 10, 20, 30], [-3, 1 << 30, 5]),
+                                          ([40, 64, 1 << 30, 1 << 30], [1 << 30, 7, 7]), ([-100, -5, 3, 50], None)])
+def test_positions_outside_the_arrays_write_nothing_beside_them(mr, offsets, kept, dtype):
+    """In front of the result and behind it, and in rows of no expert, what was there stays; the other rows are right."""
+    M, K, N, E, margin = 64, 128, 64, 3, 300
+    ops = operands(M, K, E, N, 2)
+    inside = np.clip(offsets, 0, M)
+    ends = np.maximum(inside[1:], inside[:-1])
+    number = ends - inside[:-1] if kept is None else np.minimum(ends - inside[:-1], np.maximum(kept, 0))
+    rows = [(int(a), int(n)) for a, n in zip(inside[:-1], number)]
+    owners = np.zeros(M, dtype=int)
+    for at, n in rows:
+        owners[at:at + n] += 1
+    whole = torch.full((M + 2 * margin, N), 7.0, dtype=dtype, device="cuda")
+    before = whole[margin:margin + M].clone()
+    got = mr.moe_expert_matmul_fp4(*ops, i32(offsets), None if kept is None else i32(kept), out=whole[margin:margin + M])
+    torch.cuda.synchronize()
+    assert bool((whole[:margin] == 7.0).all()) and bool((whole[margin + M:] == 7.0).all())
+    once = owners < 2                                            # a row of two experts has the result of either
+    want, size = expected(*ops, rows)
+    check(got[torch.from_numpy(once).cuda()], want[once], size[once], K, before[torch.from_numpy(once).cuda()])
