@@ -279,7 +279,7 @@ typedef enum { MOE_GLU_PLAIN = 0, MOE_GLU_E4M3 = 1, MOE_GLU_FP4 = 2 } moe_glu_fo
  * (the blocks' scales are those of the fp32 values).  g = -infinity gives a NaN.  A sigmoid below
  * 2^-126 has fewer digits than others, and one below 2^-149 is 0.
  * I is a multiple of 16 (MOE_GLU_FP4: of 32) up to MOE_MAX_WIDTH; h and out are 16-byte
- * aligned, scale is 4-byte aligned. */
+ * aligned, scale is 4-byte aligned.  All M rows are read and written, those of dropped assignments too. */
 MOE_API moe_status moe_expert_glu(const void* h, moe_dtype dt, int64_t M, int32_t I, moe_glu_form form, void* out,
                                   void* scale, moe_stream_t stream);
 
@@ -309,14 +309,16 @@ typedef enum { MOE_WEIGHTS_E4M3 = 0, MOE_WEIGHTS_FP4 = 1 } moe_weight_kind;
  * Sums are fp32, and what they are formed of stays finite where they do, however large or small
  * the values and the scales are.  Of each 128 values of x, those below 2^-28 of the largest lose digits;
  * the activations are rounded to 11 bits, relative to the larger of themselves and 2^-28 of
- * the largest of their 128.  Repeated calls give the same bits.  With e4m3 weights a token's
+ * the largest of their 128, three more than a result has.  Repeated calls give the same bits.  With e4m3 weights a token's
  * result does not depend on the others; with 4-bit ones its last bits may, on how many
  * tokens have its expert and on its place among them (up to 4 are computed in one way, more in
  * another, and of many the last few by themselves).
  * H and I are multiples of 16 (of 32 where a matrix of 4 bits has them as its row length)
  * up to MOE_SMALL_WIDTH; x, out and the codes are 16-byte aligned, the scales, idx and
  * gate 4-byte aligned.  work: moe_layer_small_work_size bytes, 16-byte aligned, of any
- * content; calls that may run at the same time each take their own. */
+ * content; calls that may run at the same time each take their own.
+ * With 4-bit weights and from some 16 tokens on the chain of moe_quantize_fp4, moe_expert_matmul_fp4 and
+ * moe_expert_glu takes less time, on tokens and activations that are rounded to 4 bits. */
 MOE_API size_t moe_layer_small_work_size(int64_t T, int32_t H, int32_t I, int32_t k);
 MOE_API moe_status moe_layer_small(const void* x, int64_t T, int32_t H, int32_t I, int32_t E, int32_t k,
                                    const int32_t* idx, const float* gate,

@@ -16,17 +16,18 @@
 // tcgen05.cp copies 32 to all quarters in front of the products that read them.
 //   b: the words of rows 4 r .. 4 r + 3 make a piece as they lie, so that tensor copies bring
 //      them, and row 4 r + j of the codes is brought to row 32 j + r; the epilogue reads the
-//      sum's columns accordingly.  (With all scales as a's: 345 us instead of 215, of 64 experts
-//      of 2048 by 4096 and 1024 rows each.)
+//      sum's columns accordingly.  (With all scales as a's: 345 us instead of 217, of 64 experts
+//      of 2048 by 4096 and 1024 rows each, when that was changed.)
 //   a: its rows start anywhere, so a warp copies word by word.
 // A stage's scales have columns of their own in tensor memory, so that their reuse is
 // ordered by the stage's.
 //
 // What bounds it: with few rows of an expert the weights' reading, 50 us for 64 experts of 2048 by
-// 4096 (285 MB, 5.7 TB/s; 8 rows each); with many the way from L2 to an SM, which takes
-// 52 KB a stage at 55 to 64 bytes a cycle, while its products would take 400 cycles: 205 us and
-// 5.0 PFLOP/s with 1024 rows each.  (CTA pairs, which bring 35 KB a stage, were no more than 6 percent
-// faster there, 590 cycles a stage however full the ring was, and slower with 256 rows each.)
+// 4096 (285 MB, 5.7 TB/s; 8 rows each).  With many, 1024 each, 208 us and 5.3 PFLOP/s: no limit is shown to be met.
+// A stage's products would take 390 cycles by the nominal rate, and the tensor pipe is busy half of the time; the stages of all
+// SMs bring 16 TB/s from L2.  Over seconds such calls meet the power limit (1363 W): 223 us, 910 cycles a stage at 1762 MHz.
+// Narrow tiles do not (327 us, 784 cycles a stage at 2070 MHz and 1290 W).  CTA pairs, which bring 35 KB a stage instead of 52,
+// were no more than 6 percent faster with 1024 rows each, and slower with 256; their clock was not recorded.
 //
 // Every wait is bounded: when one runs out, the CTA records the pipeline's error
 // bit, drains its copies and returns.
@@ -504,9 +505,10 @@ cudaError_t launch(const MatmulFp4Params& p, int sms, const char** error, cudaSt
 
 cudaError_t launch_expert_matmul_fp4(const MatmulFp4Params& p, int sms, const char** error, cudaStream_t stream) {
   // Tiles of 256 columns take 1.3 to 1.7 times as long as those of 128, if their products bound them, so
-  // that the rounds of tiles decide: 1024 rows by 64 experts of 2048 by 4096, 349 us in 58 rounds of
-  // narrow ones and 220 in 29 of wide ones; 512 rows by 8 of 1040 by 1440, 19.0 in 3 and 21.0 in 2.  With fewer
-  // rows the weights' reading does, which narrow tiles share out more evenly (64 rows: 66.7 and 68.5 us).
+  // that the rounds of tiles decide: 1024 rows by 64 experts of 2048 by 4096, 351 us in 58 rounds of
+  // narrow ones and 218 in 29 of wide ones; 512 rows by 8 of 1040 by 1440, 18.9 in 3 and 21.0 in 2.  With fewer
+  // rows the weights' reading does, which narrow tiles share out more evenly (64 rows: 66.8 and 68.7 us).  All
+  // of one call alone, behind a flush of L2, experts' rows drawn at random around these.
   const auto rounds = [&](int cols) { return ((2 * p.M / kBM + p.E) * ((p.C + cols - 1) / cols) / 2 + sms - 1) / sms; };
   const bool narrow = p.M <= int64_t(p.E) * 100 || rounds(128) * 5 <= rounds(256) * 8;
   if (p.out_bf16) return narrow ? launch<128, true>(p, sms, error, stream) : launch<256, true>(p, sms, error, stream);

@@ -29,9 +29,9 @@
 //
 // What is under way waits in L1, so that shared memory is kept small: eight tokens of an expert are
 // staged at a time, or up to 16, and more take the same tiles again, some at a time, from L2.
-// (16 tokens, 8 of 64 experts of 4096 and 2048, 8 bits: 231 us with 144 KB of shared memory, 240 with 182 KB, 390 with 230 KB.)
-// Copies to shared memory were slower: of 16 bytes a lane 320 us, tensor copies of 8 x 128 bytes by each warp 298, of 8 x 2048
-// by a producer warp 268, bulk copies of rows 309.
+// (64 tokens, 8 of 64 experts of 4096 and 2048, 8 bits: 309 us with 144 KB of shared memory, 351 with 182 KB.)
+// Copies to shared memory were slower, in an earlier form that took 231 us for 16 tokens: of 16 bytes a lane 320, tensor copies
+// of 8 x 128 bytes by each warp 298, of 8 x 2048 by a producer warp 268, bulk copies of rows 309.
 //
 // The first kernel's tiles are 8 rows of the gate and the 8 rows of the other half that go
 // with them.  The second one's sums go to memory by assignment, and a third, small kernel adds
@@ -39,9 +39,14 @@
 // the one before it ends (programmatic dependent launch); the second has its first weights under way
 // when the first one is done.
 //
-// 8 of 64 experts of 4096 and 2048, a call in a graph: 4 bits, 1 token 30 us, 16 tokens 162 us (5 TB/s of weights,
-// 45 percent of the issue slots: unpacking beside the loads); 8 bits, 16 tokens 218 us (6.4 TB/s), 64 tokens 304 us.
-// About 10 us of each are the launches, the lists and the sums over experts.
+// 8 of 64 experts of 4096 and 2048, a call in a graph, with the share of the measured copy rate at which weights are read:
+//            1 token        4             16             32             64 tokens
+//   4 bits   30 us, 53 %    73 us, 68 %   165 us, 67 %   226 us, 56 %   303 us, 42 %
+//   8 bits   42 us, 73 %                  217 us, 96 %                  309 us, 78 %
+// About 10 us of each are the launches, the lists and the sums over experts.  4 bits: unpacking and scaling beside the loads, for
+// every time that a tile is taken; from 12 tokens of an expert on that costs more than 8-bit weights' reading.  Other sizes:
+// 16 tokens, 8 of 128 experts of 2048 and 768: 73 us (4 bits) and 90 (8), a floor of 29 and 55, since 10 of 16 warps have no unit of
+// the second contraction; 8 of 128 of 7168 and 2048, 4 bits: 363 us, a floor of 273.
 #pragma once
 
 #include "block_values.cuh"
@@ -81,9 +86,9 @@ struct Lists {
 
 // What a tile of an expert with n tokens takes, in eighths of one that its weights' reading
 // bounds: `cap` tokens are taken at a time.  (Of 64 experts of 4096 and 2048 with 1, 4, 8, 12 and 16 tokens
-// each one takes, 13 at a time, 2.7, 3.6, 3.7, 5.6 and 9.6 us at 4 bits, 4.1, 4.2, 4.5, 5.3 and 9.1 at 8.  Where
+// each one takes, 13 or 14 at a time, 2.7, 3.5, 3.6, 5.6 and 9.8 us at 4 bits, 4.0, 4.1, 4.4, 5.3 and 9.1 at 8.  Where
 // experts' tokens differ, of 64 with 8 of 64 experts each, 8 more for a time over the tiles that is not the last
-// share the work best: 304 us, with 2 more 336.)
+// share the work best: 304 us, with 2 more 336, in the form of that time.)
 template <bool FP4>
 __device__ __forceinline__ int tile_cost(int n, int cap) {
   const auto pass = [](int tokens) {
@@ -331,6 +336,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
+// Within |g| + 8 roundings of 2^-24, of a value that is rounded to 11 bits.
 __device__ __forceinline__ float silu(float g) {
   const float t = __expf(-fabsf(g)), r = 1.f / (1.f + t);
   return g * (g >= 0.f ? r : t * r);
@@ -740,8 +746,8 @@ cudaError_t launch_per(const SmallLayerParams& p, int sms, cudaStream_t stream) 
   const int K = UP ? p.H : p.I, units = (K + kUnit - 1) / kUnit;
   const int pitch = units * kUnit * 2 + 16;                      // rows' same pieces lie in different banks
   // Tokens of an expert that are staged at once, and parts of tiles: of a round's tiles at least, of eight at most.
-  // More of them, which leave L1 less, where experts have more than four on average.  (64 experts of 4096 and 2048, 8 bits:
-  // 8 a token: 64 tokens 442 us with 8 at once, 387 with 12; 16 tokens 231 and 237.)
+  // More of them, which leave L1 less, where experts have more than four on average.  (8 of 64 experts of 4096 and 2048: 64 tokens,
+  // 8 bits 398 us with 8 at once, 309 with 14, 4 bits 351 and 303; 16 tokens, 8 bits 217 and 222, 4 bits 165 and 165.)
   int cap = p.T * p.k > 4 * p.E ? 2 * kTokens : kTokens, columns = 0, slots = 0;
   if (cap > p.T) cap = p.T;
   size_t smem = 0;
