@@ -623,7 +623,8 @@ __device__ __forceinline__ void run_tiles(const SmallLayerParams& p, Lists& s, c
 
 // What run_tiles leaves, or has got wrong: the same tiles and tokens, which are staged.  4 bits: one block at a time, for which the
 // other lanes' codes are 0.  Where run_tiles is right these are its bits (4 bits: those for up to 4 tokens), so that a
-// far token does not change the others of its expert.
+// far token does not change the others of its expert.  Nothing is under way ahead of its use: 8 of 64 experts of 4096 and 2048,
+// 16 tokens that are all far, 4 bits 546 us (174 otherwise), 8 bits 343 (229), calls outside a graph.
 template <bool FP4, bool UP>
 __device__ __noinline__ void run_far(const SmallLayerParams& p, const Lists& s, const Staged m, int per, int e, int tile0, int tile1, int first, int n) {
   constexpr int L = FP4 ? 1 : 2, UB = 64 * L;                    // as in run_tiles
