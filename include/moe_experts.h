@@ -306,13 +306,14 @@ typedef enum { MOE_WEIGHTS_E4M3 = 0, MOE_WEIGHTS_FP4 = 1 } moe_weight_kind;
  *   w1 [E,2I,H]: the gates' I rows, then the other I; w2 [E,H,I]; each either
  *     MOE_WEIGHTS_E4M3: q and scale as moe_quantize_weights gives them, or
  *     MOE_WEIGHTS_FP4:  q and scale as moe_quantize_fp4 gives them
- * Sums are fp32, and what they are formed of stays finite where they do, however large or small
+ * Sums are fp32, and are finite wherever fp32 holds them and their terms, however large or small
  * the values and the scales are.  Of each 128 values of x, those below 2^-28 of the largest lose digits;
  * the activations are rounded to 11 bits, relative to the larger of themselves and 2^-28 of
  * the largest of their 128, three more than a result has.  Repeated calls give the same bits.  With e4m3 weights a token's
  * result does not depend on the others; with 4-bit ones its last bits may, on how many
  * tokens have its expert and on its place among them (up to 4 are computed in one way, more in
- * another, and of many the last few by themselves).
+ * another, and of many the last few by themselves; beside one with a block of 128 values that are
+ * all below 2^-78, or reach 2^111, more are computed as up to 4 are).
  * H and I are multiples of 16 (of 32 where a matrix of 4 bits has them as its row length)
  * up to MOE_SMALL_WIDTH; x, out and the codes are 16-byte aligned, the scales, idx and
  * gate 4-byte aligned.  work: moe_layer_small_work_size bytes, 16-byte aligned, of any
